@@ -30,12 +30,21 @@ __all__ = [
     "fp8bs_diag_gemm_unpromoted", "diag_gemm_unpromoted",
     "quantize_act", "quantize_weight", "gemm", "grouped_gemm", "requant_1x128_to_128x1", "swiglu_quantize",
     "OUT_F32", "OUT_BF16", "SCALE_BLOCK128x128", "SCALE_ROW1x128", "SCALE_ABSMAX", "SCALE_POW2",
+    "fp8bs_fp4_scale_bytes", "fp8bs_quantize_fp4", "fp8bs_swiglu_quantize_fp4", "fp8bs_dequantize_fp4",
+    "fp8bs_gemm_fp4", "fp8bs_grouped_gemm_fp4", "fp8bs_moe_route", "fp8bs_moe_route_backward", "fp8bs_moe_layout",
+    "fp4_scale_bytes", "quantize_fp4", "swiglu_quantize_fp4", "dequantize_fp4", "gemm_fp4", "grouped_gemm_fp4",
+    "moe_route", "moe_route_backward", "moe_layout", "moe_layout_rows", "moe_route_workspace_bytes",
+    "moe_layout_workspace_bytes", "FP4_E4M3X16", "FP4_UE8M0X32", "IN_F32", "IN_BF16", "SCORE_SOFTMAX",
+    "SCORE_SIGMOID",
 ]
 
 OUT_F32, OUT_BF16 = 0, 1
 SCALES_KB_MAJOR, SCALES_ROW_MAJOR = 0, 1
 SCALE_BLOCK128x128, SCALE_ROW1x128 = 0, 1
 SCALE_ABSMAX, SCALE_POW2 = 0, 1
+FP4_E4M3X16, FP4_UE8M0X32 = 0, 1
+IN_F32, IN_BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 STATUS_NAMES = {0: "FP8BS_OK", 1: "FP8BS_ERR_INVALID_ARG", 2: "FP8BS_ERR_SHAPE", 3: "FP8BS_ERR_ALIGNMENT",
                 4: "FP8BS_ERR_UNSUPPORTED_ARCH", 5: "FP8BS_ERR_CUDA", 6: "FP8BS_ERR_TIMEOUT",
@@ -51,7 +60,7 @@ class Fp8bsError(RuntimeError):
 _lib = None
 _lock = threading.Lock()
 
-_c_i64, _c_int, _c_vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_c_i64, _c_int, _c_vp, _c_f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 _SIGNATURES = {
     "fp8bs_quantize_act": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp],
     "fp8bs_quantize_weight": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp],
@@ -77,7 +86,28 @@ _SIGNATURES = {
     "fp8bs_diag_gemm_unpromoted": [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp],
     "fp8bs_set_wait_timeout_ms": [_c_i64],
     "fp8bs_status_string": [_c_int],
+    "fp8bs_fp4_scale_bytes": [_c_i64, _c_i64, _c_int],
+    "fp8bs_quantize_fp4": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_vp],
+    "fp8bs_swiglu_quantize_fp4": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp],
+    "fp8bs_dequantize_fp4": [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_int, _c_i64, _c_vp],
+    "fp8bs_gemm_fp4": [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_i64, _c_i64, _c_i64,
+                       _c_vp],
+    "fp8bs_grouped_gemm_fp4": [_c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int,
+                               _c_i64, _c_i64, _c_vp],
+    "fp8bs_moe_route": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_i64, _c_int, _c_int,
+                        _c_f32, _c_f32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp],
+    "fp8bs_moe_route_workspace_bytes": [_c_i64, _c_int, _c_i64],
+    "fp8bs_moe_route_backward": [_c_vp, _c_int, _c_i64, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_i64, _c_int, _c_int,
+                                 _c_f32, _c_f32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp],
+    "fp8bs_moe_layout": [_c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp],
+    "fp8bs_moe_layout_rows": [_c_i64, _c_int, _c_int],
+    "fp8bs_moe_layout_workspace_bytes": [_c_i64, _c_int, _c_int],
 }
+
+# Results other than a status: sizes in bytes or rows (-1: refused), text.
+_RESULTS = {"fp8bs_status_string": ctypes.c_char_p, "fp8bs_fp4_scale_bytes": _c_i64,
+            "fp8bs_moe_route_workspace_bytes": _c_i64, "fp8bs_moe_layout_rows": _c_i64,
+            "fp8bs_moe_layout_workspace_bytes": _c_i64}
 
 
 def build(force: bool = False) -> str:
@@ -97,7 +127,7 @@ def load_library(path: str | None = None):
             for name, argtypes in _SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.argtypes = argtypes
-                fn.restype = ctypes.c_char_p if name == "fp8bs_status_string" else ctypes.c_int
+                fn.restype = _RESULTS.get(name, ctypes.c_int)
             _lib = lib
     return _lib
 
@@ -237,6 +267,80 @@ def fp8bs_status_string(status: int) -> str:
     return load_library().fp8bs_status_string(int(status)).decode()
 
 
+def fp8bs_quantize_fp4(x, rows_in, K, ldx, rows, M, fmt, q, sf, g, stream=None):
+    _check(load_library().fp8bs_quantize_fp4(_ptr(x), rows_in, K, ldx, _ptr(rows), M, int(fmt), _ptr(q), _ptr(sf),
+                                             _ptr(g), _stream(stream)), "fp8bs_quantize_fp4")
+
+
+def fp8bs_swiglu_quantize_fp4(h, M, I, ldh, live, fmt, q, sf, g, stream=None):
+    _check(load_library().fp8bs_swiglu_quantize_fp4(_ptr(h), M, I, ldh, _ptr(live), int(fmt), _ptr(q), _ptr(sf),
+                                                    _ptr(g), _stream(stream)), "fp8bs_swiglu_quantize_fp4")
+
+
+def fp8bs_dequantize_fp4(q, sf, g, M, K, fmt, out, out_dtype, ldo, stream=None):
+    _check(load_library().fp8bs_dequantize_fp4(_ptr(q), _ptr(sf), _ptr(g), M, K, int(fmt), _ptr(out), int(out_dtype),
+                                               ldo, _stream(stream)), "fp8bs_dequantize_fp4")
+
+
+def fp8bs_gemm_fp4(a, sfa, ga, b, sfb, gb, fmt, d, d_dtype, M, N, K, stream=None):
+    _check(load_library().fp8bs_gemm_fp4(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb), int(fmt), _ptr(d),
+                                         int(d_dtype), M, N, K, _stream(stream)), "fp8bs_gemm_fp4")
+
+
+def fp8bs_grouped_gemm_fp4(a, sfa, ga, M_total, offsets, num_groups, b, sfb, gb, fmt, d, d_dtype, N, K, stream=None):
+    _check(load_library().fp8bs_grouped_gemm_fp4(_ptr(a), _ptr(sfa), _ptr(ga), M_total, _ptr(offsets), num_groups,
+                                                 _ptr(b), _ptr(sfb), _ptr(gb), int(fmt), _ptr(d), int(d_dtype), N, K,
+                                                 _stream(stream)), "fp8bs_grouped_gemm_fp4")
+
+
+def fp8bs_moe_route(logits, in_dtype, T, E, ld, score, bias, valid, seq, S, k, normalize, scale, alpha, idx, w, counts,
+                    tokens, loss, ws, ws_bytes, stream=None):
+    _check(load_library().fp8bs_moe_route(_ptr(logits), int(in_dtype), T, E, ld, int(score), _ptr(bias), _ptr(valid),
+                                          _ptr(seq), S, k, int(normalize), scale, alpha, _ptr(idx), _ptr(w),
+                                          _ptr(counts), _ptr(tokens), _ptr(loss), _ptr(ws), ws_bytes,
+                                          _stream(stream)), "fp8bs_moe_route")
+
+
+def fp8bs_moe_route_backward(logits, in_dtype, T, E, ld, score, valid, seq, S, k, normalize, scale, alpha, idx, counts,
+                             tokens, dw, dloss, dlogits, ldd, stream=None):
+    _check(load_library().fp8bs_moe_route_backward(_ptr(logits), int(in_dtype), T, E, ld, int(score), _ptr(valid),
+                                                   _ptr(seq), S, k, int(normalize), scale, alpha, _ptr(idx),
+                                                   _ptr(counts), _ptr(tokens), _ptr(dw), _ptr(dloss), _ptr(dlogits),
+                                                   ldd, _stream(stream)), "fp8bs_moe_route_backward")
+
+
+def fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, ws_bytes, stream=None):
+    _check(load_library().fp8bs_moe_layout(_ptr(idx), T, k, E, _ptr(offsets), _ptr(row_token), rows, _ptr(row_of),
+                                           _ptr(ws), ws_bytes, _stream(stream)), "fp8bs_moe_layout")
+
+
+def _size(name: str, *args) -> int:
+    n = getattr(load_library(), name)(*args)
+    if n < 0:
+        raise Fp8bsError(1, name)
+    return n
+
+
+def fp8bs_fp4_scale_bytes(M: int, K: int, fmt: int) -> int:
+    return _size("fp8bs_fp4_scale_bytes", M, K, int(fmt))
+
+
+def moe_route_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return _size("fp8bs_moe_route_workspace_bytes", T, E, S)
+
+
+def moe_layout_rows(T: int, k: int, E: int) -> int:
+    """The most rows that the padded segments of T tokens' k choices among E experts can take."""
+    return _size("fp8bs_moe_layout_rows", T, k, E)
+
+
+def moe_layout_workspace_bytes(T: int, k: int, E: int) -> int:
+    return _size("fp8bs_moe_layout_workspace_bytes", T, k, E)
+
+
+fp4_scale_bytes = fp8bs_fp4_scale_bytes
+
+
 # ------------------------------------------------------ allocating conveniences
 
 def quantize_act(x, transposed: bool = False, pow2: bool = False, stream=None):
@@ -348,3 +452,136 @@ def quantize_act_weight(x, w, pow2: bool = False, stream=None):
     fp8bs_quantize_act_weight(x, M, K, x.stride(0), xq, sx, w, N, Kw, w.stride(0), wq, sw,
                               SCALE_POW2 if pow2 else SCALE_ABSMAX, stream)
     return xq, sx, wq, sw
+
+
+def _fp4_outputs(lead, K, fmt, device):
+    import torch
+    q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=device)
+    sf = torch.empty((*lead[:-1], fp8bs_fp4_scale_bytes(lead[-1], K, fmt)), dtype=torch.uint8, device=device)
+    g = torch.empty(lead, dtype=torch.float32, device=device) if fmt == FP4_E4M3X16 else None
+    return q, sf, g
+
+
+def quantize_fp4(x, fmt: int = FP4_E4M3X16, rows=None, stream=None):
+    """x: [M, K] bfloat16 CUDA tensor (K % 64 == 0), or expert weights [G, N, K]
+    (contiguous).  Returns (q [..., K/2] uint8, two E2M1 codes a byte; sf uint8,
+    the scales in 512-byte blocks of 128 rows; g float32, a scale per row, None
+    for FP4_UE8M0X32).  ``rows``: int32 [M'], quantise x[rows[i]] as row i (a
+    row of zeros where rows[i] < 0)."""
+    K = x.shape[-1]
+    if x.dim() == 3:
+        G, N, _ = x.shape
+        q, sf, g = _fp4_outputs((G, N), K, fmt, x.device)
+        if N % 128 == 0:      # the experts' scale blocks follow one another
+            fp8bs_quantize_fp4(x, G * N, K, x.stride(1), None, G * N, fmt, q, sf, g, stream)
+        else:
+            for i in range(G):
+                fp8bs_quantize_fp4(x[i], N, K, x.stride(1), None, N, fmt, q[i], sf[i], None if g is None else g[i],
+                                   stream)
+        return q, sf, g
+    M = x.shape[0] if rows is None else rows.shape[0]
+    q, sf, g = _fp4_outputs((M,), K, fmt, x.device)
+    fp8bs_quantize_fp4(x, x.shape[0], K, x.stride(0), rows, M, fmt, q, sf, g, stream)
+    return q, sf, g
+
+
+def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
+    """h: [M, 2I] bfloat16 CUDA tensor (gate | up).  Returns the 4-bit codes and
+    scales of BF16(silu(gate) * up), as quantize_fp4; rows with live[i] < 0
+    (int32 [M]) are rows of zeros."""
+    M, two_i = h.shape
+    q, sf, g = _fp4_outputs((M,), two_i // 2, fmt, h.device)
+    fp8bs_swiglu_quantize_fp4(h, M, two_i // 2, h.stride(0), live, fmt, q, sf, g, stream)
+    return q, sf, g
+
+
+def dequantize_fp4(q, sf, g=None, fmt: int = FP4_E4M3X16, out_dtype=None, stream=None):
+    """The values [M, K] of 4-bit codes, bfloat16 (default) or float32."""
+    import torch
+    M, K = q.shape[0], 2 * q.shape[1]
+    out = torch.empty((M, K), dtype=out_dtype or torch.bfloat16, device=q.device)
+    fp8bs_dequantize_fp4(q, sf, g, M, K, fmt, out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, K, stream)
+    return out
+
+
+def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
+    """D = A B^T of 4-bit operands; a = (q [M, K/2], sf, g) and b = (q [N, K/2], sf, g) as
+    quantize_fp4 returns them."""
+    import torch
+    (qa, sfa, ga), (qb, sfb, gb) = a, b
+    M, N, K = qa.shape[0], qb.shape[0], 2 * qa.shape[1]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=qa.device)
+    fp8bs_gemm_fp4(qa, sfa, ga, qb, sfb, gb, fmt, out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, M, N, K,
+                   stream)
+    return out
+
+
+def grouped_gemm_fp4(a, offsets, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
+    """Per-expert D rows = A rows of the expert x B[g]^T; offsets int32 CUDA tensor [G+1], b as
+    quantize_fp4 returns it for weights [G, N, K]."""
+    import torch
+    (qa, sfa, ga), (qb, sfb, gb) = a, b
+    M, K = qa.shape[0], 2 * qa.shape[1]
+    G, N, _ = qb.shape
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=qa.device)
+    fp8bs_grouped_gemm_fp4(qa, sfa, ga, M, offsets, G, qb, sfb, gb, fmt, out,
+                           OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, N, K, stream)
+    return out
+
+
+def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None, seq=None, normalize: bool = True,
+              scale: float = 1.0, alpha: float | None = None, stream=None):
+    """Expert choice of each token: logits [T, E] float32 or bfloat16.  Returns
+    (idx [T, k] int32, w [T, k] float32), and with ``alpha`` (the balance
+    loss's factor) also (counts [S, E] int32, tokens [S] int32, loss [1]).
+    ``valid``: uint8 [T]; ``seq``: int32 [S + 1], the sequences' first tokens."""
+    import torch
+    T, E = logits.shape
+    dev = logits.device
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    in_dtype = IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32
+    S = 1 if seq is None else seq.shape[0] - 1
+    if alpha is None:
+        fp8bs_moe_route(logits, in_dtype, T, E, logits.stride(0), score, bias, valid, None, 1, k, normalize, scale, 0.0,
+                        idx, w, None, None, None, None, 0, stream)
+        return idx, w
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    n = moe_route_workspace_bytes(T, E, S)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    fp8bs_moe_route(logits, in_dtype, T, E, logits.stride(0), score, bias, valid, seq, S, k, normalize, scale, alpha,
+                    idx, w, counts, tokens, loss, ws, n, stream)
+    return idx, w, counts, tokens, loss
+
+
+def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, seq=None, normalize: bool = True,
+                       scale: float = 1.0, alpha: float = 0.0, counts=None, tokens=None, dloss=None, stream=None):
+    """Gradient of moe_route's weights (dw [T, k]) and balance loss (dloss [1]
+    with counts and tokens; None leaves the loss out) with respect to the
+    logits, in their type."""
+    import torch
+    T, E = logits.shape
+    dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    fp8bs_moe_route_backward(logits, IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32, T, E, logits.stride(0),
+                             score, valid, seq, 1 if seq is None else seq.shape[0] - 1, idx.shape[1], normalize, scale,
+                             alpha, idx, counts, tokens, dw, dloss, dlogits, E, stream)
+    return dlogits
+
+
+def moe_layout(idx, E: int, stream=None):
+    """Row layout of the choices idx [T, k] among E experts: (offsets [E + 1], row_token
+    [rows], row_of [T, k]), int32, as fp8bs_moe_layout describes them."""
+    import torch
+    T, k = idx.shape
+    rows = moe_layout_rows(T, k, E)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=idx.device)
+    row_token = torch.empty(rows, dtype=torch.int32, device=idx.device)
+    row_of = torch.empty((T, k), dtype=torch.int32, device=idx.device)
+    n = moe_layout_workspace_bytes(T, k, E)
+    ws = torch.empty(n, dtype=torch.uint8, device=idx.device)
+    fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, n, stream)
+    return offsets, row_token, row_of

@@ -41,7 +41,9 @@ int current_device(int* sm_count) {
   return FP8BS_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned16(const void* p) { return aligned_to(p, 16); }
+bool aligned4(const void* p) { return aligned_to(p, 4); }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? FP8BS_OK : FP8BS_ERR_CUDA; }
 
@@ -345,6 +347,210 @@ int fp8bs_moe_combine(const void* y, int64_t rows_y, int64_t N, const int32_t* i
                                              static_cast<uint16_t*>(out), sms, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ 4 bits
+static bool fp4_format_ok(int fmt) { return fmt == FP8BS_FP4_E4M3X16 || fmt == FP8BS_FP4_UE8M0X32; }
+static int64_t fp4_blocks(int64_t K, int fmt) { return fmt == FP8BS_FP4_E4M3X16 ? (K + 63) / 64 : (K + 127) / 128; }
+
+int64_t fp8bs_fp4_scale_bytes(int64_t M, int64_t K, int fmt) {
+  if (!fp4_format_ok(fmt) || M < 0 || K < 0 || K % 64 != 0 || M > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return -1;
+  return (M + 127) / 128 * fp4_blocks(K, fmt) * 512;
+}
+
+static int quantize_fp4(const void* x, int64_t rows_in, int64_t K, int64_t ldx, const int32_t* rows, int64_t M, int fmt,
+                        bool swiglu, uint8_t* q, uint8_t* sf, float* g, void* stream) {
+  if (M < 0 || K < 0 || rows_in < 0 || ldx < (swiglu ? 2 * K : K) || !fp4_format_ok(fmt)) return FP8BS_ERR_INVALID_ARG;
+  if (rows == nullptr && rows_in != M) return FP8BS_ERR_INVALID_ARG;
+  if (K % 64 != 0) return FP8BS_ERR_SHAPE;
+  if (M > (int64_t(1) << 30) || K > (int64_t(1) << 24) || rows_in > (int64_t(1) << 31) - 1) return FP8BS_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8BS_OK;
+  if (q == nullptr || sf == nullptr || (rows_in > 0 && x == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (fmt == FP8BS_FP4_E4M3X16 && g == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(sf) || (ldx * 2) % 16 != 0) return FP8BS_ERR_ALIGNMENT;
+  if (!aligned4(g) || !aligned4(rows)) return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  return from_cuda(fp8bs::launch_quantize_fp4(static_cast<const uint16_t*>(x), rows_in, K, ldx, rows, M, fmt, swiglu, q,
+                                              sf, g, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_quantize_fp4(const void* x, int64_t rows_in, int64_t K, int64_t ldx, const int32_t* rows, int64_t M, int fmt,
+                       uint8_t* q, uint8_t* sf, float* g, void* stream) {
+  return quantize_fp4(x, rows_in, K, ldx, rows, M, fmt, false, q, sf, g, stream);
+}
+
+int fp8bs_swiglu_quantize_fp4(const void* h, int64_t M, int64_t I, int64_t ldh, const int32_t* live, int fmt,
+                              uint8_t* q, uint8_t* sf, float* g, void* stream) {
+  return quantize_fp4(h, M, I, ldh, live, M, fmt, true, q, sf, g, stream);
+}
+
+int fp8bs_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* g, int64_t M, int64_t K, int fmt, void* out,
+                         int out_dtype, int64_t ldo, void* stream) {
+  if (M < 0 || K < 0 || ldo < K || !fp4_format_ok(fmt)) return FP8BS_ERR_INVALID_ARG;
+  if (out_dtype != FP8BS_OUT_F32 && out_dtype != FP8BS_OUT_BF16) return FP8BS_ERR_INVALID_ARG;
+  if (K % 64 != 0) return FP8BS_ERR_SHAPE;
+  if (M > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8BS_OK;
+  if (q == nullptr || sf == nullptr || out == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (fmt == FP8BS_FP4_E4M3X16 && g == nullptr) return FP8BS_ERR_INVALID_ARG;
+  const bool bf16 = out_dtype == FP8BS_OUT_BF16;
+  if (!aligned16(q) || !aligned16(sf) || !aligned16(out) || !aligned4(g) || (ldo * (bf16 ? 2 : 4)) % 16 != 0)
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  return from_cuda(fp8bs::launch_dequantize_fp4(q, sf, g, M, K, fmt, out, bf16, ldo, static_cast<cudaStream_t>(stream)));
+}
+
+static int gemm_fp4(const uint8_t* a, const uint8_t* sfa, const float* ga, int64_t M, const int32_t* offsets,
+                    int num_groups, const uint8_t* b, const uint8_t* sfb, const float* gb, int fmt, void* d, int d_dtype,
+                    int64_t N, int64_t K, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || !fp4_format_ok(fmt)) return FP8BS_ERR_INVALID_ARG;
+  if (d_dtype != FP8BS_OUT_F32 && d_dtype != FP8BS_OUT_BF16) return FP8BS_ERR_INVALID_ARG;
+  if (K % 64 != 0 || N % 8 != 0) return FP8BS_ERR_SHAPE;
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 24) || K > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  if (K == 0) return FP8BS_ERR_SHAPE;
+  // tile numbers and scale-block rows are 32-bit in the kernel
+  const int64_t mt = (M + 127) / 128 + num_groups, nt = (N + 31) / 32, kb = fp4_blocks(K, fmt);
+  if (mt * nt >= (int64_t(1) << 31) || mt * kb >= (int64_t(1) << 31) || ((N + 127) / 128 * num_groups + 1) * kb >= (int64_t(1) << 31))
+    return FP8BS_ERR_SHAPE;
+  if (a == nullptr || sfa == nullptr || b == nullptr || sfb == nullptr || d == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (fmt == FP8BS_FP4_E4M3X16 && (ga == nullptr || gb == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sfa) || !aligned16(b) || !aligned16(sfb) || !aligned16(d)) return FP8BS_ERR_ALIGNMENT;
+  if (fmt == FP8BS_FP4_E4M3X16 && (!aligned4(ga) || !aligned16(gb))) return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::Fp4GemmArgs g;
+  g.a = a; g.sfa = sfa; g.ga = ga; g.b = b; g.sfb = sfb; g.gb = gb; g.d = d; g.offsets = offsets;
+  g.M = M; g.N = N; g.K = K; g.num_groups = num_groups;
+  g.out_bf16 = d_dtype == FP8BS_OUT_BF16;
+  g.timeout_ns = g_timeout_ns.load();
+  bool tmap_failed = false, reg_failed = false;
+  const cudaError_t e = fp8bs::launch_gemm_fp4(g, fmt, sms, static_cast<cudaStream_t>(stream), &tmap_failed, &reg_failed);
+  if (tmap_failed) return FP8BS_ERR_ALIGNMENT;
+  return from_cuda(e);
+}
+
+int fp8bs_gemm_fp4(const uint8_t* a, const uint8_t* sfa, const float* ga, const uint8_t* b, const uint8_t* sfb,
+                   const float* gb, int fmt, void* d, int d_dtype, int64_t M, int64_t N, int64_t K, void* stream) {
+  return gemm_fp4(a, sfa, ga, M, nullptr, 1, b, sfb, gb, fmt, d, d_dtype, N, K, stream);
+}
+
+int fp8bs_grouped_gemm_fp4(const uint8_t* a, const uint8_t* sfa, const float* ga, int64_t M_total,
+                           const int32_t* offsets, int num_groups, const uint8_t* b, const uint8_t* sfb, const float* gb,
+                           int fmt, void* d, int d_dtype, int64_t N, int64_t K, void* stream) {
+  if (num_groups < 1 || num_groups > 512) return FP8BS_ERR_INVALID_ARG;
+  if (offsets == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned4(offsets)) return FP8BS_ERR_ALIGNMENT;
+  return gemm_fp4(a, sfa, ga, M_total, offsets, num_groups, b, sfb, gb, fmt, d, d_dtype, N, K, stream);
+}
+
+// ------------------------------------------------------------------ router
+static bool route_sizes_ok(int64_t T, int E, int64_t S) {
+  return T >= 0 && T < (int64_t(1) << 31) && E >= 1 && E <= 1024 && S >= 1 && S <= 65535;
+}
+
+int64_t fp8bs_moe_route_workspace_bytes(int64_t T, int E, int64_t S) {
+  return route_sizes_ok(T, E, S) ? fp8bs::route_workspace_bytes(T, E, S) : -1;
+}
+
+// Argument checks that the router's two directions share; fills *r.
+static int route_args(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score, const uint8_t* valid,
+                      const int32_t* seq, int64_t S, int k, int normalize, float scale, float alpha,
+                      fp8bs::RouteArgs* r) {
+  if (in_dtype != FP8BS_IN_F32 && in_dtype != FP8BS_IN_BF16) return FP8BS_ERR_INVALID_ARG;
+  if (score != FP8BS_SCORE_SOFTMAX && score != FP8BS_SCORE_SIGMOID) return FP8BS_ERR_INVALID_ARG;
+  if (!route_sizes_ok(T, E, S) || k < 1 || k > 32 || k > E || ld < E) return FP8BS_ERR_INVALID_ARG;
+  if (seq == nullptr && S != 1) return FP8BS_ERR_INVALID_ARG;
+  if (T > 0 && logits == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned_to(logits, in_dtype == FP8BS_IN_F32 ? 4 : 2) || !aligned4(seq)) return FP8BS_ERR_ALIGNMENT;
+  *r = fp8bs::RouteArgs{};
+  r->logits = logits; r->bf16 = in_dtype == FP8BS_IN_BF16; r->T = T; r->ld = ld; r->E = E; r->k = k;
+  r->S = static_cast<int>(S); r->score = score; r->valid = valid; r->seq = seq; r->normalize = normalize != 0;
+  r->scale = scale; r->alpha = alpha;
+  return FP8BS_OK;
+}
+
+int fp8bs_moe_route(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score, const float* bias,
+                    const uint8_t* valid, const int32_t* seq, int64_t S, int k, int normalize, float scale, float alpha,
+                    int32_t* idx, float* w, int32_t* counts, int32_t* tokens, float* loss, void* ws, int64_t ws_bytes,
+                    void* stream) {
+  fp8bs::RouteArgs r;
+  int st = route_args(logits, in_dtype, T, E, ld, score, valid, seq, S, k, normalize, scale, alpha, &r);
+  if (st != FP8BS_OK) return st;
+  if (bias != nullptr && score != FP8BS_SCORE_SIGMOID) return FP8BS_ERR_INVALID_ARG;
+  const bool stats = loss != nullptr;
+  if ((counts != nullptr) != stats || (tokens != nullptr) != stats) return FP8BS_ERR_INVALID_ARG;
+  if (T > 0 && (idx == nullptr || w == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (stats && (ws == nullptr || ws_bytes < fp8bs::route_workspace_bytes(T, E, S))) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned4(bias) || !aligned4(idx) || !aligned4(w) || !aligned4(counts) || !aligned4(tokens) || !aligned4(loss) ||
+      !aligned16(ws))
+    return FP8BS_ERR_ALIGNMENT;
+  if (T == 0 && !stats) return FP8BS_OK;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  r.bias = bias; r.idx = idx; r.w = w; r.counts = counts; r.tokens = tokens; r.loss = loss;
+  return from_cuda(fp8bs::launch_route(r, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_moe_route_backward(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score,
+                             const uint8_t* valid, const int32_t* seq, int64_t S, int k, int normalize, float scale,
+                             float alpha, const int32_t* idx, const int32_t* counts, const int32_t* tokens,
+                             const float* dw, const float* dloss, void* dlogits, int64_t ldd, void* stream) {
+  fp8bs::RouteArgs r;
+  int st = route_args(logits, in_dtype, T, E, ld, score, valid, seq, S, k, normalize, scale, alpha, &r);
+  if (st != FP8BS_OK) return st;
+  if (ldd < E) return FP8BS_ERR_INVALID_ARG;
+  if (dloss != nullptr && (counts == nullptr || tokens == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (T == 0) return FP8BS_OK;
+  if (idx == nullptr || dw == nullptr || dlogits == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned4(idx) || !aligned4(counts) || !aligned4(tokens) || !aligned4(dw) || !aligned4(dloss) ||
+      !aligned_to(dlogits, in_dtype == FP8BS_IN_F32 ? 4 : 2))
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  r.idx = const_cast<int32_t*>(idx); r.counts = const_cast<int32_t*>(counts); r.tokens = const_cast<int32_t*>(tokens);
+  r.dw = dw; r.dloss = dloss; r.dlogits = dlogits; r.ldd = ldd;
+  return from_cuda(fp8bs::launch_route_backward(r, static_cast<cudaStream_t>(stream)));
+}
+
+static bool layout_sizes_ok(int64_t T, int k, int E) {
+  return T >= 0 && k >= 1 && k <= 64 && E >= 1 && E <= 1024 && T <= (int64_t(1) << 24) / k;
+}
+
+int64_t fp8bs_moe_layout_rows(int64_t T, int k, int E) {
+  if (!layout_sizes_ok(T, k, E)) return -1;
+  const int64_t pairs = T * k;
+  return (pairs + (pairs < E ? pairs : E) * 127 + 127) / 128 * 128;
+}
+
+int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E) {
+  return layout_sizes_ok(T, k, E) ? fp8bs::layout_workspace_bytes(T, k, E) : -1;
+}
+
+int fp8bs_moe_layout(const int32_t* idx, int64_t T, int k, int E, int32_t* offsets, int32_t* row_token, int64_t rows,
+                     int32_t* row_of, void* ws, int64_t ws_bytes, void* stream) {
+  if (T < 0 || k < 1 || k > 64 || E < 1 || E > 1024) return FP8BS_ERR_INVALID_ARG;
+  if (!layout_sizes_ok(T, k, E) || rows < fp8bs_moe_layout_rows(T, k, E) || rows > (int64_t(1) << 31) - 1)
+    return FP8BS_ERR_SHAPE;
+  if (offsets == nullptr || (rows > 0 && row_token == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (T > 0 && (idx == nullptr || row_of == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (T > 0 && (ws == nullptr || ws_bytes < fp8bs::layout_workspace_bytes(T, k, E))) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned4(idx) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(row_of) || !aligned4(ws))
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::LayoutArgs a{};
+  a.idx = idx; a.pairs = T * k; a.k = k; a.E = E; a.offsets = offsets; a.row_token = row_token; a.rows = rows;
+  a.row_of = row_of; a.hist = static_cast<int32_t*>(ws);
+  return from_cuda(fp8bs::launch_layout(a, static_cast<cudaStream_t>(stream)));
+}
+
 int fp8bs_selftest_wait_timeout(int64_t timeout_us, void* stream) {
   if (timeout_us < 1 || timeout_us > 10000000) return FP8BS_ERR_INVALID_ARG;
   int sms = 0;
@@ -372,12 +578,16 @@ int fp8bs_diag_gemm_unpromoted(const uint8_t* a, const uint8_t* b, float* d, int
 
 int fp8bs_get_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8BS_ERR_CUDA;
-  int v = 0, mx = 0, q = 0, dg = 0;
+  int v = 0, mx = 0, q = 0, f4 = 0, rt = 0, dg = 0;
   if (fp8bs::gemm_take_status(&v) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::gemm_mx_take_status(&mx) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::quant_take_status(&q) != cudaSuccess) return FP8BS_ERR_CUDA;
+  if (fp8bs::gemm_fp4_take_status(&f4) != cudaSuccess) return FP8BS_ERR_CUDA;
+  if (fp8bs::route_take_status(&rt) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::diag_take_status(&dg) != cudaSuccess) return FP8BS_ERR_CUDA;
-  return v != FP8BS_OK ? v : mx != FP8BS_OK ? mx : q != FP8BS_OK ? q : dg;
+  for (const int st : {v, mx, q, f4, rt})
+    if (st != FP8BS_OK) return st;
+  return dg;
 }
 
 int fp8bs_set_wait_timeout_ms(int64_t ms) {

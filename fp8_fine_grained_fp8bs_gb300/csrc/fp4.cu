@@ -1,0 +1,352 @@
+// 4-bit quantisers and the dequantiser (E2M1 codes with block scales along
+// K), the operands of the 4-bit GEMMs (gemm_fp4.cu).
+//
+//   FP8BS_FP4_E4M3X16:   g = max(fl(rowmax / 2688), 2^-100)
+//                        s = E4M3(fl(amax_16 / fl(6 g)))
+//                        code = E2M1(fl(x * fl(1 / fl(s g)))), 0 where s = 0
+//   FP8BS_FP4_UE8M0X32:  s = 2^k, the smallest with amax_32 / s <= 6,
+//                        -127 <= k;  code = E2M1(x / s) (exact quotient)
+//
+// 2688 = 6 * 448: the row's largest element meets the largest code of the
+// largest block scale.  The float32 scale of a row keeps E4M3 block scales
+// (2^-9 .. 448) in range whatever the row's magnitude, and is found in the
+// same pass as the codes, so no earlier pass over the tensor is needed.
+//
+// All memory-bound streams: a row is read once into registers (16 elements,
+// a "unit", per thread and step; rows longer than the registers hold are read
+// twice, from L2 the second time), its maximum is reduced across the row's
+// warps, and codes and scales leave with 8-byte and 4-byte stores.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fp8bs {
+namespace {
+
+constexpr int kUnit = 16;          // elements per thread and step
+constexpr int kUnitsPerThread = 2; // steps whose elements stay in registers
+constexpr int kQuantThreads = 256; // CTA size while a row takes at most 8 warps
+constexpr float kMinRowScale = 7.888609052210118e-31f;  // 2^-100: s * g and its reciprocal stay normal
+
+enum Fp4Source { kRows = 0, kSwiglu = 1 };
+
+struct Fp4QuantParams {
+  const uint16_t* x;      // [rows_in][ldx] BF16 (SwiGLU: gate | up)
+  const int32_t* rows;    // optional: source row of each output row (SwiGLU: liveness), < 0 a zero row
+  int64_t rows_in, ldx, M, K;
+  uint8_t* q;             // [M][K / 2]
+  uint8_t* sf;            // blocked scales
+  float* g;               // [M] (E4M3x16)
+};
+
+// Byte offset of the scale word (groups 4w .. 4w+3) of a row in the blocked
+// layout: 512-byte blocks of 128 rows x 4 groups, row r at 16 (r % 32) +
+// 4 ((r / 32) % 4), the layout tcgen05.cp.32x128b copies into tensor memory.
+__device__ __forceinline__ int64_t sf_word_offset(int64_t row, int64_t word, int64_t words) {
+  return ((row >> 7) * words + word) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// silu(gate) * up of two BF16 pairs, rounded to BF16: gate / (1 + e^-gate)
+// with expf and IEEE division; below -64, where 1 adds nothing to e^-gate and
+// e^-gate overflows in the end, gate e^(gate/2) e^(gate/2).
+__device__ __forceinline__ uint32_t swiglu_pair(uint32_t gate, uint32_t up) {
+  float v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = __uint_as_float(i == 0 ? gate << 16 : gate & 0xFFFF0000u);
+    const float b = __uint_as_float(i == 0 ? up << 16 : up & 0xFFFF0000u);
+    const bool low = a < -64.0f;
+    const float e = expf(low ? 0.5f * a : -a);
+    v[i] = (low ? a * e * e : a / (1.0f + e)) * b;
+  }
+  const __nv_bfloat162 r = __floats2bfloat162_rn(v[0], v[1]);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int kSrc>
+__device__ __forceinline__ void load_unit(const uint16_t* row, int64_t K, int64_t unit, uint32_t (&v)[8]) {
+  const uint4* p = reinterpret_cast<const uint4*>(row + unit * kUnit);
+  const uint4 a = __ldg(p), b = __ldg(p + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  if (kSrc == kSwiglu) {
+    const uint4* u = reinterpret_cast<const uint4*>(row + K + unit * kUnit);
+    const uint4 c = __ldg(u), d = __ldg(u + 1);
+    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = swiglu_pair(v[i], w[i]);
+  }
+}
+
+// Largest magnitude of a unit, as the upper half of a float32 (BF16 bits).
+__device__ __forceinline__ uint32_t unit_absmax(const uint32_t (&v)[8]) {
+  uint32_t m = v[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Eight values times r to eight codes, element 0 in the lowest four bits.
+__device__ __forceinline__ uint32_t codes8(const uint32_t* v, float r) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16) * r;
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u) * r;
+  }
+  uint32_t c;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(c)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return c;
+}
+
+__device__ __forceinline__ uint32_t e4m3_of(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+  return r & 0xFFu;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code)));
+  float f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n}\n" : "=f"(f) : "r"(h));
+  return f;
+}
+
+// Scale byte and reciprocal of a group with largest magnitude `amax`.
+template <int kFmt>
+__device__ __forceinline__ uint32_t group_scale(float amax, float g, float& r) {
+  if (kFmt == 0) {
+    const uint32_t s = e4m3_of(amax / (g * 6.0f));
+    const float d = e4m3_value(s) * g;
+    r = d > 0.0f ? 1.0f / d : 0.0f;
+    return s;
+  }
+  // amax = 1.m x 2^e: 2^(e-2) reaches 6 x 2^(e-2) = 1.5 x 2^e, so one more where
+  // the mantissa is above 1.5.  BF16 subnormals (e < -126) come out at k = -127.
+  const uint32_t b = __float_as_uint(amax);
+  const int k = static_cast<int>(b >> 23) - 129 + ((b & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+  const uint32_t byte = static_cast<uint32_t>(max(k, -127) + 127);
+  r = __uint_as_float((254u - byte) << 23);   // 2^-k, normal for every k in [-127, 126]
+  return byte;
+}
+
+// One row per kWarps warps.  kBig: rows longer than the units a thread keeps.
+template <int kFmt, int kSrc, int kWarps, bool kBig>
+__global__ void __launch_bounds__(kWarps > 8 ? kWarps * 32 : kQuantThreads)
+    fp4_quant_kernel(const Fp4QuantParams p) {
+  constexpr int kThreads = kWarps > 8 ? kWarps * 32 : kQuantThreads;
+  constexpr int kRowThreads = kWarps * 32;
+  constexpr int kRowsPerCta = kThreads / kRowThreads;
+  __shared__ uint32_t s_max[kThreads / 32];
+  griddep_launch_dependents();  // a GEMM launched behind this kernel may start its set-up
+  const int lane = threadIdx.x & 31;
+  const int t = threadIdx.x % kRowThreads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + threadIdx.x / kRowThreads;
+  const int64_t units = p.K / kUnit;
+  const int64_t words = kFmt == 0 ? units / 4 : (units + 7) / 8;
+  int64_t src = row;
+  bool live = row < p.M;
+  if (live && p.rows != nullptr) {
+    const int32_t r = p.rows[row];
+    live = r >= 0 && (kSrc == kSwiglu || r < p.rows_in);
+    if (kSrc != kSwiglu) src = r;
+  }
+  const uint16_t* xr = p.x + (live ? src * p.ldx : 0);
+
+  uint32_t v[kUnitsPerThread][8];
+  uint32_t am[kUnitsPerThread];
+  uint32_t rowmax = 0;
+  const int steps = kBig ? static_cast<int>((units + kRowThreads - 1) / kRowThreads) : kUnitsPerThread;
+  auto load = [&](int i, uint32_t (&w)[8]) {
+    const int64_t u = t + static_cast<int64_t>(i) * kRowThreads;
+    if (live && u < units) {
+      load_unit<kSrc>(xr, p.K, u, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 0u;
+    }
+  };
+  if (!kBig) {
+#pragma unroll
+    for (int i = 0; i < kUnitsPerThread; ++i) load(i, v[i]);
+#pragma unroll
+    for (int i = 0; i < kUnitsPerThread; ++i) {
+      am[i] = unit_absmax(v[i]);
+      rowmax = max(rowmax, am[i]);
+    }
+  } else if (kFmt == 0) {
+    for (int i = 0; i < steps; ++i) {
+      load(i, v[0]);
+      rowmax = max(rowmax, unit_absmax(v[0]));
+    }
+  }
+  float g = 0.0f;
+  if (kFmt == 0) {
+    rowmax = __reduce_max_sync(0xffffffffu, rowmax);
+    if (kWarps > 1) {
+      if (lane == 0) s_max[threadIdx.x >> 5] = rowmax;
+      __syncthreads();
+      const int w0 = (threadIdx.x / kRowThreads) * kWarps;
+      rowmax = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) rowmax = max(rowmax, s_max[w0 + w]);
+    }
+    g = fmaxf(__uint_as_float(rowmax << 16) / 2688.0f, kMinRowScale);
+    if (t == 0 && row < p.M) p.g[row] = g;
+  }
+  auto emit = [&](int i, const uint32_t (&w)[8], uint32_t amax) {
+    const int64_t u = t + static_cast<int64_t>(i) * kRowThreads;
+    if (kFmt == 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // two units per group
+    float r;
+    const uint32_t s = group_scale<kFmt>(__uint_as_float(amax << 16), g, r);
+    uint32_t word;
+    if (kFmt == 0) {
+      word = s << (8 * (lane & 3));
+    } else {
+      word = u < units ? s << (8 * ((lane >> 1) & 3)) : 0u;   // a last word of two groups ends in zeros
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    }
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    if (u >= units) return;
+    if (row >= p.M) word = 0u;  // scale rows up to a multiple of 128
+    if (kFmt == 0) {
+      if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(p.sf + sf_word_offset(row, u >> 2, words)) = word;
+    } else {
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(p.sf + sf_word_offset(row, u >> 3, words)) = word;
+    }
+    if (row < p.M)
+      *reinterpret_cast<uint2*>(p.q + row * (p.K / 2) + u * (kUnit / 2)) = make_uint2(codes8(w, r), codes8(w + 4, r));
+  };
+  if (!kBig) {
+#pragma unroll
+    for (int i = 0; i < kUnitsPerThread; ++i) emit(i, v[i], am[i]);
+  } else {
+    for (int i = 0; i < steps; ++i) {
+      load(i, v[0]);
+      emit(i, v[0], unit_absmax(v[0]));
+    }
+  }
+}
+
+// value = code * s (* g): the first product is exact in float32, the second
+// rounds once, BF16 output once more.
+template <int kFmt, bool kBf16>
+__global__ void __launch_bounds__(kQuantThreads)
+    fp4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf, const float* __restrict__ g,
+                       int64_t M, int64_t K, void* __restrict__ out, int64_t ldo, int row_threads) {
+  const int64_t units = K / kUnit;
+  const int64_t words = kFmt == 0 ? units / 4 : (units + 7) / 8;
+  const int rows_per_cta = kQuantThreads / row_threads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_cta + threadIdx.x / row_threads;
+  if (row >= M) return;
+  const float gr = kFmt == 0 ? __ldg(g + row) : 1.0f;
+  for (int64_t u = threadIdx.x % row_threads; u < units; u += row_threads) {
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(q + row * (K / 2) + u * (kUnit / 2)));
+    const int64_t grp = kFmt == 0 ? u : u >> 1;
+    const uint32_t sb = __ldg(sf + sf_word_offset(row, grp >> 2, words) + (grp & 3));
+    const float s = kFmt == 0 ? e4m3_value(sb) : __uint_as_float(sb == 0u ? 0x00400000u : sb << 23);
+    float f[kUnit];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t byte = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu;
+      uint32_t h;
+      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u16 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n}\n"
+          : "=r"(h)
+          : "h"(static_cast<uint16_t>(byte)));
+      float lo, hi;
+      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n}\n"
+          : "=f"(lo), "=f"(hi)
+          : "r"(h));
+      f[2 * i] = lo * s;
+      f[2 * i + 1] = hi * s;
+      if (kFmt == 0) {
+        f[2 * i] *= gr;
+        f[2 * i + 1] *= gr;
+      }
+    }
+    if (kBf16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * ldo + u * kUnit);
+      o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ldo + u * kUnit);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    }
+  }
+}
+
+template <int kFmt, int kSrc, int kWarps, bool kBig>
+cudaError_t run_quant(const Fp4QuantParams& p, cudaStream_t stream) {
+  constexpr int kThreads = kWarps > 8 ? kWarps * 32 : kQuantThreads;
+  constexpr int kRowsPerCta = kThreads / (kWarps * 32);
+  const int64_t ctas = (p.M + 127) / 128 * (128 / kRowsPerCta);
+  fp4_quant_kernel<kFmt, kSrc, kWarps, kBig><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int kFmt, int kSrc>
+cudaError_t pick_quant(const Fp4QuantParams& p, cudaStream_t stream) {
+  // the fewest warps that hold a row in registers
+  const int64_t per_warp = 32 * kUnit * kUnitsPerThread;
+  if (p.K <= per_warp) return run_quant<kFmt, kSrc, 1, false>(p, stream);
+  if (p.K <= 2 * per_warp) return run_quant<kFmt, kSrc, 2, false>(p, stream);
+  if (p.K <= 4 * per_warp) return run_quant<kFmt, kSrc, 4, false>(p, stream);
+  if (p.K <= 8 * per_warp) return run_quant<kFmt, kSrc, 8, false>(p, stream);
+  if (p.K <= 16 * per_warp) return run_quant<kFmt, kSrc, 16, false>(p, stream);
+  return run_quant<kFmt, kSrc, 16, true>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_fp4(const uint16_t* x, int64_t rows_in, int64_t K, int64_t ldx, const int32_t* rows,
+                                int64_t M, int fmt, bool swiglu, uint8_t* q, uint8_t* sf, float* g,
+                                cudaStream_t stream) {
+  Fp4QuantParams p;
+  p.x = x; p.rows = rows; p.rows_in = rows_in; p.ldx = ldx; p.M = M; p.K = K;
+  p.q = q; p.sf = sf; p.g = g;
+  if (fmt == 0)
+    return swiglu ? pick_quant<0, kSwiglu>(p, stream) : pick_quant<0, kRows>(p, stream);
+  return swiglu ? pick_quant<1, kSwiglu>(p, stream) : pick_quant<1, kRows>(p, stream);
+}
+
+cudaError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* g, int64_t M, int64_t K, int fmt,
+                                  void* out, bool out_bf16, int64_t ldo, cudaStream_t stream) {
+  const int64_t units = K / kUnit;
+  int row_threads = 32;
+  while (row_threads < kQuantThreads && row_threads < units) row_threads *= 2;
+  const int rows_per_cta = kQuantThreads / row_threads;
+  const unsigned grid = static_cast<unsigned>((M + rows_per_cta - 1) / rows_per_cta);
+  if (fmt == 0) {
+    if (out_bf16)
+      fp4_dequant_kernel<0, true><<<grid, kQuantThreads, 0, stream>>>(q, sf, g, M, K, out, ldo, row_threads);
+    else
+      fp4_dequant_kernel<0, false><<<grid, kQuantThreads, 0, stream>>>(q, sf, g, M, K, out, ldo, row_threads);
+  } else {
+    if (out_bf16)
+      fp4_dequant_kernel<1, true><<<grid, kQuantThreads, 0, stream>>>(q, sf, g, M, K, out, ldo, row_threads);
+    else
+      fp4_dequant_kernel<1, false><<<grid, kQuantThreads, 0, stream>>>(q, sf, g, M, K, out, ldo, row_threads);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fp8bs

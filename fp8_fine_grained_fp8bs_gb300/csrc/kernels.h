@@ -74,6 +74,84 @@ cudaError_t launch_gemm_pow2(const GemmArgs& args, int sm_count, cudaStream_t st
                              bool* reg_check_failed);
 cudaError_t gemm_mx_take_status(int* status);
 
+// ---- fp4.cu (4-bit quantisers and dequantiser; plain loads, no waits)
+// fmt: fp8bs_fp4_format.  rows: see fp8bs_quantize_fp4 (swiglu: the `live`
+// list of fp8bs_swiglu_quantize_fp4, x the gate/up matrix).
+cudaError_t launch_quantize_fp4(const uint16_t* x, int64_t rows_in, int64_t K, int64_t ldx, const int32_t* rows,
+                                int64_t M, int fmt, bool swiglu, uint8_t* q, uint8_t* sf, float* g,
+                                cudaStream_t stream);
+cudaError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* g, int64_t M, int64_t K, int fmt,
+                                  void* out, bool out_bf16, int64_t ldo, cudaStream_t stream);
+
+// ---- gemm_fp4.cu
+struct Fp4GemmArgs {
+  const uint8_t* a;        // [M][K / 2] E2M1 pairs
+  const uint8_t* sfa;      // blocked scales of A
+  const float* ga;         // [M] (E4M3x16)
+  const uint8_t* b;        // [G][N][K / 2] (G = 1 for the dense GEMM)
+  const uint8_t* sfb;      // [G] blocked scales of B
+  const float* gb;         // [G][N] (E4M3x16)
+  void* d;                 // [M][N]
+  const int32_t* offsets;  // device [G + 1], NULL for the dense GEMM
+  int64_t M, N, K;
+  int num_groups;
+  bool out_bf16;
+  uint64_t timeout_ns;
+};
+// tmap_failed, reg_check_failed: as launch_gemm.
+cudaError_t launch_gemm_fp4(const Fp4GemmArgs& args, int fmt, int sm_count, cudaStream_t stream, bool* tmap_failed,
+                            bool* reg_check_failed);
+cudaError_t gemm_fp4_take_status(int* status);
+
+// ---- route.cu (the MoE router and the layout of its choices; no waits)
+struct RouteArgs {
+  const void* logits;      // [T][ld] float32 or BF16
+  bool bf16;
+  int64_t T, ld;
+  int E, k, S;
+  int score;               // 0 softmax, 1 sigmoid
+  const float* bias;       // [E] or NULL
+  const uint8_t* valid;    // [T] or NULL
+  const int32_t* seq;      // [S + 1] or NULL (one sequence)
+  bool normalize;
+  float scale, alpha;
+  int32_t* idx;            // [T][k] (read by the backward pass)
+  float* w;                // [T][k]
+  int32_t* counts;         // [S][E]
+  int32_t* tokens;         // [S]
+  float* loss;             // [1], NULL: no statistics
+  const float* dw;         // backward: [T][k]
+  const float* dloss;      // backward: [1] or NULL
+  void* dlogits;           // backward: [T][ldd], the logits' type
+  int64_t ldd;
+  // set by the launchers
+  int64_t chunk;
+  float* part_p;
+  int32_t* part_n;
+  int32_t* part_t;
+  float* share;
+  int32_t* done;
+};
+int64_t route_workspace_bytes(int64_t T, int E, int64_t S);
+cudaError_t launch_route(RouteArgs args, void* ws, cudaStream_t stream);
+cudaError_t launch_route_backward(RouteArgs args, cudaStream_t stream);
+// Reads and clears the router's device status word (invalid sequences).
+cudaError_t route_take_status(int* status);
+
+struct LayoutArgs {
+  const int32_t* idx;      // [pairs]
+  int64_t pairs;
+  int k, E;
+  int32_t* offsets;        // [E + 1]
+  int32_t* row_token;      // [rows]
+  int64_t rows;
+  int32_t* row_of;         // [pairs]
+  int32_t* hist;           // workspace, more than one chunk
+  int64_t chunk;           // set by the launcher
+};
+int64_t layout_workspace_bytes(int64_t T, int k, int E);
+cudaError_t launch_layout(LayoutArgs args, cudaStream_t stream);
+
 // ---- moe.cu (row movement of the MoE dispatch and combine; no waits)
 cudaError_t launch_gather_q_rows(const uint8_t* q, const float* s, int64_t rows_in, int64_t H, bool s_in_kb_major,
                                  const int32_t* idx, int64_t rows_out, uint8_t* q_out, float* s_out,

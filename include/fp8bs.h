@@ -351,6 +351,187 @@ int fp8bs_gather_bf16_rows(const void* y, int64_t rows_in, int64_t N, const int3
 int fp8bs_moe_combine(const void* y, int64_t rows_y, int64_t N, const int32_t* idx, const float* w, int64_t T, int k,
                       void* out, void* stream);
 
+/* ---------------------------------------------------------------- 4 bits
+ * Microscaled 4-bit operands: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) with a scale per block of consecutive elements of K.
+ *
+ *   codes   [M][K/2] bytes, two codes a byte, the element of even column in
+ *           the low four bits.
+ *   scales  one byte per row and block, in blocks of 512 bytes that hold 128
+ *           rows x 4 groups: with J = K / 16 or K / 32 groups a row, the scale
+ *           of row r and group j is byte
+ *             ((r / 128) * ceil(J / 4) + j / 4) * 512
+ *             + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4,
+ *           fp8bs_fp4_scale_bytes(M, K, fmt) bytes in all.  The quantisers
+ *           fill the rows up to a multiple of 128 with zeros.
+ *   g       [M] float32, one scale per row (FP8BS_FP4_E4M3X16 only).
+ */
+typedef enum {
+  /* E4M3 scale per 16 elements and a float32 scale per row:
+   *   g = max(fl32(rowmax / 2688), 2^-100)            (2688 = 6 * 448)
+   *   s = E4M3_rne(fl32(amax / fl32(6 g)))            per 16 elements
+   *   code = E2M1_rne_satfinite(fl32(x * fl32(1 / fl32(s g)))), zero if s = 0
+   *   value = code * s * g */
+  FP8BS_FP4_E4M3X16 = 0,
+  /* UE8M0 scale per 32 elements (byte b stands for 2^(b - 127)): s = 2^k, the
+   * smallest power of two with amax / s <= 6, k >= -127;
+   *   code = E2M1_rne_satfinite(x / s), value = code * s.  g is not used and
+   * may be NULL. */
+  FP8BS_FP4_UE8M0X32 = 1
+} fp8bs_fp4_format;
+
+/* Bytes of the blocked scales of an [M][K] matrix; -1 for arguments that the
+ * calls below refuse. */
+int64_t fp8bs_fp4_scale_bytes(int64_t M, int64_t K, int fmt);
+
+/*
+ * 4-bit quantisation, optionally of gathered rows (the dispatch of tokens into
+ * the padded segments of their experts, quantised on the way):
+ *
+ *   out row i = the codes, scales (and g) of x[rows ? rows[i] : i][:];
+ *   rows[i] < 0 (or >= rows_in): a row of zeros (scales 0, g = 2^-100).
+ *
+ *   x     [rows_in][ldx] BF16, K columns used.                        (in)
+ *   rows  DEVICE int32 [M], or NULL: then rows_in must be M.          (in)
+ *   q, sf, g: see above.                                              (out)
+ * Rules: K % 64 == 0 (FP8BS_ERR_SHAPE); ldx >= K, ldx*2 % 16 == 0; x, q, sf
+ * 16-byte aligned.  0 <= M <= 2^30.
+ */
+int fp8bs_quantize_fp4(const void* x, int64_t rows_in, int64_t K, int64_t ldx, const int32_t* rows, int64_t M,
+                       int fmt, uint8_t* q, uint8_t* sf, float* g, void* stream);
+
+/*
+ * SwiGLU and 4-bit quantisation in one pass, the input of the experts' down
+ * projection: v = BF16_rne(gate / (1 + e^-gate) * up) (float32, IEEE division;
+ * below gate = -64 as gate e^(gate/2) e^(gate/2) up, which does not overflow),
+ * quantised as by fp8bs_quantize_fp4.
+ *
+ *   h     [M][ldh] BF16, gate in columns [0, I), up in [I, 2I).       (in)
+ *   live  DEVICE int32 [M], or NULL: live[i] < 0 gives a row of zeros and
+ *         h's row i is not read (padding; fp8bs_moe_layout's row_token). (in)
+ * Rules: I % 64 == 0, ldh >= 2I, ldh*2 % 16 == 0, I*2 % 16 == 0.
+ */
+int fp8bs_swiglu_quantize_fp4(const void* h, int64_t M, int64_t I, int64_t ldh, const int32_t* live, int fmt,
+                              uint8_t* q, uint8_t* sf, float* g, void* stream);
+
+/*
+ * The values that 4-bit codes stand for: out[m][k] = code * s (* g), the
+ * products in float32, rounded once more for BF16 output (fp8bs_out_dtype).
+ * Rules: K % 64 == 0; ldo >= K, ldo * (2 or 4) % 16 == 0; pointers 16-byte
+ * aligned (g: 4).
+ */
+int fp8bs_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* g, int64_t M, int64_t K, int fmt,
+                         void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * 4-bit GEMM, D = A * B^T of the values that the codes stand for, the block
+ * scales applied by the tensor core, all of K accumulated in FP32:
+ *
+ *   D[m][n] = ga[m] gb[n] sum_k a[m][k] sa(m, k) b[n][k] sb(n, k)
+ *
+ *   a, sfa, ga: [M][K] as above; b, sfb, gb: [N][K]; ga, gb unused (may be
+ *   NULL) with FP8BS_FP4_UE8M0X32.  d [M][N] FP32 or BF16 (fp8bs_out_dtype).
+ * Rules: K % 64 == 0, K > 0, N % 8 == 0, M arbitrary; pointers 16-byte aligned
+ * (ga: 4).  Scale bytes must not be NaN (E4M3 0x7F, 0xFF; UE8M0 0xFF) in rows
+ * below M and N.
+ */
+int fp8bs_gemm_fp4(const uint8_t* a, const uint8_t* sfa, const float* ga,
+                   const uint8_t* b, const uint8_t* sfb, const float* gb, int fmt,
+                   void* d, int d_dtype, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * Grouped (MoE) form: rows [offsets[g], offsets[g+1]) of A times expert g's
+ * weight, offsets as in fp8bs_grouped_gemm (device int32, multiples of 128,
+ * checked on the device).  b [G][N][K/2]; sfb: fp8bs_fp4_scale_bytes(N, K, fmt)
+ * bytes per expert, one expert after the other; gb [G][N].
+ */
+int fp8bs_grouped_gemm_fp4(const uint8_t* a, const uint8_t* sfa, const float* ga, int64_t M_total,
+                           const int32_t* offsets, int num_groups,
+                           const uint8_t* b, const uint8_t* sfb, const float* gb, int fmt,
+                           void* d, int d_dtype, int64_t N, int64_t K, void* stream);
+
+/* ---------------------------------------------------------------- router */
+typedef enum { FP8BS_IN_F32 = 0, FP8BS_IN_BF16 = 1 } fp8bs_in_dtype;
+typedef enum { FP8BS_SCORE_SOFTMAX = 0, FP8BS_SCORE_SIGMOID = 1 } fp8bs_score_kind;
+
+/*
+ * The MoE router: each token's k experts and gate weights, and, for training,
+ * the counts and the balance loss of every sequence.
+ *
+ *   s_i = softmax(z)_i or sigmoid(z_i);  p_i = s_i / sum_j s_j.
+ *   The experts chosen are the k of largest z_i, or of largest s_i + bias_i
+ *   (bias: sigmoid only), in descending order, ties to the lower index.  A
+ *   logit of -inf or NaN is not eligible: p_i = s_i = 0; a slot that finds no
+ *   eligible expert holds idx -1 and weight 0.  Tokens with valid[t] == 0 have
+ *   no eligible expert, whatever their logits hold.
+ *   w[t][j] = scale * s_idx / (normalize ? sum over the token's slots : 1).
+ *   Each sum that scores are divided by has 1e-20 added.
+ *
+ *   loss = alpha / S * sum_q sum_i f_qi P_qi   over the sequences q,
+ *     f_qi = E counts[q][i] / (k tokens[q]),  P_qi = sum_t p_i / tokens[q],
+ *   tokens[q] the sequence's tokens with an eligible expert (one without any
+ *   adds nothing).
+ *
+ *   logits [T][ld] float32 or BF16 (fp8bs_in_dtype), E columns.       (in)
+ *   bias   [E] float32 or NULL.  valid [T] bytes or NULL.              (in)
+ *   seq    DEVICE int32 [S + 1], 0 = seq[0] <= ... <= seq[S] = T, or NULL with
+ *          S = 1.  Checked on the device where it is read: a violation
+ *          records FP8BS_ERR_DEVICE_ARG and leaves the outputs undefined. (in)
+ *   idx    [T][k] int32, w [T][k] float32.                            (out)
+ *   counts [S][E] int32, tokens [S] int32, loss [1] float32: all three, or all
+ *          NULL to leave the statistics out (seq is then not read).   (out)
+ *   ws     scratch of fp8bs_moe_route_workspace_bytes(T, E, S) bytes with
+ *          statistics, else NULL.
+ * Rules: 1 <= E <= 1024, 1 <= k <= min(E, 32), ld >= E, 1 <= S <= 65535,
+ * T < 2^31; pointers aligned to their elements, ws to 16 bytes.  Sums are taken
+ * in a fixed order: the same inputs give the same bits.  Logits of +inf are
+ * outside the contract.
+ */
+int fp8bs_moe_route(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score, const float* bias,
+                    const uint8_t* valid, const int32_t* seq, int64_t S, int k, int normalize, float scale,
+                    float alpha, int32_t* idx, float* w, int32_t* counts, int32_t* tokens, float* loss,
+                    void* ws, int64_t ws_bytes, void* stream);
+/* -1 for arguments that fp8bs_moe_route refuses. */
+int64_t fp8bs_moe_route_workspace_bytes(int64_t T, int E, int64_t S);
+
+/*
+ * Gradient of fp8bs_moe_route with respect to the logits, from those of the
+ * weights and of the loss (the counts, and so f, are constants):
+ *   dlogits = dw . d w / d z + dloss[0] * d loss / d z,
+ * 0 for logits that are not eligible.  The scores are recomputed.
+ *
+ *   idx, counts, tokens: fp8bs_moe_route's outputs; other arguments as there.
+ *   dw      [T][k] float32 (slots with idx < 0 are not read).          (in)
+ *   dloss   DEVICE float32 [1], or NULL (counts, tokens may be NULL too). (in)
+ *   dlogits [T][ldd], of the logits' type, ldd >= E.                   (out)
+ */
+int fp8bs_moe_route_backward(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score,
+                             const uint8_t* valid, const int32_t* seq, int64_t S, int k, int normalize, float scale,
+                             float alpha, const int32_t* idx, const int32_t* counts, const int32_t* tokens,
+                             const float* dw, const float* dloss, void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * Row layout of the chosen experts, on the device: the segments that the
+ * grouped GEMMs read, as the host planner lays them out for one rank.
+ *
+ *   offsets   [E + 1] int32: expert e's segment is rows [offsets[e],
+ *             offsets[e+1]), its choices in token order, padded to a multiple
+ *             of 128.                                                   (out)
+ *   row_token [rows] int32: the token of each row, -1 for padding and for the
+ *             rows past offsets[E].                                     (out)
+ *   row_of    [T][k] int32: the row of each choice, -1 where idx is negative
+ *             or not below E.                                           (out)
+ *   idx [T][k] int32 (in); rows >= fp8bs_moe_layout_rows(T, k, E), the most
+ *   that any choice of experts can take (FP8BS_ERR_SHAPE otherwise).
+ *   ws: scratch of fp8bs_moe_layout_workspace_bytes(T, k, E) bytes.
+ * Rules: 1 <= E <= 1024, 1 <= k <= 64, T * k <= 2^24; pointers aligned to 4.
+ */
+int fp8bs_moe_layout(const int32_t* idx, int64_t T, int k, int E, int32_t* offsets, int32_t* row_token, int64_t rows,
+                     int32_t* row_of, void* ws, int64_t ws_bytes, void* stream);
+/* Both return -1 for arguments that fp8bs_moe_layout refuses. */
+int64_t fp8bs_moe_layout_rows(int64_t T, int k, int E);
+int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E);
+
 /*
  * Synchronises `stream`, then returns and clears the device status of the
  * current device: FP8BS_OK, FP8BS_ERR_TIMEOUT, FP8BS_ERR_DEVICE_ARG, or
