@@ -49,6 +49,7 @@ constexpr uint32_t kF4LaunchRegs = 168;
 static_assert(kF4RegsControl * 128 + kF4RegsEpilogue * kF4EpiThreads == kF4LaunchRegs * kF4Threads, "register split");
 constexpr int kF4StageK = 256;              // elements of K per stage
 constexpr int kF4MmaK = 64;                 // elements of K per MMA
+constexpr int kStageMmas = kF4StageK / kF4MmaK;
 constexpr int kSfBlockBytes = 512;          // 128 rows x 4 scales
 
 struct F4Params {
@@ -65,7 +66,7 @@ struct F4Params {
   uint64_t timeout_ns;
 };
 
-template <int kFmt, int BN, bool kPair>
+template <int kFmt, int BN, bool kGrouped, bool kPair>
 struct F4Cfg {
   static constexpr int kABytes = kBlockM * 128;
   static constexpr int kBBytes = (kPair ? BN / 2 : BN) * 128;
@@ -79,7 +80,8 @@ struct F4Cfg {
   static constexpr int kSfBase = kAccBufs * BN;
   static constexpr int kOutBytes = (kF4EpiThreads / 32) * kOutBoxBytes;
   static constexpr int kMaxStages = (static_cast<int>(kF4TmemCols) - kSfBase) / kSfCols;
-  static constexpr int kTailBytes = (2 * 8 + 2 * 2 + 1) * 8 + 16 + 2 * (kMaxGroups + 1) * 4;
+  static constexpr int kGroupBytes = kGrouped ? 2 * (kMaxGroups + 1) * 4 : 0;
+  static constexpr int kTailBytes = (2 * 8 + 2 * 2 + 1) * 8 + 16 + 8 + kGroupBytes;
   static constexpr int kFit = (kSmemBudget - kOutBytes - kTailBytes - 1024) / kStageBytes;
   static constexpr int kStages0 = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
@@ -93,7 +95,7 @@ struct F4Cfg {
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffGroups = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kOffGroups + 2 * (kMaxGroups + 1) * 4 + 1024;
+  static constexpr int kSmemBytes = kOffGroups + kGroupBytes + 1024;
   static constexpr int kColsPerThread = BN / 2;
   static_assert(kOffOut % 1024 == 0, "staging boxes need 1024-byte alignment for the 128-byte swizzle");
   static_assert(kSmemBytes <= kSmemBudget, "shared memory budget");
@@ -137,7 +139,7 @@ __device__ __forceinline__ void mma_fp4(uint32_t tmem_d, uint64_t adesc, uint64_
 template <int kFmt, int BN, bool kPair>
 __device__ __forceinline__ void issue_stage(uint32_t dtmem, uint32_t a, uint32_t b, uint32_t sfa, uint32_t sfb,
                                             uint32_t sf_col, uint32_t n_half, int mmas, bool first) {
-  using C = F4Cfg<kFmt, BN, kPair>;
+  using C = F4Cfg<kFmt, BN, false, kPair>;
   constexpr int kPerBlock = kFmt == 0 ? 1 : 2;              // MMAs that read one scale block
   constexpr uint32_t kSfbCol = C::kSfPerStage * 4;
 #pragma unroll
@@ -160,7 +162,7 @@ __device__ __forceinline__ void issue_stage(uint32_t dtmem, uint32_t a, uint32_t
   }
   const uint64_t adesc = sw128_kmajor_desc(a), bdesc = sw128_kmajor_desc(b);
 #pragma unroll
-  for (int k = 0; k < kF4StageK / kF4MmaK; ++k) {
+  for (int k = 0; k < kStageMmas; ++k) {
     if (k < mmas) {
       const int j = k / kPerBlock;
       const uint32_t id = kFmt == 0 ? 0u : 2u * static_cast<uint32_t>(k & 1);
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSfA, const __grid_constant__ CUtensorMap tmSfB,
                     const __grid_constant__ CUtensorMap tmD, const F4Params p) {
-  using C = F4Cfg<kFmt, BN, kPair>;
+  using C = F4Cfg<kFmt, BN, kGrouped, kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + C::kOffA;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   int* s_off = reinterpret_cast<int*>(smem + C::kOffGroups);
   int* s_cum = s_off + (kMaxGroups + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform, and known to be
   const int lane = threadIdx.x & 31;
   const int ntn = (p.N + BN - 1) / BN;
   const int nst = (p.N + 127) / 128;   // 128-column scale tiles of one B
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   tc_fence_after_sync();
   if (kPair) cluster_sync();
   griddep_wait();  // operands, scales and D are touched only after the preceding kernel
-  const uint32_t tmem_base = misc[0];
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, misc[0], 0);
   const int total_tiles = static_cast<int>(misc[2]);
 
   if (warp < kF4EpiWarp0) {
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const int sfb_row = (g * nst + n0 / 128) * p.nsb;
         for (int kb = 0; kb < p.nkb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns)) { live = false; break; }
-          if (lane == 0) {
+          if (elect_one()) {
             uint8_t* da = sA + stage * C::kABytes;
             uint8_t* db = sB + stage * C::kBBytes;
             uint8_t* dsa = sSfA + stage * C::kSfABytes;
@@ -385,11 +387,15 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         for (int kb = 0; kb < p.nkb; ++kb) {
           if (!warp_wait(&full[stage], phase, p.timeout_ns)) { live = false; break; }
           tc_fence_after_sync();
-          if (lane == 0) {
-            const int mmas = min(kF4StageK / kF4MmaK, (p.K - kb * kF4StageK) / kF4MmaK);
-            issue_stage<kFmt, BN, kPair>(dtmem, smem_u32(sA + stage * C::kABytes), smem_u32(sB + stage * C::kBBytes),
-                                         smem_u32(sSfA + stage * C::kSfABytes), smem_u32(sSfB + stage * C::kSfBBytes),
-                                         tmem_base + C::kSfBase + stage * C::kSfCols, n_half, mmas, kb == 0);
+          const int mmas = min(kStageMmas, (p.K - kb * kF4StageK) / kF4MmaK);
+          if (elect_one()) {
+            const uint32_t a = smem_u32(sA + stage * C::kABytes), b = smem_u32(sB + stage * C::kBBytes);
+            const uint32_t sfa = smem_u32(sSfA + stage * C::kSfABytes), sfb = smem_u32(sSfB + stage * C::kSfBBytes);
+            const uint32_t sf_col = tmem_base + C::kSfBase + stage * C::kSfCols;
+            if (mmas == kStageMmas)   // the count known: straight-line issue
+              issue_stage<kFmt, BN, kPair>(dtmem, a, b, sfa, sfb, sf_col, n_half, kStageMmas, kb == 0);
+            else
+              issue_stage<kFmt, BN, kPair>(dtmem, a, b, sfa, sfb, sf_col, n_half, mmas, kb == 0);
             if (kPair) {
               mma_commit_pair(&empty[stage], 0x3);
               if (kb + 1 == p.nkb) mma_commit_pair(&acc_full[abuf], 0x3);
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       }
       if (!live) record_fp4_status(kStatusTimeout);
       // every MMA issued must have completed before TMEM is released
-      if (lane == 0) {
+      if (elect_one()) {
         if (kPair)
           mma_commit_pair(&teardown[0], 0x1);
         else
@@ -497,7 +503,7 @@ bool encode_scales(CUtensorMap* map, const uint8_t* base, int64_t blocks, uint32
 template <int kFmt, int BN, bool kGrouped, bool kPair>
 cudaError_t run_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed,
                     bool* reg_check_failed) {
-  using C = F4Cfg<kFmt, BN, kPair>;
+  using C = F4Cfg<kFmt, BN, kGrouped, kPair>;
   auto kern = gemm_fp4_kernel<kFmt, BN, kGrouped, kPair>;
   cudaFuncAttributes attr;
   cudaError_t err = cudaFuncGetAttributes(&attr, kern);
