@@ -96,7 +96,6 @@ struct F4Cfg {
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffGroups = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffGroups + kGroupBytes + 1024;
-  static constexpr int kColsPerThread = BN / 2;
   static_assert(kOffOut % 1024 == 0, "staging boxes need 1024-byte alignment for the 128-byte swizzle");
   static_assert(kSmemBytes <= kSmemBudget, "shared memory budget");
 };
@@ -109,6 +108,16 @@ template <int kFmt>
 __host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, uint32_t sf_id) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (kFmt == 1 ? 1u << 23 : 0u) | (static_cast<uint32_t>(m >> 4) << 24) | (sf_id << 29);
+}
+
+// Four floats of the shared memory of a CTA of the cluster (an address from mapa_shared).
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 template <int kFmt, bool kPair>
@@ -225,6 +234,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     const __grid_constant__ CUtensorMap tmSfA, const __grid_constant__ CUtensorMap tmSfB,
                     const __grid_constant__ CUtensorMap tmD, const F4Params p) {
   using C = F4Cfg<kFmt, BN, kGrouped, kPair>;
+  constexpr int kColsPerThread = BN / 2;   // of an epilogue thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + C::kOffA;
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       const uint32_t abuf = epi_tiles % C::kAccBufs;
       const uint32_t aphase = (epi_tiles / C::kAccBufs) & 1u;
       const int y0 = row0 + quarter * 32;
-      const int ncol0 = n0 + colhalf * C::kColsPerThread;
+      const int ncol0 = n0 + colhalf * kColsPerThread;
       const bool mine = y0 < row_end && ncol0 < p.N;
       const float ga = kFmt == 0 && mine && y0 + lane < p.M ? __ldg(p.ga + y0 + lane) : 1.0f;
       const float* gb = p.gb + static_cast<int64_t>(g) * p.N + ncol0;
@@ -446,12 +456,12 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         break;
       }
       tc_fence_after_sync();
-      uint32_t acc[C::kColsPerThread / 32][32];
-      const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * C::kColsPerThread;
+      uint32_t acc[kColsPerThread / 32][32];
+      const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * kColsPerThread;
 #pragma unroll
-      for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
+      for (int ch = 0; ch < kColsPerThread / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
 #pragma unroll
-      for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_wait_ld(acc[ch]);
+      for (int ch = 0; ch < kColsPerThread / 32; ++ch) tmem_wait_ld(acc[ch]);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -463,9 +473,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       if (mine) {
         const float* v = reinterpret_cast<const float*>(&acc[0][0]);
         if (p.out_bf16)
-          store_scaled<kFmt, C::kColsPerThread, true>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
+          store_scaled<kFmt, kColsPerThread, true>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
         else
-          store_scaled<kFmt, C::kColsPerThread, false>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
+          store_scaled<kFmt, kColsPerThread, false>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -485,6 +495,200 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   }
 }
 
+
+// ------------------------------------------------------------ few rows of A
+// One m-tile (M <= 128): the product is a stream of B.  A cluster of 1, 2, 4
+// or 8 CTAs shares one 64-column tile, each CTA taking a part of K; the
+// partial tiles meet in shared memory and every CTA adds up and stores its
+// part of the columns, rank by rank, so the result does not depend on timing.
+// Only the rows of A that exist (rounded up to a swizzle atom of 8) are
+// loaded; what the other rows of the MMA hold reaches only rows of D that are
+// not stored.  Two CTAs share an SM while a stage is small.
+constexpr int kSkinnyBN = 64;
+constexpr int kSkinnyThreads = 192;      // warps 0-3 epilogue, 4 producer, 5 MMA issuer
+constexpr uint32_t kSkinnyTmemCols = 256;
+constexpr int kSkinnyMaxStages = 6;
+constexpr int kSkinnyMinSmem = 78 * 1024;
+constexpr int kSkinnyPitch = kSkinnyBN + 4;   // floats per row of the partial tile: 16-byte writes of a warp spread over the banks
+
+template <int kFmt>
+struct SkinnyCfg {
+  using C = F4Cfg<kFmt, kSkinnyBN, false, false>;
+  static constexpr int kBBytes = kSkinnyBN * 128;
+  static constexpr int kSfBase = kSkinnyBN;
+  static constexpr int kMaxStages =
+      std::min(kSkinnyMaxStages, (static_cast<int>(kSkinnyTmemCols) - kSfBase) / C::kSfCols);
+  static int stage_bytes(int a_rows) { return a_rows * 128 + kBBytes + C::kSfABytes + C::kSfBBytes; }
+};
+
+template <int kFmt>
+__global__ void __launch_bounds__(kSkinnyThreads, 2)
+    gemm_fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmSfA, const __grid_constant__ CUtensorMap tmSfB,
+                           const F4Params p, void* __restrict__ d, int a_rows, int stages, int split) {
+  using S = SkinnyCfg<kFmt>;
+  using C = typename S::C;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], acc_full, teardown;
+  __shared__ uint32_t s_tmem;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int a_bytes = a_rows * 128;
+  uint8_t* sA = smem;                                   // [stages], 1024-byte aligned: a_rows is a multiple of 8
+  uint8_t* sB = sA + stages * a_bytes;
+  uint8_t* sSfA = sB + stages * S::kBBytes;
+  uint8_t* sSfB = sSfA + stages * C::kSfABytes;
+  float* part = reinterpret_cast<float*>(smem);         // the partial tile, once every stage has been read
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
+  const int n0 = static_cast<int>(blockIdx.x) / split * kSkinnyBN;
+  const int kb0 = static_cast<int>(rank) * p.nkb / split, kb1 = static_cast<int>(rank + 1) * p.nkb / split;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&teardown, 1);
+    fence_barrier_init();
+  }
+  if (warp == 4 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmSfA);
+    prefetch_tmap(&tmSfB);
+  }
+  if (warp == 5) {
+    tmem_alloc(&s_tmem, kSkinnyTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  griddep_wait();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, s_tmem, 0);
+  bool live = true;
+
+  if (warp == 4) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    const int sfb_row = n0 / 128 * p.nsb;
+    const uint32_t bytes = static_cast<uint32_t>(a_bytes + S::kBBytes + C::kSfABytes + C::kSfBBytes);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns)) { live = false; break; }
+      if (elect_one()) {
+        const int sk = kb * C::kSfPerStage;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        tma_load_2d(sB + stage * S::kBBytes, &tmB, &full[stage], kb * 128, n0);
+        tma_load_2d(sA + stage * a_bytes, &tmA, &full[stage], kb * 128, 0);
+        tma_load_2d(sSfA + stage * C::kSfABytes, &tmSfA, &full[stage], 0, sk);
+        tma_load_2d(sSfB + stage * C::kSfBBytes, &tmSfB, &full[stage], 0, sfb_row + sk);
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+    }
+    if (!live)
+      for (int s = 0; s < stages && s < issued; ++s) {
+        int st = stage - 1 - s;
+        uint32_t ph = phase;
+        if (st < 0) { st += stages; ph ^= 1; }
+        (void)mbar_wait(&full[st], ph, p.timeout_ns);
+      }
+  } else if (warp == 5) {
+    int stage = 0;
+    uint32_t phase = 0;
+    const uint32_t n_half = static_cast<uint32_t>(n0 % 128) / 32;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&full[stage], phase, p.timeout_ns)) { live = false; break; }
+      tc_fence_after_sync();
+      const int mmas = min(kStageMmas, (p.K - kb * kF4StageK) / kF4MmaK);
+      if (elect_one()) {
+        const uint32_t a = smem_u32(sA + stage * a_bytes), b = smem_u32(sB + stage * S::kBBytes);
+        const uint32_t sfa = smem_u32(sSfA + stage * C::kSfABytes), sfb = smem_u32(sSfB + stage * C::kSfBBytes);
+        const uint32_t sf_col = tmem_base + S::kSfBase + stage * C::kSfCols;
+        if (mmas == kStageMmas)
+          issue_stage<kFmt, kSkinnyBN, false>(tmem_base, a, b, sfa, sfb, sf_col, n_half, kStageMmas, kb == kb0);
+        else
+          issue_stage<kFmt, kSkinnyBN, false>(tmem_base, a, b, sfa, sfb, sf_col, n_half, mmas, kb == kb0);
+        mma_commit(&empty[stage]);
+        if (kb + 1 == kb1) mma_commit(&acc_full);
+      }
+      __syncwarp();
+      if (++stage == stages) { stage = 0; phase ^= 1; }
+    }
+    // every MMA issued must have completed before tensor memory is released
+    if (elect_one()) mma_commit(&teardown);
+    __syncwarp();
+    (void)mbar_wait(&teardown, 0, p.timeout_ns);
+  } else if (warp * 32 < p.M) {
+    if (mbar_wait(&acc_full, 0, p.timeout_ns)) {
+      tc_fence_after_sync();
+      uint32_t acc[2][32];
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+      tmem_ld32(taddr, acc[0]);
+      tmem_ld32(taddr + 32, acc[1]);
+      tmem_wait_ld(acc[0]);
+      tmem_wait_ld(acc[1]);
+      const int row = warp * 32 + lane;
+      // acc_full: every MMA of this CTA is done, so no stage is read or written any more
+      if (row < p.M) {
+#pragma unroll
+        for (int c = 0; c < kSkinnyBN; c += 4)
+          *reinterpret_cast<uint4*>(part + row * kSkinnyPitch + c) =
+              make_uint4(acc[c / 32][c % 32], acc[c / 32][c % 32 + 1], acc[c / 32][c % 32 + 2], acc[c / 32][c % 32 + 3]);
+      }
+    } else {
+      live = false;
+    }
+  }
+  if (!live) record_fp4_status(kStatusTimeout);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (split > 1) cluster_sync();
+  // pieces of four columns, dealt over the cluster's threads
+  const int cols = min(kSkinnyBN, p.N - n0);
+  for (int i = static_cast<int>(rank) * kSkinnyThreads + static_cast<int>(threadIdx.x); i < static_cast<int>(p.M) * (kSkinnyBN / 4);
+       i += split * kSkinnyThreads) {
+    const int row = i / (kSkinnyBN / 4), c = i % (kSkinnyBN / 4) * 4;
+    if (c >= cols) continue;
+    const float* src = part + row * kSkinnyPitch + c;
+    float4 v;
+    if (split == 1) {
+      v = *reinterpret_cast<const float4*>(src);
+    } else {
+      v = ld_cluster(mapa_shared(src, 0));
+      for (int r = 1; r < split; ++r) {
+        const float4 w = ld_cluster(mapa_shared(src, static_cast<uint32_t>(r)));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+    }
+    if (kFmt == 0) {
+      const float ga = __ldg(p.ga + row);
+      const float4 s = __ldg(reinterpret_cast<const float4*>(p.gb + n0 + c));
+      v.x *= ga * s.x;
+      v.y *= ga * s.y;
+      v.z *= ga * s.z;
+      v.w *= ga * s.w;
+    }
+    const int64_t at = static_cast<int64_t>(row) * p.N + n0 + c;
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(d) + at) = v;
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync();   // no CTA leaves while another reads its partial tile
+  if (warp == 5) tmem_dealloc(tmem_base, kSkinnyTmemCols);
+}
+
 // Scale blocks as a 2-D tensor of 512-byte rows; one box is one stage's
 // blocks of 128 rows.  Blocks past K belong to the next rows (or are filled
 // with zeros past the end) and no MMA reads them.
@@ -500,24 +704,56 @@ bool encode_scales(CUtensorMap* map, const uint8_t* base, int64_t blocks, uint32
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+
+F4Params params_of(const Fp4GemmArgs& a, int64_t nsb) {
+  F4Params kp;
+  kp.ga = a.ga;
+  kp.gb = a.gb;
+  kp.offsets = a.offsets;
+  kp.M = a.M;
+  kp.N = static_cast<int>(a.N);
+  kp.K = static_cast<int>(a.K);
+  kp.nkb = static_cast<int>((a.K + kF4StageK - 1) / kF4StageK);
+  kp.nsb = static_cast<int>(nsb);
+  kp.num_groups = a.num_groups;
+  kp.out_bf16 = a.out_bf16 ? 1 : 0;
+  kp.timeout_ns = a.timeout_ns;
+  return kp;
+}
+
+// Scale blocks along K.
+template <int kFmt>
+int64_t scale_blocks(int64_t K) {
+  constexpr int64_t block_k = kFmt == 0 ? 64 : 128;
+  return (K + block_k - 1) / block_k;
+}
+
 template <int kFmt, int BN, bool kGrouped, bool kPair>
 cudaError_t run_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed,
                     bool* reg_check_failed) {
   using C = F4Cfg<kFmt, BN, kGrouped, kPair>;
   auto kern = gemm_fp4_kernel<kFmt, BN, kGrouped, kPair>;
-  cudaFuncAttributes attr;
-  cudaError_t err = cudaFuncGetAttributes(&attr, kern);
+  // once per device: the register count that the split needs, the shared memory allowance
+  static std::atomic<int> prepared[kMaxCachedDevices];
+  int regs_ok = 0;
+  const cudaError_t err = cached_per_device(
+      prepared,
+      [&](int* v) {
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+        if (e != cudaSuccess) return e;
+        *v = attr.numRegs * kF4Threads >= static_cast<int>(kF4RegsControl * 128 + kF4RegsEpilogue * kF4EpiThreads) ? 2 : 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+      },
+      &regs_ok);
   if (err != cudaSuccess) return err;
-  if (attr.numRegs * kF4Threads < static_cast<int>(kF4RegsControl * 128 + kF4RegsEpilogue * kF4EpiThreads)) {
+  if (regs_ok != 2) {
     *reg_check_failed = true;
     return cudaErrorInvalidConfiguration;
   }
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (err != cudaSuccess) return err;
 
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) / 2;
-  const int64_t block_k = kFmt == 0 ? 64 : 128;
-  const int64_t nsb = (a.K + block_k - 1) / block_k;
+  const int64_t nsb = scale_blocks<kFmt>(a.K);
   const int64_t nst = (a.N + 127) / 128;
   CUtensorMap tmA, tmB, tmSfA, tmSfB, tmD;
   const uint64_t dA[2] = {row_bytes, static_cast<uint64_t>(a.M)};
@@ -535,19 +771,7 @@ cudaError_t run_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, boo
     return cudaErrorInvalidValue;
   }
 
-  F4Params kp;
-  kp.ga = a.ga;
-  kp.gb = a.gb;
-  kp.offsets = a.offsets;
-  kp.M = a.M;
-  kp.N = static_cast<int>(a.N);
-  kp.K = static_cast<int>(a.K);
-  kp.nkb = static_cast<int>((a.K + kF4StageK - 1) / kF4StageK);
-  kp.nsb = static_cast<int>(nsb);
-  kp.num_groups = a.num_groups;
-  kp.out_bf16 = a.out_bf16 ? 1 : 0;
-  kp.timeout_ns = a.timeout_ns;
-
+  const F4Params kp = params_of(a, nsb);
   const int64_t ntn = (a.N + BN - 1) / BN;
   int64_t mt_bound = kGrouped ? (a.M / kBlockM + a.num_groups) : (a.M + kBlockM - 1) / kBlockM;
   if (kPair) mt_bound = (mt_bound + 1) / 2;
@@ -557,11 +781,84 @@ cudaError_t run_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, boo
                                   tmSfA, tmSfB, tmD, kp);
 }
 
+// How many CTAs share the K of a 64-column tile: as many as keep the grid
+// within two CTAs per SM and every CTA at least two stages.
+int skinny_split(int64_t N, int64_t nkb, int sm_count) {
+  const int64_t tiles = (N + kSkinnyBN - 1) / kSkinnyBN;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * sm_count && nkb >= split * 2 * 2) split *= 2;
+  return split;
+}
+
+template <int kFmt>
+cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed) {
+  using S = SkinnyCfg<kFmt>;
+  using C = typename S::C;
+  auto kern = gemm_fp4_skinny_kernel<kFmt>;
+  static std::atomic<int> prepared[kMaxCachedDevices];
+  int ignored = 0;
+  cudaError_t err = cached_per_device(
+      prepared,
+      [&](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget - 1024);
+      },
+      &ignored);
+  if (err != cudaSuccess) return err;
+
+  const F4Params kp = params_of(a, scale_blocks<kFmt>(a.K));
+  const int split = skinny_split(a.N, kp.nkb, sm_count);
+  const int a_rows = static_cast<int>((a.M + 7) / 8 * 8);
+  // two CTAs of an SM share its shared memory (1 KB of each is the system's, 1 KB alignment)
+  const int stage = S::stage_bytes(a_rows);
+  int stages = std::min(S::kMaxStages, (kSmemBudget / 2 - 3 * 1024) / stage);
+  if (stages < 4) stages = std::min(S::kMaxStages, (kSmemBudget - 3 * 1024) / stage);
+  stages = std::max(2, std::min(stages, (kp.nkb + split - 1) / split));
+  const int part = static_cast<int>(a.M) * kSkinnyPitch * 4;
+  // At least a third of the SM's shared memory, so that never more than two CTAs
+  // of 256 tensor memory columns meet on an SM: a third would wait for columns
+  // that a CTA holds while it waits, in turn, for a cluster peer elsewhere.
+  const int smem = std::max(std::max(stages * stage, part) + 1024, kSkinnyMinSmem);
+
+  const uint64_t row_bytes = static_cast<uint64_t>(a.K) / 2;
+  CUtensorMap tmA, tmB, tmSfA, tmSfB;
+  const uint64_t dA[2] = {row_bytes, static_cast<uint64_t>(a.M)};
+  const uint64_t dB[2] = {row_bytes, static_cast<uint64_t>(a.N)};
+  const uint64_t stride[1] = {row_bytes};
+  bool ok = encode_operand(&tmA, a.a, 2, dA, stride, static_cast<uint32_t>(a_rows));
+  ok = ok && encode_operand(&tmB, a.b, 2, dB, stride, kSkinnyBN);
+  ok = ok && encode_scales(&tmSfA, a.sfa, kp.nsb, C::kSfPerStage);
+  ok = ok && encode_scales(&tmSfB, a.sfb, (a.N + 127) / 128 * kp.nsb, C::kSfPerStage);
+  if (!ok) {
+    *tmap_failed = true;
+    return cudaErrorInvalidValue;
+  }
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.N + kSkinnyBN - 1) / kSkinnyBN * split), 1, 1);
+  cfg.blockDim = dim3(kSkinnyThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attrs;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  err = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSfA, tmSfB, kp, a.d, a_rows, stages, split);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 template <int kFmt>
 cudaError_t pick_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed,
                      bool* reg_check_failed) {
+  if (a.offsets == nullptr && a.M <= kBlockM) return run_skinny<kFmt>(a, sm_count, stream, tmap_failed);
   const int64_t mt = (a.M + kBlockM - 1) / kBlockM;
   const bool narrow = a.N <= 128 || mt * ((a.N + 255) / 256) < sm_count;
+  if (a.offsets != nullptr && a.N > 128 && a.M <= int64_t(192) * a.num_groups)
+    return run_fp4<kFmt, 256, true, false>(a, sm_count, stream, tmap_failed, reg_check_failed);
   if (a.offsets != nullptr)
     return narrow ? run_fp4<kFmt, 128, true, false>(a, sm_count, stream, tmap_failed, reg_check_failed)
                   : run_fp4<kFmt, 256, true, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
