@@ -103,11 +103,11 @@ struct F4Cfg {
 // Instruction descriptor of the block-scaled 4-bit kinds: B scale id in bits
 // 4-5, A and B E2M1 (1 in bits 7-9 and 10-12), both K-major, N >> 3 in bits
 // 17-22, scale type in bit 23 (0 E4M3, 1 UE8M0), M >> 4 in bits 24-28, A
-// scale id in bits 29-30, K = 64 (bit 31 clear).
+// scale id in bits 29-30, K = 64 (bit 31 clear).  The scale ids are zero here.
 template <int kFmt>
-__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (kFmt == 1 ? 1u << 23 : 0u) | (static_cast<uint32_t>(m >> 4) << 24) | (sf_id << 29);
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (kFmt == 1 ? 1u << 23 : 0u) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // Four floats of the shared memory of a CTA of the cluster (an address from mapa_shared).
@@ -142,26 +142,26 @@ __device__ __forceinline__ void mma_fp4(uint32_t tmem_d, uint64_t adesc, uint64_
 
 // Issues one stage's MMAs: copies the stage's scale blocks into its columns
 // of tensor memory, then one MMA per 64 elements of K that the stage holds.
-// a, b: shared-memory addresses of the tiles; sfa, sfb: of the scale blocks;
-// sf_col: first tensor memory column of the stage's scales; n_half: 32-column
-// offset of the tile within its 128-column scale tile (BN = 64).
-template <int kFmt, int BN, bool kPair>
+// a, b: shared-memory addresses of the tiles; sfa, sfb: of the scale blocks,
+// kNTiles tiles of 128 columns of B; sf_col: first tensor memory column of the
+// stage's scales; idesc: with scale ids of zero.
+template <int kFmt, int kNTiles, bool kPair>
 __device__ __forceinline__ void issue_stage(uint32_t dtmem, uint32_t a, uint32_t b, uint32_t sfa, uint32_t sfb,
-                                            uint32_t sf_col, uint32_t n_half, int mmas, bool first) {
-  using C = F4Cfg<kFmt, BN, false, kPair>;
-  constexpr int kPerBlock = kFmt == 0 ? 1 : 2;              // MMAs that read one scale block
-  constexpr uint32_t kSfbCol = C::kSfPerStage * 4;
+                                            uint32_t sf_col, uint32_t idesc, int mmas, bool first) {
+  constexpr int kBlocks = kFmt == 0 ? 4 : 2;                // scale blocks per 128 rows and stage
+  constexpr int kPerBlock = kStageMmas / kBlocks;           // MMAs that read one scale block
+  constexpr uint32_t kSfbCol = kBlocks * 4;
 #pragma unroll
-  for (int j = 0; j < C::kSfPerStage; ++j) {
+  for (int j = 0; j < kBlocks; ++j) {
     if (j * kPerBlock < mmas) {
       if (kPair)
         tmem_cp_rows_pair(sf_col + 4 * j, sf_rows_desc(sfa + j * kSfBlockBytes));
       else
         tmem_cp_rows(sf_col + 4 * j, sf_rows_desc(sfa + j * kSfBlockBytes));
 #pragma unroll
-      for (int h = 0; h < C::kNTiles; ++h) {
-        const uint32_t dst = sf_col + kSfbCol + 4 * (j * C::kNTiles + h);
-        const uint64_t src = sf_rows_desc(sfb + (h * C::kSfPerStage + j) * kSfBlockBytes);
+      for (int h = 0; h < kNTiles; ++h) {
+        const uint32_t dst = sf_col + kSfbCol + 4 * (j * kNTiles + h);
+        const uint64_t src = sf_rows_desc(sfb + (h * kBlocks + j) * kSfBlockBytes);
         if (kPair)
           tmem_cp_rows_pair(dst, src);
         else
@@ -175,8 +175,8 @@ __device__ __forceinline__ void issue_stage(uint32_t dtmem, uint32_t a, uint32_t
     if (k < mmas) {
       const int j = k / kPerBlock;
       const uint32_t id = kFmt == 0 ? 0u : 2u * static_cast<uint32_t>(k & 1);
-      mma_fp4<kFmt, kPair>(dtmem, adesc + 2 * k, bdesc + 2 * k, idesc_fp4<kFmt>(kPair ? 2 * kBlockM : kBlockM, BN, id),
-                           sf_col + 4 * j, sf_col + kSfbCol + 4 * C::kNTiles * j + n_half, (!first || k > 0) ? 1u : 0u);
+      mma_fp4<kFmt, kPair>(dtmem, adesc + 2 * k, bdesc + 2 * k, idesc | (id << 4) | (id << 29), sf_col + 4 * j,
+                           sf_col + kSfbCol + 4 * kNTiles * j, (!first || k > 0) ? 1u : 0u);
     }
   }
 }
@@ -393,7 +393,6 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         const uint32_t aphase = (tiles_done / C::kAccBufs) & 1u;
         if (!warp_wait(&acc_empty[abuf], aphase ^ 1u, p.timeout_ns)) { live = false; break; }
         const uint32_t dtmem = tmem_base + abuf * BN;
-        const uint32_t n_half = BN < 128 ? static_cast<uint32_t>((t % ntn) * BN % 128) / 32 : 0u;
         for (int kb = 0; kb < p.nkb; ++kb) {
           if (!warp_wait(&full[stage], phase, p.timeout_ns)) { live = false; break; }
           tc_fence_after_sync();
@@ -402,10 +401,11 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             const uint32_t a = smem_u32(sA + stage * C::kABytes), b = smem_u32(sB + stage * C::kBBytes);
             const uint32_t sfa = smem_u32(sSfA + stage * C::kSfABytes), sfb = smem_u32(sSfB + stage * C::kSfBBytes);
             const uint32_t sf_col = tmem_base + C::kSfBase + stage * C::kSfCols;
+            constexpr uint32_t kIdesc = idesc_fp4<kFmt>(kPair ? 2 * kBlockM : kBlockM, BN);
             if (mmas == kStageMmas)   // the count known: straight-line issue
-              issue_stage<kFmt, BN, kPair>(dtmem, a, b, sfa, sfb, sf_col, n_half, kStageMmas, kb == 0);
+              issue_stage<kFmt, C::kNTiles, kPair>(dtmem, a, b, sfa, sfb, sf_col, kIdesc, kStageMmas, kb == 0);
             else
-              issue_stage<kFmt, BN, kPair>(dtmem, a, b, sfa, sfb, sf_col, n_half, mmas, kb == 0);
+              issue_stage<kFmt, C::kNTiles, kPair>(dtmem, a, b, sfa, sfb, sf_col, kIdesc, mmas, kb == 0);
             if (kPair) {
               mma_commit_pair(&empty[stage], 0x3);
               if (kb + 1 == p.nkb) mma_commit_pair(&acc_full[abuf], 0x3);
@@ -497,52 +497,57 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 
 
 // ------------------------------------------------------------ few rows of A
-// One m-tile (M <= 128): the product is a stream of B.  A cluster of 1, 2, 4
-// or 8 CTAs shares one 64-column tile, each CTA taking a part of K; the
-// partial tiles meet in shared memory and every CTA adds up and stores its
-// part of the columns, rank by rank, so the result does not depend on timing.
-// Only the rows of A that exist (rounded up to a swizzle atom of 8) are
-// loaded; what the other rows of the MMA hold reaches only rows of D that are
-// not stored.  Two CTAs share an SM while a stage is small.
-constexpr int kSkinnyBN = 64;
+// M <= 128: the product is a stream of B, which takes the MMA's side of 128
+// rows: a tile is 128 rows of B (columns of D) times all rows of A (rounded up
+// to 16, the MMA's N), so each MMA consumes 4 KB of B whatever M is.  With A on
+// the side of 128 rows and 64-column tiles, half the B per MMA and per scale
+// copy, one token times [7168][7168] took 9.4 us, and 6.7 with three of four
+// MMAs left out.
+//
+// A cluster of 1, 2, 4 or 8 CTAs shares a tile, each CTA taking a part of K;
+// the partial tiles meet in shared memory and every CTA adds up and stores its
+// part, rank by rank, so the result does not depend on timing.  Two CTAs share
+// an SM while a stage is small.
 constexpr int kSkinnyThreads = 192;      // warps 0-3 epilogue, 4 producer, 5 MMA issuer
 constexpr uint32_t kSkinnyTmemCols = 256;
 constexpr int kSkinnyMaxStages = 6;
 constexpr int kSkinnyMinSmem = 78 * 1024;
-constexpr int kSkinnyPitch = kSkinnyBN + 4;   // floats per row of the partial tile: 16-byte writes of a warp spread over the banks
+constexpr int kSkinnyPitch = 128 + 4;    // floats per row of the partial tile
 
 template <int kFmt>
 struct SkinnyCfg {
-  using C = F4Cfg<kFmt, kSkinnyBN, false, false>;
-  static constexpr int kBBytes = kSkinnyBN * 128;
-  static constexpr int kSfBase = kSkinnyBN;
-  static constexpr int kMaxStages =
-      std::min(kSkinnyMaxStages, (static_cast<int>(kSkinnyTmemCols) - kSfBase) / C::kSfCols);
-  static int stage_bytes(int a_rows) { return a_rows * 128 + kBBytes + C::kSfABytes + C::kSfBBytes; }
+  static constexpr int kBlocks = kFmt == 0 ? 4 : 2;                 // scale blocks per 128 rows and stage
+  static constexpr int kWBytes = 128 * 128;                         // 128 rows of B
+  static constexpr int kSfBytes = kBlocks * kSfBlockBytes;          // of one operand
+  static constexpr int kSfCols = 2 * kBlocks * 4;                   // tensor memory columns per stage
+  static int stage_bytes(int rows) { return rows * 128 + kWBytes + 2 * kSfBytes; }
+  // accumulators take `rows` columns, rounded up to the 32 that a load reads
+  static int max_stages(int rows) {
+    return std::min(kSkinnyMaxStages, (static_cast<int>(kSkinnyTmemCols) - (rows + 31) / 32 * 32) / kSfCols);
+  }
 };
 
 template <int kFmt>
 __global__ void __launch_bounds__(kSkinnyThreads, 2)
     gemm_fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                            const __grid_constant__ CUtensorMap tmSfA, const __grid_constant__ CUtensorMap tmSfB,
-                           const F4Params p, void* __restrict__ d, int a_rows, int stages, int split) {
+                           const F4Params p, void* __restrict__ d, int rows, int stages, int split) {
   using S = SkinnyCfg<kFmt>;
-  using C = typename S::C;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kSkinnyMaxStages], empty[kSkinnyMaxStages], acc_full, teardown;
   __shared__ uint32_t s_tmem;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int a_bytes = a_rows * 128;
-  uint8_t* sA = smem;                                   // [stages], 1024-byte aligned: a_rows is a multiple of 8
-  uint8_t* sB = sA + stages * a_bytes;
-  uint8_t* sSfA = sB + stages * S::kBBytes;
-  uint8_t* sSfB = sSfA + stages * C::kSfABytes;
+  const int a_bytes = rows * 128;
+  uint8_t* sB = smem;                                   // [stages] 128 rows of B
+  uint8_t* sA = sB + stages * S::kWBytes;               // [stages] rows of A; a multiple of 16: 1024-byte aligned
+  uint8_t* sSfB = sA + stages * a_bytes;
+  uint8_t* sSfA = sSfB + stages * S::kSfBytes;
   float* part = reinterpret_cast<float*>(smem);         // the partial tile, once every stage has been read
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
-  const int n0 = static_cast<int>(blockIdx.x) / split * kSkinnyBN;
+  const int n0 = static_cast<int>(blockIdx.x) / split * 128;
   const int kb0 = static_cast<int>(rank) * p.nkb / split, kb1 = static_cast<int>(rank + 1) * p.nkb / split;
 
   if (threadIdx.x == 0) {
@@ -567,6 +572,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  griddep_launch_dependents();  // every CTA holds its tensor memory: the next kernel may start its set-up
   griddep_wait();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, s_tmem, 0);
   bool live = true;
@@ -576,16 +582,16 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     uint32_t phase = 0;
     int issued = 0;
     const int sfb_row = n0 / 128 * p.nsb;
-    const uint32_t bytes = static_cast<uint32_t>(a_bytes + S::kBBytes + C::kSfABytes + C::kSfBBytes);
+    const uint32_t bytes = static_cast<uint32_t>(a_bytes + S::kWBytes + 2 * S::kSfBytes);
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns)) { live = false; break; }
       if (elect_one()) {
-        const int sk = kb * C::kSfPerStage;
+        const int sk = kb * S::kBlocks;
         mbar_arrive_expect_tx(&full[stage], bytes);
-        tma_load_2d(sB + stage * S::kBBytes, &tmB, &full[stage], kb * 128, n0);
+        tma_load_2d(sB + stage * S::kWBytes, &tmB, &full[stage], kb * 128, n0);
+        tma_load_2d(sSfB + stage * S::kSfBytes, &tmSfB, &full[stage], 0, sfb_row + sk);
         tma_load_2d(sA + stage * a_bytes, &tmA, &full[stage], kb * 128, 0);
-        tma_load_2d(sSfA + stage * C::kSfABytes, &tmSfA, &full[stage], 0, sk);
-        tma_load_2d(sSfB + stage * C::kSfBBytes, &tmSfB, &full[stage], 0, sfb_row + sk);
+        tma_load_2d(sSfA + stage * S::kSfBytes, &tmSfA, &full[stage], 0, sk);
       }
       __syncwarp();
       ++issued;
@@ -601,19 +607,20 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   } else if (warp == 5) {
     int stage = 0;
     uint32_t phase = 0;
-    const uint32_t n_half = static_cast<uint32_t>(n0 % 128) / 32;
+    const uint32_t idesc = idesc_fp4<kFmt>(128, rows);
+    const uint32_t sf_base = tmem_base + (rows + 31) / 32 * 32;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!warp_wait(&full[stage], phase, p.timeout_ns)) { live = false; break; }
       tc_fence_after_sync();
       const int mmas = min(kStageMmas, (p.K - kb * kF4StageK) / kF4MmaK);
       if (elect_one()) {
-        const uint32_t a = smem_u32(sA + stage * a_bytes), b = smem_u32(sB + stage * S::kBBytes);
-        const uint32_t sfa = smem_u32(sSfA + stage * C::kSfABytes), sfb = smem_u32(sSfB + stage * C::kSfBBytes);
-        const uint32_t sf_col = tmem_base + S::kSfBase + stage * C::kSfCols;
+        const uint32_t b = smem_u32(sB + stage * S::kWBytes), a = smem_u32(sA + stage * a_bytes);
+        const uint32_t sfb = smem_u32(sSfB + stage * S::kSfBytes), sfa = smem_u32(sSfA + stage * S::kSfBytes);
+        const uint32_t sf_col = sf_base + stage * S::kSfCols;
         if (mmas == kStageMmas)
-          issue_stage<kFmt, kSkinnyBN, false>(tmem_base, a, b, sfa, sfb, sf_col, n_half, kStageMmas, kb == kb0);
+          issue_stage<kFmt, 1, false>(tmem_base, b, a, sfb, sfa, sf_col, idesc, kStageMmas, kb == kb0);
         else
-          issue_stage<kFmt, kSkinnyBN, false>(tmem_base, a, b, sfa, sfb, sf_col, n_half, mmas, kb == kb0);
+          issue_stage<kFmt, 1, false>(tmem_base, b, a, sfb, sfa, sf_col, idesc, mmas, kb == kb0);
         mma_commit(&empty[stage]);
         if (kb + 1 == kb1) mma_commit(&acc_full);
       }
@@ -624,26 +631,22 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     if (elect_one()) mma_commit(&teardown);
     __syncwarp();
     (void)mbar_wait(&teardown, 0, p.timeout_ns);
-  } else if (warp * 32 < p.M) {
-    if (mbar_wait(&acc_full, 0, p.timeout_ns)) {
-      tc_fence_after_sync();
-      uint32_t acc[2][32];
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-      tmem_ld32(taddr, acc[0]);
-      tmem_ld32(taddr + 32, acc[1]);
-      tmem_wait_ld(acc[0]);
-      tmem_wait_ld(acc[1]);
-      const int row = warp * 32 + lane;
-      // acc_full: every MMA of this CTA is done, so no stage is read or written any more
-      if (row < p.M) {
+  } else if (mbar_wait(&acc_full, 0, p.timeout_ns)) {
+    // every MMA of this CTA is done, so no stage is read or written any more;
+    // lane = column of D, register = row
+    tc_fence_after_sync();
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int r0 = 0; r0 < p.M; r0 += 32) {
+      uint32_t acc[32];
+      tmem_ld32(taddr + r0, acc);
+      tmem_wait_ld(acc);
+      float* out = part + r0 * kSkinnyPitch + warp * 32 + lane;
 #pragma unroll
-        for (int c = 0; c < kSkinnyBN; c += 4)
-          *reinterpret_cast<uint4*>(part + row * kSkinnyPitch + c) =
-              make_uint4(acc[c / 32][c % 32], acc[c / 32][c % 32 + 1], acc[c / 32][c % 32 + 2], acc[c / 32][c % 32 + 3]);
-      }
-    } else {
-      live = false;
+      for (int r = 0; r < 32; ++r)
+        if (r0 + r < p.M) out[r * kSkinnyPitch] = __uint_as_float(acc[r]);
     }
+  } else {
+    live = false;
   }
   if (!live) record_fp4_status(kStatusTimeout);
   tc_fence_before_sync();
@@ -651,11 +654,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   tc_fence_after_sync();
   if (split > 1) cluster_sync();
   // pieces of four columns, dealt over the cluster's threads
-  const int cols = min(kSkinnyBN, p.N - n0);
-  for (int i = static_cast<int>(rank) * kSkinnyThreads + static_cast<int>(threadIdx.x); i < static_cast<int>(p.M) * (kSkinnyBN / 4);
+  for (int i = static_cast<int>(rank) * kSkinnyThreads + static_cast<int>(threadIdx.x); i < static_cast<int>(p.M) * 32;
        i += split * kSkinnyThreads) {
-    const int row = i / (kSkinnyBN / 4), c = i % (kSkinnyBN / 4) * 4;
-    if (c >= cols) continue;
+    const int row = i >> 5, c = (i & 31) * 4;
+    if (n0 + c >= p.N) continue;   // N is a multiple of 8
     const float* src = part + row * kSkinnyPitch + c;
     float4 v;
     if (split == 1) {
@@ -781,19 +783,9 @@ cudaError_t run_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, boo
                                   tmSfA, tmSfB, tmD, kp);
 }
 
-// How many CTAs share the K of a 64-column tile: as many as keep the grid
-// within two CTAs per SM and every CTA at least two stages.
-int skinny_split(int64_t N, int64_t nkb, int sm_count) {
-  const int64_t tiles = (N + kSkinnyBN - 1) / kSkinnyBN;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sm_count && nkb >= split * 2 * 2) split *= 2;
-  return split;
-}
-
 template <int kFmt>
 cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed) {
   using S = SkinnyCfg<kFmt>;
-  using C = typename S::C;
   auto kern = gemm_fp4_skinny_kernel<kFmt>;
   static std::atomic<int> prepared[kMaxCachedDevices];
   int ignored = 0;
@@ -807,12 +799,15 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
   if (err != cudaSuccess) return err;
 
   const F4Params kp = params_of(a, scale_blocks<kFmt>(a.K));
-  const int split = skinny_split(a.N, kp.nkb, sm_count);
-  const int a_rows = static_cast<int>((a.M + 7) / 8 * 8);
-  // two CTAs of an SM share its shared memory (1 KB of each is the system's, 1 KB alignment)
-  const int stage = S::stage_bytes(a_rows);
-  int stages = std::min(S::kMaxStages, (kSmemBudget / 2 - 3 * 1024) / stage);
-  if (stages < 4) stages = std::min(S::kMaxStages, (kSmemBudget - 3 * 1024) / stage);
+  const int rows = static_cast<int>((a.M + 15) / 16 * 16);
+  // Stages of two CTAs on an SM (each also has 1 KB of the system's and 1 KB for
+  // alignment), and of K among the CTAs of a cluster: as many CTAs as are
+  // resident at once, each with two stages at least.
+  const int stage = S::stage_bytes(rows);
+  int stages = std::min(S::max_stages(rows), (kSmemBudget / 2 - 3 * 1024) / stage);
+  const int64_t tiles = (a.N + 127) / 128;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * sm_count && kp.nkb >= split * 2 * 2) split *= 2;
   stages = std::max(2, std::min(stages, (kp.nkb + split - 1) / split));
   const int part = static_cast<int>(a.M) * kSkinnyPitch * 4;
   // At least a third of the SM's shared memory, so that never more than two CTAs
@@ -825,10 +820,10 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
   const uint64_t dA[2] = {row_bytes, static_cast<uint64_t>(a.M)};
   const uint64_t dB[2] = {row_bytes, static_cast<uint64_t>(a.N)};
   const uint64_t stride[1] = {row_bytes};
-  bool ok = encode_operand(&tmA, a.a, 2, dA, stride, static_cast<uint32_t>(a_rows));
-  ok = ok && encode_operand(&tmB, a.b, 2, dB, stride, kSkinnyBN);
-  ok = ok && encode_scales(&tmSfA, a.sfa, kp.nsb, C::kSfPerStage);
-  ok = ok && encode_scales(&tmSfB, a.sfb, (a.N + 127) / 128 * kp.nsb, C::kSfPerStage);
+  bool ok = encode_operand(&tmA, a.a, 2, dA, stride, static_cast<uint32_t>(rows));
+  ok = ok && encode_operand(&tmB, a.b, 2, dB, stride, 128);
+  ok = ok && encode_scales(&tmSfA, a.sfa, kp.nsb, S::kBlocks);
+  ok = ok && encode_scales(&tmSfB, a.sfb, tiles * kp.nsb, S::kBlocks);
   if (!ok) {
     *tmap_failed = true;
     return cudaErrorInvalidValue;
@@ -841,13 +836,13 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
   attrs[1].val.clusterDim.y = 1;
   attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + kSkinnyBN - 1) / kSkinnyBN * split), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, 1);
   cfg.blockDim = dim3(kSkinnyThreads, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attrs;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  err = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSfA, tmSfB, kp, a.d, a_rows, stages, split);
+  err = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSfA, tmSfB, kp, a.d, rows, stages, split);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
