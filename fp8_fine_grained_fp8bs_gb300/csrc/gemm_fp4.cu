@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                     const __grid_constant__ CUtensorMap tmSfA, const __grid_constant__ CUtensorMap tmSfB,
                     const __grid_constant__ CUtensorMap tmD, const F4Params p) {
   using C = F4Cfg<kFmt, BN, kGrouped, kPair>;
-  constexpr int kColsPerThread = BN / 2;   // of an epilogue thread
+  constexpr int kCols = BN / 2;   // of an epilogue thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + C::kOffA;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       const uint32_t abuf = epi_tiles % C::kAccBufs;
       const uint32_t aphase = (epi_tiles / C::kAccBufs) & 1u;
       const int y0 = row0 + quarter * 32;
-      const int ncol0 = n0 + colhalf * kColsPerThread;
+      const int ncol0 = n0 + colhalf * kCols;
       const bool mine = y0 < row_end && ncol0 < p.N;
       const float ga = kFmt == 0 && mine && y0 + lane < p.M ? __ldg(p.ga + y0 + lane) : 1.0f;
       const float* gb = p.gb + static_cast<int64_t>(g) * p.N + ncol0;
@@ -456,12 +456,12 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         break;
       }
       tc_fence_after_sync();
-      uint32_t acc[kColsPerThread / 32][32];
-      const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * kColsPerThread;
+      uint32_t acc[kCols / 32][32];
+      const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * kCols;
 #pragma unroll
-      for (int ch = 0; ch < kColsPerThread / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
+      for (int ch = 0; ch < kCols / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
 #pragma unroll
-      for (int ch = 0; ch < kColsPerThread / 32; ++ch) tmem_wait_ld(acc[ch]);
+      for (int ch = 0; ch < kCols / 32; ++ch) tmem_wait_ld(acc[ch]);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       if (mine) {
         const float* v = reinterpret_cast<const float*>(&acc[0][0]);
         if (p.out_bf16)
-          store_scaled<kFmt, kColsPerThread, true>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
+          store_scaled<kFmt, kCols, true>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
         else
-          store_scaled<kFmt, kColsPerThread, false>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
+          store_scaled<kFmt, kCols, false>(v, ga, gb, s_out, lane, &tmD, ncol0, p.N, y0);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -547,7 +547,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint32_t rank = split > 1 ? cluster_ctarank() : 0u;
-  const int n0 = static_cast<int>(blockIdx.x) / split * 128;
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int ntn = (p.N + 127) / 128;
+  const int n0 = tile % ntn * 128, m0 = tile / ntn * 128;
+  const int m_rows = min(128, static_cast<int>(p.M) - m0);
   const int kb0 = static_cast<int>(rank) * p.nkb / split, kb1 = static_cast<int>(rank + 1) * p.nkb / split;
 
   if (threadIdx.x == 0) {
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
-    const int sfb_row = n0 / 128 * p.nsb;
+    const int sfb_row = n0 / 128 * p.nsb, sfa_row = m0 / 128 * p.nsb;
     const uint32_t bytes = static_cast<uint32_t>(a_bytes + S::kWBytes + 2 * S::kSfBytes);
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns)) { live = false; break; }
@@ -590,8 +593,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         mbar_arrive_expect_tx(&full[stage], bytes);
         tma_load_2d(sB + stage * S::kWBytes, &tmB, &full[stage], kb * 128, n0);
         tma_load_2d(sSfB + stage * S::kSfBytes, &tmSfB, &full[stage], 0, sfb_row + sk);
-        tma_load_2d(sA + stage * a_bytes, &tmA, &full[stage], kb * 128, 0);
-        tma_load_2d(sSfA + stage * S::kSfBytes, &tmSfA, &full[stage], 0, sk);
+        tma_load_2d(sA + stage * a_bytes, &tmA, &full[stage], kb * 128, m0);
+        tma_load_2d(sSfA + stage * S::kSfBytes, &tmSfA, &full[stage], 0, sfa_row + sk);
       }
       __syncwarp();
       ++issued;
@@ -636,14 +639,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     // lane = column of D, register = row
     tc_fence_after_sync();
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-    for (int r0 = 0; r0 < p.M; r0 += 32) {
+    for (int r0 = 0; r0 < m_rows; r0 += 32) {
       uint32_t acc[32];
       tmem_ld32(taddr + r0, acc);
       tmem_wait_ld(acc);
       float* out = part + r0 * kSkinnyPitch + warp * 32 + lane;
 #pragma unroll
       for (int r = 0; r < 32; ++r)
-        if (r0 + r < p.M) out[r * kSkinnyPitch] = __uint_as_float(acc[r]);
+        if (r0 + r < m_rows) out[r * kSkinnyPitch] = __uint_as_float(acc[r]);
     }
   } else {
     live = false;
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   tc_fence_after_sync();
   if (split > 1) cluster_sync();
   // pieces of four columns, dealt over the cluster's threads
-  for (int i = static_cast<int>(rank) * kSkinnyThreads + static_cast<int>(threadIdx.x); i < static_cast<int>(p.M) * 32;
+  for (int i = static_cast<int>(rank) * kSkinnyThreads + static_cast<int>(threadIdx.x); i < m_rows * 32;
        i += split * kSkinnyThreads) {
     const int row = i >> 5, c = (i & 31) * 4;
     if (n0 + c >= p.N) continue;   // N is a multiple of 8
@@ -663,24 +666,29 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     if (split == 1) {
       v = *reinterpret_cast<const float4*>(src);
     } else {
-      v = ld_cluster(mapa_shared(src, 0));
-      for (int r = 1; r < split; ++r) {
-        const float4 w = ld_cluster(mapa_shared(src, static_cast<uint32_t>(r)));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
+      float4 w[8];   // every rank's piece in flight, added in the ranks' order
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < split) w[r] = ld_cluster(mapa_shared(src, static_cast<uint32_t>(r)));
+      v = w[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+        if (r < split) {
+          v.x += w[r].x;
+          v.y += w[r].y;
+          v.z += w[r].z;
+          v.w += w[r].w;
+        }
     }
     if (kFmt == 0) {
-      const float ga = __ldg(p.ga + row);
+      const float ga = __ldg(p.ga + m0 + row);
       const float4 s = __ldg(reinterpret_cast<const float4*>(p.gb + n0 + c));
       v.x *= ga * s.x;
       v.y *= ga * s.y;
       v.z *= ga * s.z;
       v.w *= ga * s.w;
     }
-    const int64_t at = static_cast<int64_t>(row) * p.N + n0 + c;
+    const int64_t at = static_cast<int64_t>(m0 + row) * p.N + n0 + c;
     if (p.out_bf16)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     else
@@ -799,17 +807,17 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
   if (err != cudaSuccess) return err;
 
   const F4Params kp = params_of(a, scale_blocks<kFmt>(a.K));
-  const int rows = static_cast<int>((a.M + 15) / 16 * 16);
+  const int rows = static_cast<int>((std::min<int64_t>(a.M, 128) + 15) / 16 * 16);
   // Stages of two CTAs on an SM (each also has 1 KB of the system's and 1 KB for
   // alignment), and of K among the CTAs of a cluster: as many CTAs as are
   // resident at once, each with two stages at least.
   const int stage = S::stage_bytes(rows);
   int stages = std::min(S::max_stages(rows), (kSmemBudget / 2 - 3 * 1024) / stage);
-  const int64_t tiles = (a.N + 127) / 128;
+  const int64_t ntn = (a.N + 127) / 128, tiles = (a.M + 127) / 128 * ntn;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= 2 * sm_count && kp.nkb >= split * 2 * 2) split *= 2;
   stages = std::max(2, std::min(stages, (kp.nkb + split - 1) / split));
-  const int part = static_cast<int>(a.M) * kSkinnyPitch * 4;
+  const int part = static_cast<int>(std::min<int64_t>(a.M, 128)) * kSkinnyPitch * 4;
   // At least a third of the SM's shared memory, so that never more than two CTAs
   // of 256 tensor memory columns meet on an SM: a third would wait for columns
   // that a CTA holds while it waits, in turn, for a cluster peer elsewhere.
@@ -822,8 +830,8 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
   const uint64_t stride[1] = {row_bytes};
   bool ok = encode_operand(&tmA, a.a, 2, dA, stride, static_cast<uint32_t>(rows));
   ok = ok && encode_operand(&tmB, a.b, 2, dB, stride, 128);
-  ok = ok && encode_scales(&tmSfA, a.sfa, kp.nsb, S::kBlocks);
-  ok = ok && encode_scales(&tmSfB, a.sfb, tiles * kp.nsb, S::kBlocks);
+  ok = ok && encode_scales(&tmSfA, a.sfa, (a.M + 127) / 128 * kp.nsb, S::kBlocks);
+  ok = ok && encode_scales(&tmSfB, a.sfb, ntn * kp.nsb, S::kBlocks);
   if (!ok) {
     *tmap_failed = true;
     return cudaErrorInvalidValue;
@@ -849,16 +857,28 @@ cudaError_t run_skinny(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, 
 template <int kFmt>
 cudaError_t pick_fp4(const Fp4GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed,
                      bool* reg_check_failed) {
-  if (a.offsets == nullptr && a.M <= kBlockM) return run_skinny<kFmt>(a, sm_count, stream, tmap_failed);
-  const int64_t mt = (a.M + kBlockM - 1) / kBlockM;
-  const bool narrow = a.N <= 128 || mt * ((a.N + 255) / 256) < sm_count;
-  if (a.offsets != nullptr && a.N > 128 && a.M <= int64_t(192) * a.num_groups)
-    return run_fp4<kFmt, 256, true, false>(a, sm_count, stream, tmap_failed, reg_check_failed);
-  if (a.offsets != nullptr)
-    return narrow ? run_fp4<kFmt, 128, true, false>(a, sm_count, stream, tmap_failed, reg_check_failed)
-                  : run_fp4<kFmt, 256, true, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
-  return narrow ? run_fp4<kFmt, 128, false, false>(a, sm_count, stream, tmap_failed, reg_check_failed)
-                : run_fp4<kFmt, 256, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
+  const int64_t mt = (a.M + kBlockM - 1) / kBlockM, nkb = (a.K + kF4StageK - 1) / kF4StageK;
+  if (a.offsets != nullptr) {
+    // Pairs take the rows of a group two m-tiles at a time: with one m-tile a group
+    // their second halves idle (32 experts, N4096 K7168: 4224 rows 90.0 us on single
+    // CTAs and 101.9 on pairs, 6144 rows 102.7 and 110.2, 9728 rows 145.3 and 131.7).
+    return a.N <= 128 || mt * ((a.N + 255) / 256) < sm_count || a.M <= int64_t(256) * a.num_groups
+               ? run_fp4<kFmt, 128, true, false>(a, sm_count, stream, tmap_failed, reg_check_failed)
+               : run_fp4<kFmt, 256, true, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
+  }
+  const int64_t small = mt * ((a.N + 127) / 128), large = (mt + 1) / 2 * ((a.N + 255) / 256);
+  // One m-tile; or so few tiles that four CTAs can share each one's K, four stages
+  // or more apiece (M256 N4096 K7168: 11.2 us against 13.4 for 128x128 tiles
+  // that walk all of K; sharing by two loses, M200 N7168 K7168: 16.3 against 14.5).
+  if (a.M <= kBlockM || (small * 4 <= 2 * sm_count && nkb >= 16)) return run_skinny<kFmt>(a, sm_count, stream, tmap_failed);
+  // 256x256 tiles of a CTA pair against 128x128 tiles of one CTA by the waves they
+  // take: a stage costs 0.40 and 0.36 us, the pairs 1.5 us more to start
+  // (M512 N7168 K7168: 17.7 us in one wave of pairs, 24.3 in two of single CTAs;
+  // M1000 N4104 K448: 6.8 and 5.7).
+  const int64_t waves_small = (small + sm_count - 1) / sm_count, waves_large = (large + sm_count / 2 - 1) / (sm_count / 2);
+  return waves_large * nkb * 40 + 150 < waves_small * nkb * 36
+             ? run_fp4<kFmt, 256, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed)
+             : run_fp4<kFmt, 128, false, false>(a, sm_count, stream, tmap_failed, reg_check_failed);
 }
 
 }  // namespace
