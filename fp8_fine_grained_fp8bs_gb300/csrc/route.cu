@@ -70,48 +70,59 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 
 // One token's logits in registers: z[i] is expert 32 i + lane, -inf past E.
 template <int NL>
-__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int lane, bool live, float (&z)[NL]) {
+__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int lane, float (&z)[NL]) {
+  if (a.bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + lane;
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int e = 32 * i + lane;
-    z[i] = live && e < a.E ? load_logit(a.logits, a.bf16, t * a.ld + e) : -INFINITY;
+    for (int i = 0; i < NL; ++i)
+      z[i] = 32 * i + lane < a.E ? __uint_as_float(static_cast<uint32_t>(__ldg(p + 32 * i)) << 16) : -INFINITY;
+  } else {
+    const float* p = static_cast<const float*>(a.logits) + t * a.ld + lane;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) z[i] = 32 * i + lane < a.E ? __ldg(p + 32 * i) : -INFINITY;
   }
 }
 
-// Scores of a token (0 where not eligible) and their sum (+ eps).  softmax
-// returns them normalised (and the sum 1), with the maximum and the inverse
-// of the exponentials' sum, which the score of a single logit needs.
+// e^x and 1 / x by the hardware's base-2 exponential and reciprocal, for the
+// scores that only enter sums and gradients (relative error below 2^-21 where
+// the result matters); the weights and biased keys use expf and IEEE division.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// sigmoid(z) and its derivative from t = e^-|z|, which cannot overflow.
+__device__ __forceinline__ float fast_sigmoid(float z, float& slope) {
+  const float t = fast_exp(-fabsf(z)), r = fast_rcp(1.0f + t);
+  slope = t * r * r;
+  return z >= 0.0f ? r : t * r;
+}
+
+// Scores of a token up to a common factor, 0 where not eligible: e^(z - top)
+// with top the maximum over all lanes, or sigmoid(z) (and its derivative in
+// slope).  Returns 1 / (their sum + eps); p_i is s[i] times that.
 template <int NL, int kScore>
-__device__ __forceinline__ float scores_of(const float (&z)[NL], float (&s)[NL], float& top, float& inv) {
+__device__ __forceinline__ float scores_of(const float (&z)[NL], float top, float (&s)[NL], float (&slope)[NL]) {
   float sum = 0.0f;
-  if (kScore == 0) {
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) top = fmaxf(top, z[i]);   // fmaxf ignores NaN
-    top = warp_max(top);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      s[i] = eligible(z[i]) ? expf(z[i] - top) : 0.0f;
-      sum += s[i];
-    }
-    inv = 1.0f / (warp_sum(sum) + kScoreEps);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) s[i] *= inv;
-    return 1.0f;
-  }
-  top = 0.0f;
-  inv = 1.0f;
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    s[i] = eligible(z[i]) ? sigmoid(z[i]) : 0.0f;
+    const float v = kScore == 0 ? fast_exp(z[i] - top) : fast_sigmoid(z[i], slope[i]);
+    s[i] = fmaxf(v, 0.0f);   // NaN logits (and -inf where all are) count as 0
     sum += s[i];
   }
-  return warp_sum(sum) + kScoreEps;
+  return fast_rcp(warp_sum(sum) + kScoreEps);
 }
-template <int kScore>
-__device__ __forceinline__ float score_of(float z, float top, float inv) {
-  if (!eligible(z)) return 0.0f;
-  return kScore == 0 ? expf(z - top) * inv : sigmoid(z);
+template <int NL>
+__device__ __forceinline__ float token_max(const float (&z)[NL]) {
+  float top = z[0];
+#pragma unroll
+  for (int i = 1; i < NL; ++i) top = fmaxf(top, z[i]);   // ignores NaN
+  return warp_max(top);
 }
 
 // The sequences of a launch: [seq[s], seq[s + 1]) covers 0 .. T in order.
@@ -139,20 +150,74 @@ __device__ __forceinline__ int sequence_of(const RouteArgs& a, int64_t t) {
 }
 __device__ __forceinline__ int64_t sequence_end(const RouteArgs& a, int s) { return a.seq == nullptr ? a.T : a.seq[s + 1]; }
 
+// Candidates for the k largest of a warp's keys key[i] (expert 32 i + lane;
+// -inf or NaN where not eligible), at least `slack` below the k-th largest
+// lane maximum: no key among the k largest is below that maximum, since k
+// lanes hold one that is not.  Of 256 random keys and k = 8 about nine pass,
+// so the exact order is worked out on one key per lane.  Leaves the
+// candidates' experts in `list` (lanes' first ones before their second ones)
+// and returns their number, which may be above 32 (ties, few lanes): only the
+// first 32 are in the list then.
+template <int NL>
+__device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool slack, int lane, uint16_t* list) {
+  float m = key[0];
+#pragma unroll
+  for (int i = 1; i < NL; ++i) m = fmaxf(m, key[i]);
+  uint32_t cur = eligible(m) ? order_key(m) : 0u;
+  uint32_t t = 0;
+  int seen = 0;
+  while (seen < k) {
+    t = __reduce_max_sync(kFull, cur);
+    if (t == 0u) break;       // fewer than k lanes hold an eligible key: all keys are candidates
+    const bool at = cur == t;
+    seen += __popc(__ballot_sync(kFull, at));
+    if (at) cur = 0u;
+  }
+  constexpr float kLowest = -3.402823466e38f;
+  float bound = t == 0u ? kLowest : __uint_as_float((t >> 31) != 0u ? t ^ 0x80000000u : ~t);
+  if (slack) bound = fmaxf(bound - (1e-5f + 1e-6f * fabsf(bound)), kLowest);
+  uint32_t mask = 0;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
+  int n = 0;
+  const uint32_t below = (1u << lane) - 1u;
+  uint32_t who = __ballot_sync(kFull, mask != 0u);
+  while (who != 0u) {
+    const int at = n + __popc(who & below);
+    if (mask != 0u && at < 32) list[at] = static_cast<uint16_t>(32 * (__ffs(mask) - 1) + lane);
+    mask &= mask - 1u;
+    n += __popc(who);
+    who = __ballot_sync(kFull, mask != 0u);
+  }
+  __syncwarp();
+  return n;
+}
+
+// CTAs that an SM should hold, which bounds the registers of a thread.
+template <int NL>
+constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? 2 : 1;
+
 // CTA c routes tokens [c * chunk, (c + 1) * chunk).  With statistics, each
 // stretch of one sequence inside the chunk leaves its sums in row c + s of
 // the partial arrays: along the tokens every step from one (chunk, sequence)
 // to the next raises c or s, so the rows are distinct.
+//
+// Bound by instructions: see ROUTE_NOTE
 template <int NL, int kScore, bool kStats>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_kernel(const RouteArgs a) {
   __shared__ float s_p[kStats ? kRouteWarps * 32 * NL : 1];
   __shared__ int s_n[kStats ? 32 * NL : 1];
   __shared__ int s_t[kRouteWarps];
+  __shared__ uint16_t s_list[kRouteWarps][32];
+  __shared__ uint64_t s_order[kRouteWarps][32];
+  griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (kStats) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     if (!sequences_ok(a)) return;
   }
+  const bool biased = kScore == 1 && a.bias != nullptr;
   const int64_t hi = min(a.T, static_cast<int64_t>(blockIdx.x + 1) * a.chunk);
   int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
   int s = kStats && lo < hi ? sequence_of(a, lo) : 0;
@@ -167,53 +232,102 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
       __syncthreads();
     }
     for (int64_t t = lo + warp; t < end; t += kRouteWarps) {
+      int32_t* idx = a.idx + t * a.k;
+      float* wt = a.w + t * a.k;
+      if (a.valid != nullptr && a.valid[t] == 0) {
+        if (lane < a.k) {
+          idx[lane] = -1;
+          wt[lane] = 0.0f;
+        }
+        continue;
+      }
       float z[NL], sc[NL];
-      load_token<NL>(a, t, lane, a.valid == nullptr || a.valid[t] != 0, z);
-      float top = 0.0f, inv = 1.0f, all = 1.0f;
-      if (kScore == 0 || kStats || a.bias != nullptr) all = scores_of<NL, kScore>(z, sc, top, inv);
-      uint32_t key[NL];
+      load_token<NL>(a, t, lane, z);
+      // scores of all experts: for the statistics, for softmax weights that are
+      // not normalised over the chosen, and (approximate) for biased keys
+      float top = 0.0f, inv = 1.0f;
+      const bool all = kStats || biased || (kScore == 0 && !a.normalize);
+      if (all) {
+        float slope[NL];
+        if (kScore == 0) top = token_max(z);
+        inv = scores_of<NL, kScore>(z, top, sc, slope);
+      }
+      int n;
+      if (biased) {
+        float key[NL];
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int e = 32 * i + lane;
-        float v = z[i];
-        if (kScore == 1 && a.bias != nullptr && e < a.E) v = sc[i] + __ldg(a.bias + e);
-        key[i] = eligible(z[i]) ? order_key(v) : 0u;
+        for (int i = 0; i < NL; ++i)   // z * 0 is NaN for the infinities and NaN: not eligible
+          key[i] = fmaf(z[i], 0.0f, sc[i] + (32 * i + lane < a.E ? __ldg(a.bias + 32 * i + lane) : 0.0f));
+        n = candidates<NL>(key, a.k, true, lane, s_list[warp]);
+      } else {
+        n = candidates<NL>(z, a.k, false, lane, s_list[warp]);
       }
       if (kStats) {
-        bool any = false;
+        live_tokens += n > 0 ? 1 : 0;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) any |= key[i] != 0u;
-        live_tokens += __any_sync(kFull, any) ? 1 : 0;
-        const float r = 1.0f / all;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) acc[i] += sc[i] * r;
+        for (int i = 0; i < NL; ++i) acc[i] += sc[i] * inv;
       }
-      int mine = -1;
-      for (int j = 0; j < a.k; ++j) {
-        uint32_t m = key[0];
+      // one candidate per lane and its place among them; mine: its expert
+      int mine = -1, slot = lane;
+      float zm = -INFINITY, sm = 0.0f;   // its logit, its score (softmax: below)
+      if (n <= 32) {
+        uint64_t order = 0;
+        if (lane < n) {
+          mine = s_list[warp][lane];
+          zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
+          if (kScore == 1) sm = sigmoid(zm);
+          const uint32_t key = order_key(biased ? sm + __ldg(a.bias + mine) : zm);
+          order = static_cast<uint64_t>(key) << 32 | (0xffffffffu - static_cast<uint32_t>(mine));
+          slot = 0;
+        }
+        s_order[warp][lane] = order;
+        __syncwarp();
+        for (int o = 0; o < n; ++o) slot += s_order[warp][o] > order ? 1 : 0;
+        if (lane >= n) slot = lane;
+      } else {
+        // too many: the k largest one by one; lane j keeps the j-th
+        uint32_t key[NL];
 #pragma unroll
-        for (int i = 1; i < NL; ++i) m = max(m, key[i]);
-        m = __reduce_max_sync(kFull, m);
-        if (m == 0u) break;   // no eligible expert is left
-        uint32_t cand = 0xffffffffu;
+        for (int i = 0; i < NL; ++i) {
+          float v = z[i];
+          if (biased && eligible(v)) v = sigmoid(v) + __ldg(a.bias + 32 * i + lane);
+          key[i] = eligible(z[i]) ? order_key(v) : 0u;
+        }
+        for (int j = 0; j < a.k; ++j) {
+          uint32_t m = key[0];
 #pragma unroll
-        for (int i = NL - 1; i >= 0; --i)
-          if (key[i] == m) cand = 32u * i + lane;
-        const uint32_t e = __reduce_min_sync(kFull, cand);
+          for (int i = 1; i < NL; ++i) m = max(m, key[i]);
+          m = __reduce_max_sync(kFull, m);   // never 0: more than 32 are eligible, and k <= 32
+          uint32_t cand = 0xffffffffu;
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-          if (e == 32u * i + lane) key[i] = 0u;
-        if (lane == j) mine = static_cast<int>(e);
+          for (int i = NL - 1; i >= 0; --i)
+            if (key[i] == m) cand = 32u * i + lane;
+          const uint32_t e = __reduce_min_sync(kFull, cand);
+#pragma unroll
+          for (int i = 0; i < NL; ++i)
+            if (e == 32u * i + lane) key[i] = 0u;
+          if (lane == j) mine = static_cast<int>(e);
+        }
+        if (lane < a.k) {
+          zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
+          if (kScore == 1) sm = sigmoid(zm);
+        }
       }
-      float ws = 0.0f;
-      if (mine >= 0) ws = score_of<kScore>(load_logit(a.logits, a.bf16, t * a.ld + mine), top, inv);
-      float w = ws;
-      if (a.normalize) w = ws / (warp_sum(ws) + kScoreEps);
-      if (lane < a.k) {
-        a.idx[t * a.k + lane] = mine;
-        a.w[t * a.k + lane] = w * a.scale;
+      if (slot >= a.k) mine = -1;
+      // normalised softmax weights need no sum over the experts not chosen
+      if (kScore == 0) {
+        if (!all) top = warp_max(mine >= 0 ? zm : -INFINITY);
+        sm = expf(zm - top);
+        if (!a.normalize) sm *= inv;
+      }
+      float w = mine >= 0 ? sm : 0.0f;
+      if (a.normalize) w *= fast_rcp(warp_sum(w) + kScoreEps);
+      if (slot < a.k) {
+        idx[slot] = mine;
+        wt[slot] = w * a.scale;
         if (kStats && mine >= 0) atomicAdd(&s_n[mine], 1);
       }
+      __syncwarp();   // the lists are read before the next token's go in
     }
     if (kStats) {
 #pragma unroll
@@ -251,6 +365,8 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
   __shared__ int s_n[32][33];
   __shared__ int s_t[32];
   __shared__ bool s_last;
+  griddep_launch_dependents();
+  griddep_wait();
   if (!sequences_ok(a)) return;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int s = blockIdx.y, e = blockIdx.x * 32 + lane;
@@ -307,79 +423,86 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
 }
 
 // d logits from the gradients of the gate weights and of the balance loss.
+// With g_i = d loss / d p_i (the sequence's constants) and d_j the gradients
+// of the chosen scores,
+//   softmax: dz_i = p_i (g_i + d_i - sum_l p_l (g_l + d_l))
+//   sigmoid: dz_i = s_i (1 - s_i) (d_i + (g_i - sum_l p_l g_l) / sum_l s_l).
+// Every lane first stores its experts' dz without d_i; the lanes that hold the
+// token's choices then store theirs whole over those k.
 template <int NL, int kScore>
-__global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const RouteArgs a) {
-  __shared__ float s_d[kRouteWarps][32 * NL];
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_backward_kernel(const RouteArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (!sequences_ok(a)) return;
-#pragma unroll
-  for (int i = 0; i < NL; ++i) s_d[warp][32 * i + lane] = 0.0f;
-  __syncwarp();
   const int64_t hi = min(a.T, static_cast<int64_t>(blockIdx.x + 1) * a.chunk);
   int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
   int s = lo < hi ? sequence_of(a, lo) : 0;
   const float up = a.dloss == nullptr ? 0.0f
                                       : __ldg(a.dloss) * (a.alpha / static_cast<float>(a.S)) *
                                             (static_cast<float>(a.E) / static_cast<float>(a.k));
+  auto store = [&](int64_t at, float v) {
+    if (a.bf16)
+      static_cast<__nv_bfloat16*>(a.dlogits)[at] = __float2bfloat16_rn(v);
+    else
+      static_cast<float*>(a.dlogits)[at] = v;
+  };
   while (lo < hi) {
     const int64_t end = min(hi, sequence_end(a, s));
-    float coef[NL];   // d loss / d p of this sequence
-    const float per = 1.0f / static_cast<float>(a.tokens != nullptr ? max(a.tokens[s], 1) : 1);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int e = 32 * i + lane;
-      coef[i] = a.dloss != nullptr && e < a.E
-                    ? static_cast<float>(a.counts[static_cast<int64_t>(s) * a.E + e]) * per * per * up
-                    : 0.0f;
+    const int32_t* counts = a.dloss == nullptr ? nullptr : a.counts + static_cast<int64_t>(s) * a.E;
+    float unit = 0.0f;   // g_i per count
+    if (counts != nullptr) {
+      const float per = 1.0f / static_cast<float>(max(a.tokens[s], 1));
+      unit = up * per * per;
     }
+    float coef[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      coef[i] = counts != nullptr && 32 * i + lane < a.E ? static_cast<float>(counts[32 * i + lane]) * unit : 0.0f;
     for (int64_t t = lo + warp; t < end; t += kRouteWarps) {
-      float z[NL], sc[NL];
-      load_token<NL>(a, t, lane, a.valid == nullptr || a.valid[t] != 0, z);
-      float top, inv;
-      const float all = scores_of<NL, kScore>(z, sc, top, inv);
+      if (a.valid != nullptr && a.valid[t] == 0) {
+        for (int e = lane; e < a.E; e += 32) store(t * a.ldd + e, 0.0f);
+        continue;
+      }
+      float z[NL], sc[NL], slope[NL];
       int mine = -1;
-      float ws = 0.0f, dw = 0.0f;
+      float dw = 0.0f, zm = -INFINITY;
       if (lane < a.k) {
         const int e = a.idx[t * a.k + lane];
         if (e >= 0 && e < a.E) {
           mine = e;
           dw = a.dw[t * a.k + lane];
-          ws = score_of<kScore>(load_logit(a.logits, a.bf16, t * a.ld + e), top, inv);
         }
       }
+      load_token<NL>(a, t, lane, z);
+      if (mine >= 0) zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
+      const float top = kScore == 0 ? token_max(z) : 0.0f;
+      const float inv = scores_of<NL, kScore>(z, top, sc, slope);
+      float ws = 0.0f, slope_m = 0.0f;
+      if (eligible(zm)) ws = kScore == 0 ? fast_exp(zm - top) * inv : fast_sigmoid(zm, slope_m);
       float dws = a.scale * dw;
       if (a.normalize) {
-        const float r = 1.0f / (warp_sum(ws) + kScoreEps);
-        const float mean = warp_sum(dw * ws) * r;
-        dws = a.scale * r * (dw - mean);
+        const float r = fast_rcp(warp_sum(ws) + kScoreEps);
+        dws = a.scale * r * (dw - warp_sum(dw * ws) * r);
       }
-      if (mine >= 0) s_d[warp][mine] = dws;
-      __syncwarp();
-      float u[NL];
       float dot = 0.0f;
-      const float r = 1.0f / all;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const float d = s_d[warp][32 * i + lane];
-        u[i] = kScore == 0 ? d + coef[i] : d;
-        dot += (kScore == 0 ? u[i] : coef[i]) * sc[i] * r;
-      }
+      for (int i = 0; i < NL; ++i) dot += coef[i] * sc[i];
+      dot *= inv;
+      if (kScore == 0) dot += dws * ws;
       dot = warp_sum(dot);
-      __syncwarp();
-      if (mine >= 0) s_d[warp][mine] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int e = 32 * i + lane;
-        float dz = kScore == 0 ? sc[i] * (u[i] - dot) : (u[i] + (coef[i] - dot) * r) * sc[i] * (1.0f - sc[i]);
-        if (!eligible(z[i])) dz = 0.0f;
-        if (e < a.E) {
-          if (a.bf16)
-            static_cast<__nv_bfloat16*>(a.dlogits)[t * a.ldd + e] = __float2bfloat16_rn(dz);
-          else
-            static_cast<float*>(a.dlogits)[t * a.ldd + e] = dz;
-        }
+        float dz = kScore == 0 ? sc[i] * inv * (coef[i] - dot) : (coef[i] - dot) * inv * slope[i];
+        dz = eligible(z[i]) ? dz : 0.0f;
+        if (32 * i + lane < a.E) store(t * a.ldd + 32 * i + lane, dz);
       }
-      __syncwarp();
+      __syncwarp();   // orders the stores of one address
+      if (mine >= 0) {
+        const float g = counts != nullptr ? static_cast<float>(__ldg(counts + mine)) * unit : 0.0f;
+        const float dz = kScore == 0 ? ws * (g + dws - dot) : (dws + (g - dot) * inv) * slope_m;
+        store(t * a.ldd + mine, eligible(zm) ? dz : 0.0f);
+      }
     }
     lo = end;
     while (lo < hi && sequence_end(a, s) <= lo) ++s;
@@ -388,10 +511,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
 
 // ------------------------------------------------------------------ layout
 // A counting sort of the T k choices by expert, stable in token order.  The
-// choices are cut into chunks of one CTA each; layout_count leaves each
-// chunk's histogram, layout_place adds up the histograms before its own and
-// places its choices: each warp ranks its stretch (equal experts of 32
-// choices found with match_any), the warps' counts are summed in order.
+// choices are cut into chunks of one CTA each: layout_count leaves the chunks'
+// histograms, expert by expert; layout_scan, a warp per expert, turns each
+// expert's into the sum of the chunks before; layout_place ranks a chunk's
+// choices (each warp its stretch, equal experts among 32 choices found with
+// match_any, the warps' counts summed in order) and writes them.  One chunk
+// needs the last alone.
 constexpr int kLayoutThreads = 512;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kMaxExperts = 1024;
@@ -400,22 +525,54 @@ constexpr int kMaxLayoutChunks = 512;
 
 __global__ void __launch_bounds__(kLayoutThreads) layout_count_kernel(const LayoutArgs a) {
   __shared__ int s_n[kMaxExperts];
+  griddep_launch_dependents();
   for (int e = threadIdx.x; e < a.E; e += kLayoutThreads) s_n[e] = 0;
   __syncthreads();
+  griddep_wait();
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(a.pairs, lo + a.chunk);
   for (int64_t i = lo + threadIdx.x; i < hi; i += kLayoutThreads) {
     const int e = a.idx[i];
     if (e >= 0 && e < a.E) atomicAdd(&s_n[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kLayoutThreads) a.hist[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_n[e];
+  for (int e = threadIdx.x; e < a.E; e += kLayoutThreads)
+    a.hist[static_cast<int64_t>(e) * (gridDim.x + 1) + blockIdx.x] = s_n[e];
+}
+
+// hist[e][0 .. chunks): exclusive sums; hist[e][chunks]: the total.
+__global__ void __launch_bounds__(32) layout_scan_kernel(const LayoutArgs a, int chunks) {
+  griddep_launch_dependents();
+  griddep_wait();
+  int* h = a.hist + static_cast<int64_t>(blockIdx.x) * (chunks + 1);
+  const int lane = threadIdx.x;
+  constexpr int kPer = kMaxLayoutChunks / 32;
+  int v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = 32 * i + lane < chunks ? h[32 * i + lane] : 0;
+  int run = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (32 * i < chunks) {
+      int x = v[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      if (32 * i + lane < chunks) h[32 * i + lane] = run + x - v[i];
+      run += __shfl_sync(kFull, x, 31);
+    }
+  }
+  if (lane == 0) h[chunks] = run;
 }
 
 __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const LayoutArgs a) {
   __shared__ uint16_t s_w[kLayoutWarps][kMaxExperts];   // counts of a warp, then of the warps before it
   __shared__ int s_base[kMaxExperts];                   // first row of this chunk's choices
-  __shared__ int s_total[kMaxExperts + 1];              // choices of an expert, then first rows
+  __shared__ int s_total[kMaxExperts];                  // choices of an expert
   __shared__ int s_scan[kLayoutWarps];
+  griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = gridDim.x;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
@@ -434,22 +591,15 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kLayoutThreads) {
-    int before = 0, total = 0;
-    if (chunks > 1) {
-      for (int c = 0; c < chunks; ++c) {
-        const int n = a.hist[static_cast<int64_t>(c) * a.E + e];
-        before += c < static_cast<int>(blockIdx.x) ? n : 0;
-        total += n;
-      }
-    }
     int run = 0;
     for (int w = 0; w < kLayoutWarps; ++w) {
       const int n = s_w[w][e];
       s_w[w][e] = static_cast<uint16_t>(run);
       run += n;
     }
-    s_base[e] = before;
-    s_total[e] = chunks > 1 ? total : run;
+    const int* h = a.hist + static_cast<int64_t>(e) * (chunks + 1);
+    s_base[e] = chunks > 1 ? h[blockIdx.x] : 0;
+    s_total[e] = chunks > 1 ? h[chunks] : run;
   }
   __syncthreads();
   // first rows: exclusive sum of the padded counts, two experts per thread
@@ -502,26 +652,35 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
   }
 }
 
+// Launches with programmatic stream serialisation: the kernel may be set up
+// while the one before it on the stream ends; it waits for it (griddep_wait)
+// before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int NL>
 cudaError_t run_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, (a.T + a.chunk - 1) / a.chunk));
-  if (backward) {
-    if (a.score == 0)
-      route_backward_kernel<NL, 0><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
-      route_backward_kernel<NL, 1><<<grid, kRouteThreads, 0, stream>>>(a);
-  } else if (a.loss != nullptr) {
-    if (a.score == 0)
-      route_kernel<NL, 0, true><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
-      route_kernel<NL, 1, true><<<grid, kRouteThreads, 0, stream>>>(a);
-  } else {
-    if (a.score == 0)
-      route_kernel<NL, 0, false><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
-      route_kernel<NL, 1, false><<<grid, kRouteThreads, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+  if (backward)
+    return a.score == 0 ? launch_behind(route_backward_kernel<NL, 0>, grid, kRouteThreads, stream, a)
+                        : launch_behind(route_backward_kernel<NL, 1>, grid, kRouteThreads, stream, a);
+  if (a.loss != nullptr)
+    return a.score == 0 ? launch_behind(route_kernel<NL, 0, true>, grid, kRouteThreads, stream, a)
+                        : launch_behind(route_kernel<NL, 1, true>, grid, kRouteThreads, stream, a);
+  return a.score == 0 ? launch_behind(route_kernel<NL, 0, false>, grid, kRouteThreads, stream, a)
+                      : launch_behind(route_kernel<NL, 1, false>, grid, kRouteThreads, stream, a);
 }
 
 cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
@@ -533,8 +692,11 @@ cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
   return run_route<32>(a, backward, stream);
 }
 
+// Tokens per CTA: at most 608 CTAs, and at most 24 + T / 64 (the partial sums
+// stay small beside the logits).
 int64_t route_chunk(int64_t T) {
-  const int64_t c = (T + kMaxChunks - 1) / kMaxChunks;
+  const int64_t chunks = std::min<int64_t>(kMaxChunks, 24 + T / 64);
+  const int64_t c = (T + chunks - 1) / chunks;
   return std::max<int64_t>(kRouteWarps, (c + kRouteWarps - 1) / kRouteWarps * kRouteWarps);
 }
 
@@ -563,8 +725,7 @@ cudaError_t launch_route(RouteArgs a, void* ws, cudaStream_t stream) {
   a.done = reinterpret_cast<int32_t*>(a.share + static_cast<int64_t>(slices) * a.S);
   const cudaError_t e = pick_route(a, false, stream);
   if (e != cudaSuccess) return e;
-  route_finish_kernel<<<dim3(slices, static_cast<unsigned>(a.S)), kFinishThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_behind(route_finish_kernel, dim3(slices, static_cast<unsigned>(a.S)), kFinishThreads, stream, a);
 }
 
 cudaError_t launch_route_backward(RouteArgs a, cudaStream_t stream) {
@@ -575,19 +736,19 @@ cudaError_t launch_route_backward(RouteArgs a, cudaStream_t stream) {
 int64_t layout_workspace_bytes(int64_t T, int k, int E) {
   const int64_t pairs = T * k, chunk = layout_chunk(pairs);
   const int64_t chunks = (pairs + chunk - 1) / chunk;
-  return chunks > 1 ? 4 * chunks * E : 4;
+  return chunks > 1 ? 4 * (chunks + 1) * E : 4;
 }
 
 cudaError_t launch_layout(LayoutArgs a, cudaStream_t stream) {
   a.chunk = layout_chunk(a.pairs);
   const unsigned chunks = static_cast<unsigned>(std::max<int64_t>(1, (a.pairs + a.chunk - 1) / a.chunk));
   if (chunks > 1) {
-    layout_count_kernel<<<chunks, kLayoutThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_behind(layout_count_kernel, chunks, kLayoutThreads, stream, a);
+    if (e != cudaSuccess) return e;
+    e = launch_behind(layout_scan_kernel, static_cast<unsigned>(a.E), 32, stream, a, static_cast<int>(chunks));
     if (e != cudaSuccess) return e;
   }
-  layout_place_kernel<<<chunks, kLayoutThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_behind(layout_place_kernel, chunks, kLayoutThreads, stream, a);
 }
 
 cudaError_t route_take_status(int* status) {
