@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace fp8bs {
 namespace {
@@ -650,24 +651,6 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
     if (i < whi) a.row_of[i] = row;
     if (ok) a.row_token[row] = static_cast<int32_t>(i / a.k);
   }
-}
-
-// Launches with programmatic stream serialisation: the kernel may be set up
-// while the one before it on the stream ends; it waits for it (griddep_wait)
-// before it touches memory.
-template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream, const A&... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int NL>
