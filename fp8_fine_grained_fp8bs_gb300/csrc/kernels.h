@@ -134,7 +134,7 @@ struct RouteArgs {
 };
 int64_t route_workspace_bytes(int64_t T, int E, int64_t S);
 cudaError_t launch_route(RouteArgs args, void* ws, cudaStream_t stream);
-cudaError_t launch_route_backward(RouteArgs args, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteArgs& args, cudaStream_t stream);
 // Reads and clears the router's device status word (invalid sequences).
 cudaError_t route_take_status(int* status);
 
@@ -146,11 +146,10 @@ struct LayoutArgs {
   int32_t* row_token;      // [rows]
   int64_t rows;
   int32_t* row_of;         // [pairs]
-  int32_t* hist;           // workspace, more than one chunk
-  int64_t chunk;           // set by the launcher
+  int32_t* hist;           // workspace
 };
 int64_t layout_workspace_bytes(int64_t T, int k, int E);
-cudaError_t launch_layout(LayoutArgs args, cudaStream_t stream);
+cudaError_t launch_layout(const LayoutArgs& args, cudaStream_t stream);
 
 // ---- moe.cu (row movement of the MoE dispatch and combine; no waits)
 cudaError_t launch_gather_q_rows(const uint8_t* q, const float* s, int64_t rows_in, int64_t H, bool s_in_kb_major,

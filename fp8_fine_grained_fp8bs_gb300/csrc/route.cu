@@ -15,11 +15,12 @@
 // eligible expert.  f is a count and has no gradient:
 //   d loss / d p_i = alpha / S * f_i / T_s.
 //
-// One warp per token: expert e is held by lane e % 32 in register e / 32, so
-// a lane sees the same experts in every token, and the sums of p over a
-// warp's tokens stay in registers.  Sums over tokens are taken in a fixed
-// order (lane, warp, chunk of tokens), counts with integer additions, so
-// results do not vary from run to run.
+// A token takes a group of W lanes: half a warp, or a whole one for more than
+// 256 experts or 16 choices.  Expert e is held by lane e % W of the group in
+// register e / W, so a lane sees the same experts in every token, and the sums
+// of p over a group's tokens stay in registers.  Sums over tokens are taken in
+// a fixed order (lane, group, chunk of tokens), counts with integer additions,
+// so results do not vary from run to run.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,20 +39,44 @@ __device__ __forceinline__ void record_route_status(int code) { atomicCAS(&g_rou
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kMaxChunks = 608;        // chunks of tokens: four CTAs on each of 152 SMs
 constexpr float kScoreEps = 1e-20f;    // guards the sums that scores are divided by
+constexpr float kLowest = -3.402823466e38f;
 constexpr uint32_t kFull = 0xffffffffu;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Reductions over the W lanes of a group; all lanes of the warp take part.
+template <int W>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int W>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (W == 32) {
+    return __reduce_max_sync(kFull, v);
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+    for (int o = W / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
 }
+template <int W>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  if constexpr (W == 32) {
+    return __reduce_min_sync(kFull, v);
+  } else {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
+}
+// The group's votes in the low W bits.
+template <int W>
+__device__ __forceinline__ uint32_t group_ballot(bool p, int lane) {
+  const uint32_t b = __ballot_sync(kFull, p);
+  return W == 32 ? b : (b >> (lane & ~(W - 1))) & ((1u << (W & 31)) - 1u);
+}
+__device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
 
 __device__ __forceinline__ float load_logit(const void* logits, bool bf16, int64_t at) {
   if (bf16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(logits) + at)) << 16);
@@ -69,19 +94,28 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ ((b >> 31) != 0u ? 0xffffffffu : 0x80000000u);
 }
 
-// One token's logits in registers: z[i] is expert 32 i + lane, -inf past E.
-template <int NL>
-__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int lane, float (&z)[NL]) {
+__device__ __forceinline__ float from_key(uint32_t k) { return __uint_as_float((k >> 31) != 0u ? k ^ 0x80000000u : ~k); }
+
+// One token's logits in registers: z[i] is expert W i + g, -inf from expert
+// `end` on (E, or 0 for a token that is not there or masked).
+// The bits of all loads arrive before any is widened: converted one by one,
+// BF16 logits waited for each load in turn (backward 131072 x 256: 103 us
+// against 58 for float32).
+template <int W, int NL>
+__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int g, int end, float (&z)[NL]) {
+  uint32_t bits[NL];
   if (a.bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + lane;
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + g;
 #pragma unroll
-    for (int i = 0; i < NL; ++i)
-      z[i] = 32 * i + lane < a.E ? __uint_as_float(static_cast<uint32_t>(__ldg(p + 32 * i)) << 16) : -INFINITY;
+    for (int i = 0; i < NL; ++i) bits[i] = W * i + g < end ? __ldg(p + W * i) : 0xFF80u;
   } else {
-    const float* p = static_cast<const float*>(a.logits) + t * a.ld + lane;
+    const uint32_t* p = static_cast<const uint32_t*>(a.logits) + t * a.ld + g;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) z[i] = 32 * i + lane < a.E ? __ldg(p + 32 * i) : -INFINITY;
+    for (int i = 0; i < NL; ++i) bits[i] = W * i + g < end ? __ldg(p + W * i) : 0xFF800000u;
   }
+  const uint32_t shift = a.bf16 ? 16 : 0;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) z[i] = __uint_as_float(bits[i] << shift);
 }
 
 // e^x and 1 / x by the hardware's base-2 exponential and reciprocal, for the
@@ -97,33 +131,11 @@ __device__ __forceinline__ float fast_rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// sigmoid(z) and its derivative from t = e^-|z|, which cannot overflow.
-__device__ __forceinline__ float fast_sigmoid(float z, float& slope) {
-  const float t = fast_exp(-fabsf(z)), r = fast_rcp(1.0f + t);
-  slope = t * r * r;
-  return z >= 0.0f ? r : t * r;
-}
-
-// Scores of a token up to a common factor, 0 where not eligible: e^(z - top)
-// with top the maximum over all lanes, or sigmoid(z) (and its derivative in
-// slope).  Returns 1 / (their sum + eps); p_i is s[i] times that.
-template <int NL, int kScore>
-__device__ __forceinline__ float scores_of(const float (&z)[NL], float top, float (&s)[NL], float (&slope)[NL]) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const float v = kScore == 0 ? fast_exp(z[i] - top) : fast_sigmoid(z[i], slope[i]);
-    s[i] = fmaxf(v, 0.0f);   // NaN logits (and -inf where all are) count as 0
-    sum += s[i];
-  }
-  return fast_rcp(warp_sum(sum) + kScoreEps);
-}
-template <int NL>
-__device__ __forceinline__ float token_max(const float (&z)[NL]) {
-  float top = z[0];
-#pragma unroll
-  for (int i = 1; i < NL; ++i) top = fmaxf(top, z[i]);   // ignores NaN
-  return warp_max(top);
+// sigmoid(z) is 1 - q or q, with q = e^-|z| / (1 + e^-|z|) <= 1/2, which cannot
+// overflow and loses nothing to cancellation; its derivative is q (1 - q).
+__device__ __forceinline__ float sigmoid_part(float z) {
+  const float t = fast_exp(-fabsf(z));
+  return t * fast_rcp(1.0f + t);
 }
 
 // The sequences of a launch: [seq[s], seq[s + 1]) covers 0 .. T in order.
@@ -151,44 +163,53 @@ __device__ __forceinline__ int sequence_of(const RouteArgs& a, int64_t t) {
 }
 __device__ __forceinline__ int64_t sequence_end(const RouteArgs& a, int s) { return a.seq == nullptr ? a.T : a.seq[s + 1]; }
 
-// Candidates for the k largest of a warp's keys key[i] (expert 32 i + lane;
-// -inf or NaN where not eligible), at least `slack` below the k-th largest
-// lane maximum: no key among the k largest is below that maximum, since k
-// lanes hold one that is not.  Of 256 random keys and k = 8 about nine pass,
-// so the exact order is worked out on one key per lane.  Leaves the
-// candidates' experts in `list` (lanes' first ones before their second ones)
-// and returns their number, which may be above 32 (ties, few lanes): only the
-// first 32 are in the list then.
-template <int NL>
-__device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool slack, int lane, uint16_t* list) {
+// The largest key of the group's keys key[i] (expert W i + g; -inf or NaN
+// where not eligible) in `most` (0: none is eligible), and candidates for the
+// k largest of them: all keys from a bound on that k lane maxima reach, less
+// `slack`.  No key among the k largest lies below such a bound.  It is found by
+// bisection on the lane maxima, to where k or k + 1 of them reach it; of 256
+// random keys and k = 8, eleven pass on average, so that the exact order is
+// worked out on one key per lane.  Leaves the candidates' experts in `list`
+// (lanes' first ones before their second ones) and returns their number, which
+// may be above 32 (ties, k near W): only the first 32 are in the list then.
+template <int W, int NL>
+__device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool slack, int lane, uint16_t* list,
+                                          uint32_t& most) {
   float m = key[0];
 #pragma unroll
   for (int i = 1; i < NL; ++i) m = fmaxf(m, key[i]);
-  uint32_t cur = eligible(m) ? order_key(m) : 0u;
-  uint32_t t = 0;
-  int seen = 0;
-  while (seen < k) {
-    t = __reduce_max_sync(kFull, cur);
-    if (t == 0u) break;       // fewer than k lanes hold an eligible key: all keys are candidates
-    const bool at = cur == t;
-    seen += __popc(__ballot_sync(kFull, at));
-    if (at) cur = 0u;
+  const uint32_t mine = eligible(m) ? order_key(m) : 0u;
+  most = group_max<W>(mine);
+  // at least k lanes reach `low`, fewer than k reach `high`
+  uint32_t low = group_min<W>(mine), high = most + 1u;
+  bool go = high - low > 1u;
+  while (__any_sync(kFull, go)) {
+    const uint32_t mid = low + (high - low) / 2u;
+    const int n = __popc(group_ballot<W>(mine >= mid, lane));
+    if (go) {
+      if (n >= k) {
+        low = mid;
+        go = n > k + 1;
+      } else {
+        high = mid;
+      }
+      go = go && high - low > 1u;
+    }
   }
-  constexpr float kLowest = -3.402823466e38f;
-  float bound = t == 0u ? kLowest : __uint_as_float((t >> 31) != 0u ? t ^ 0x80000000u : ~t);
+  float bound = low == 0u ? kLowest : from_key(low);   // 0: fewer than k lanes hold an eligible key
   if (slack) bound = fmaxf(bound - (1e-5f + 1e-6f * fabsf(bound)), kLowest);
   uint32_t mask = 0;
 #pragma unroll
   for (int i = 0; i < NL; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
   int n = 0;
-  const uint32_t below = (1u << lane) - 1u;
-  uint32_t who = __ballot_sync(kFull, mask != 0u);
-  while (who != 0u) {
+  const int g = lane & (W - 1);
+  const uint32_t below = (1u << g) - 1u;
+  while (__any_sync(kFull, mask != 0u)) {
+    const uint32_t who = group_ballot<W>(mask != 0u, lane);
     const int at = n + __popc(who & below);
-    if (mask != 0u && at < 32) list[at] = static_cast<uint16_t>(32 * (__ffs(mask) - 1) + lane);
+    if (mask != 0u && at < 32) list[at] = static_cast<uint16_t>(W * (__ffs(mask) - 1) + g);
     mask &= mask - 1u;
     n += __popc(who);
-    who = __ballot_sync(kFull, mask != 0u);
   }
   __syncwarp();
   return n;
@@ -196,24 +217,32 @@ __device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool sl
 
 // CTAs that an SM should hold, which bounds the registers of a thread.
 template <int NL>
-constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? 2 : 1;
+constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? 3 : 1;
 
 // CTA c routes tokens [c * chunk, (c + 1) * chunk).  With statistics, each
 // stretch of one sequence inside the chunk leaves its sums in row c + s of
 // the partial arrays: along the tokens every step from one (chunk, sequence)
 // to the next raises c or s, so the rows are distinct.
 //
-// Bound by instructions: see ROUTE_NOTE
-template <int NL, int kScore, bool kStats>
+// Bound by instructions (about 330 a token of 256 logits, 500 with statistics
+// and biased sigmoids, two thirds of the issue slots busy).  131072 tokens: 154
+// us choosing the k experts one by one from all keys, two warp reductions and a
+// pass over the keys each; 86 with candidates, a warp per token; 65 with half a
+// warp, which shares the per-token steps between two tokens (with statistics
+// 166, 108 and 85 us).
+template <int W, int NL, int kScore, bool kStats>
 __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_kernel(const RouteArgs a) {
-  __shared__ float s_p[kStats ? kRouteWarps * 32 * NL : 1];
-  __shared__ int s_n[kStats ? 32 * NL : 1];
+  constexpr int kGroups = kRouteThreads / W;          // tokens at a time
+  constexpr int kPerLane = 32 / W;                    // candidates of a lane
+  __shared__ float s_p[kStats ? kGroups * W * NL : 1];
+  __shared__ int s_n[kStats ? W * NL : 1];
   __shared__ int s_t[kRouteWarps];
-  __shared__ uint16_t s_list[kRouteWarps][32];
-  __shared__ uint64_t s_order[kRouteWarps][32];
+  __shared__ uint16_t s_list[kGroups][32];
+  __shared__ __align__(16) uint64_t s_order[kGroups][32];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = threadIdx.x / W, g = threadIdx.x & (W - 1);
   if (kStats) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     if (!sequences_ok(a)) return;
@@ -222,124 +251,172 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_kernel(co
   const int64_t hi = min(a.T, static_cast<int64_t>(blockIdx.x + 1) * a.chunk);
   int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
   int s = kStats && lo < hi ? sequence_of(a, lo) : 0;
+  uint16_t* list = s_list[group];
+  uint64_t* order = s_order[group];
   while (lo < hi) {
     const int64_t end = kStats ? min(hi, sequence_end(a, s)) : hi;
     float acc[NL];
-    int live_tokens = 0;
+    int live_tokens = 0;   // of the group
     if (kStats) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) acc[i] = 0.0f;
       for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_n[e] = 0;
       __syncthreads();
     }
-    for (int64_t t = lo + warp; t < end; t += kRouteWarps) {
-      int32_t* idx = a.idx + t * a.k;
-      float* wt = a.w + t * a.k;
-      if (a.valid != nullptr && a.valid[t] == 0) {
-        if (lane < a.k) {
-          idx[lane] = -1;
-          wt[lane] = 0.0f;
-        }
-        continue;
-      }
-      float z[NL], sc[NL];
-      load_token<NL>(a, t, lane, z);
-      // scores of all experts: for the statistics, for softmax weights that are
-      // not normalised over the chosen, and (approximate) for biased keys
-      float top = 0.0f, inv = 1.0f;
+    // warps walk the tokens together; a group without one stays empty.  The
+    // mask is read a step ahead, so that the logits' loads do not wait for it.
+    auto is_valid = [&](int64_t t) { return t < end && (a.valid == nullptr || a.valid[t] != 0); };
+    bool valid_next = is_valid(lo + threadIdx.x / W);
+    for (int64_t t0 = lo + warp * (32 / W); t0 < end; t0 += kGroups) {
+      const int64_t t = t0 + lane / W;
+      const bool here = t < end, valid = valid_next;
+      valid_next = is_valid(t + kGroups);
+      float v[NL];   // logits, then scores or keys
+      load_token<W, NL>(a, here ? t : lo, g, valid ? a.E : 0, v);
+      // Scores of all experts for the statistics, for softmax weights that are
+      // not normalised over the chosen, and (approximate) for biased keys.
       const bool all = kStats || biased || (kScore == 0 && !a.normalize);
+      float inv = 1.0f;
+      uint32_t most = 0;
+      int n = 0;
+      if (!biased) n = candidates<W, NL>(v, a.k, false, lane, list, most);
+      const float top = from_key(most);   // softmax; not used where most is 0
       if (all) {
-        float slope[NL];
-        if (kScore == 0) top = token_max(z);
-        inv = scores_of<NL, kScore>(z, top, sc, slope);
-      }
-      int n;
-      if (biased) {
-        float key[NL];
-#pragma unroll
-        for (int i = 0; i < NL; ++i)   // z * 0 is NaN for the infinities and NaN: not eligible
-          key[i] = fmaf(z[i], 0.0f, sc[i] + (32 * i + lane < a.E ? __ldg(a.bias + 32 * i + lane) : 0.0f));
-        n = candidates<NL>(key, a.k, true, lane, s_list[warp]);
-      } else {
-        n = candidates<NL>(z, a.k, false, lane, s_list[warp]);
-      }
-      if (kStats) {
-        live_tokens += n > 0 ? 1 : 0;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) acc[i] += sc[i] * inv;
-      }
-      // one candidate per lane and its place among them; mine: its expert
-      int mine = -1, slot = lane;
-      float zm = -INFINITY, sm = 0.0f;   // its logit, its score (softmax: below)
-      if (n <= 32) {
-        uint64_t order = 0;
-        if (lane < n) {
-          mine = s_list[warp][lane];
-          zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
-          if (kScore == 1) sm = sigmoid(zm);
-          const uint32_t key = order_key(biased ? sm + __ldg(a.bias + mine) : zm);
-          order = static_cast<uint64_t>(key) << 32 | (0xffffffffu - static_cast<uint32_t>(mine));
-          slot = 0;
-        }
-        s_order[warp][lane] = order;
-        __syncwarp();
-        for (int o = 0; o < n; ++o) slot += s_order[warp][o] > order ? 1 : 0;
-        if (lane >= n) slot = lane;
-      } else {
-        // too many: the k largest one by one; lane j keeps the j-th
-        uint32_t key[NL];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-          float v = z[i];
-          if (biased && eligible(v)) v = sigmoid(v) + __ldg(a.bias + 32 * i + lane);
-          key[i] = eligible(z[i]) ? order_key(v) : 0u;
+          if (kScore == 0) {
+            v[i] = fast_exp(v[i] - top);
+          } else {
+            // z * 0 is NaN for NaN and the infinities: not eligible
+            v[i] = fmaf(v[i], 0.0f, fast_rcp(1.0f + fast_exp(-v[i])));
+          }
+          sum += fmaxf(v[i], 0.0f);   // 0 for NaN
+        }
+        inv = fast_rcp(group_sum<W>(sum) + kScoreEps);
+        if (kStats) {
+#pragma unroll
+          for (int i = 0; i < NL; ++i) acc[i] = fmaf(fmaxf(v[i], 0.0f), inv, acc[i]);
+        }
+        if (kScore == 0 && most == 0u) inv = 1.0f;
+      }
+      if (biased) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          if (W * i + g < a.E) v[i] += __ldg(a.bias + W * i + g);
+        n = candidates<W, NL>(v, a.k, true, lane, list, most);
+      }
+      if (kStats) live_tokens += n > 0 ? 1 : 0;
+      // Candidates of this lane: expert, logit, score, and place among them all.
+      int mine[kPerLane], slot[kPerLane];
+      float zm[kPerLane], sm[kPerLane];
+      const bool two = kPerLane > 1 && __any_sync(kFull, n > W);
+#pragma unroll
+      for (int r = 0; r < kPerLane; ++r) {
+        mine[r] = -1;
+        slot[r] = a.k;
+        zm[r] = sm[r] = 0.0f;
+        if (r == 0 || two) {
+          const int c = W * r + g;
+          uint64_t key = 0;
+          if (c < n) {
+            mine[r] = list[c];
+            zm[r] = load_logit(a.logits, a.bf16, t * a.ld + mine[r]);
+            if (kScore == 1) sm[r] = sigmoid(zm[r]);
+            const uint32_t high = order_key(biased ? sm[r] + __ldg(a.bias + mine[r]) : zm[r]);
+            key = static_cast<uint64_t>(high) << 32 | (0xffffffffu - static_cast<uint32_t>(mine[r]));
+            slot[r] = 0;
+          }
+          order[c] = key;
+        }
+      }
+      __syncwarp();
+      const int most_n = two ? 32 : min(32, static_cast<int>(__reduce_max_sync(kFull, static_cast<uint32_t>(n))));
+      {
+        const uint64_t own0 = order[g], own1 = two ? order[W * (kPerLane - 1) + g] : 0;
+        int rank0 = 0, rank1 = 0;
+        for (int o = 0; o < most_n; o += 2) {   // the orders past n are 0, below every candidate's
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(order + o);
+          rank0 += (x.x > own0 ? 1 : 0) + (x.y > own0 ? 1 : 0);
+          if (two) rank1 += (x.x > own1 ? 1 : 0) + (x.y > own1 ? 1 : 0);
+        }
+        if (mine[0] >= 0) slot[0] = rank0;
+        if (kPerLane > 1 && mine[kPerLane - 1] >= 0 && two) slot[kPerLane - 1] = rank1;
+      }
+      if (__any_sync(kFull, n > 32)) {
+        // Too many for one group or both: the k largest one by one from the keys
+        // themselves; lane j keeps the j-th.
+        const bool many = n > 32;
+        uint32_t key[NL];
+        load_token<W, NL>(a, here ? t : lo, g, many ? a.E : 0, v);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          float x = v[i];
+          if (biased && eligible(x)) x = sigmoid(x) + __ldg(a.bias + W * i + g);
+          key[i] = eligible(v[i]) ? order_key(x) : 0u;
         }
         for (int j = 0; j < a.k; ++j) {
           uint32_t m = key[0];
 #pragma unroll
           for (int i = 1; i < NL; ++i) m = max(m, key[i]);
-          m = __reduce_max_sync(kFull, m);   // never 0: more than 32 are eligible, and k <= 32
+          m = group_max<W>(m);   // 0 only where not `many`: more than 32 are eligible, and k <= 32
           uint32_t cand = 0xffffffffu;
 #pragma unroll
           for (int i = NL - 1; i >= 0; --i)
-            if (key[i] == m) cand = 32u * i + lane;
-          const uint32_t e = __reduce_min_sync(kFull, cand);
+            if (key[i] == m) cand = static_cast<uint32_t>(W * i + g);
+          const uint32_t e = group_min<W>(cand);
 #pragma unroll
           for (int i = 0; i < NL; ++i)
-            if (e == 32u * i + lane) key[i] = 0u;
-          if (lane == j) mine = static_cast<int>(e);
+            if (e == static_cast<uint32_t>(W * i + g)) key[i] = 0u;
+          if (many && g == j) mine[0] = static_cast<int>(e);
         }
-        if (lane < a.k) {
-          zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
-          if (kScore == 1) sm = sigmoid(zm);
+        if (many) {
+          slot[0] = g;
+          if (kPerLane > 1) slot[kPerLane - 1] = a.k;
+          if (g < a.k) {
+            zm[0] = load_logit(a.logits, a.bf16, t * a.ld + mine[0]);
+            if (kScore == 1) sm[0] = sigmoid(zm[0]);
+          }
         }
       }
-      if (slot >= a.k) mine = -1;
       // normalised softmax weights need no sum over the experts not chosen
-      if (kScore == 0) {
-        if (!all) top = warp_max(mine >= 0 ? zm : -INFINITY);
-        sm = expf(zm - top);
-        if (!a.normalize) sm *= inv;
+      float chosen = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kPerLane; ++r) {
+        if (slot[r] < a.k) {
+          if (kScore == 0) sm[r] = expf(zm[r] - top) * (a.normalize ? 1.0f : inv);
+          chosen += sm[r];
+        }
       }
-      float w = mine >= 0 ? sm : 0.0f;
-      if (a.normalize) w *= fast_rcp(warp_sum(w) + kScoreEps);
-      if (slot < a.k) {
-        idx[slot] = mine;
-        wt[slot] = w * a.scale;
-        if (kStats && mine >= 0) atomicAdd(&s_n[mine], 1);
+      float unit = a.scale;
+      if (a.normalize) unit *= fast_rcp(group_sum<W>(chosen) + kScoreEps);
+      if (here) {
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+          if (slot[r] < a.k) {
+            a.idx[t * a.k + slot[r]] = mine[r];
+            a.w[t * a.k + slot[r]] = sm[r] * unit;
+            if (kStats) atomicAdd(&s_n[mine[r]], 1);
+          }
+        }
+        if (g >= n && g < a.k) {   // slots that find no eligible expert
+          a.idx[t * a.k + g] = -1;
+          a.w[t * a.k + g] = 0.0f;
+        }
       }
       __syncwarp();   // the lists are read before the next token's go in
     }
     if (kStats) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) s_p[warp * 32 * NL + 32 * i + lane] = acc[i];
+      for (int i = 0; i < NL; ++i) s_p[group * W * NL + W * i + g] = acc[i];
+      live_tokens = __reduce_add_sync(kFull, g == 0 ? live_tokens : 0);
       if (lane == 0) s_t[warp] = live_tokens;
       __syncthreads();
       const int64_t row = static_cast<int64_t>(blockIdx.x) + s;
       for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kRouteWarps; ++w) sum += s_p[w * 32 * NL + e];
+        for (int r = 0; r < kGroups; ++r) sum += s_p[r * W * NL + e];
         a.part_p[row * a.E + e] = sum;
         a.part_n[row * a.E + e] = s_n[e];
       }
@@ -430,11 +507,18 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
 //   sigmoid: dz_i = s_i (1 - s_i) (d_i + (g_i - sum_l p_l g_l) / sum_l s_l).
 // Every lane first stores its experts' dz without d_i; the lanes that hold the
 // token's choices then store theirs whole over those k.
-template <int NL, int kScore>
-__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_backward_kernel(const RouteArgs a) {
+// CTAs on an SM, more of them against more registers a thread: 131072 tokens of
+// 256 logits 62.5 us with four, 71.2 with three; of 128 logits (half a warp a
+// token) 43.1 and 38.5.
+template <int W, int NL>
+constexpr int kBackwardCtas = NL <= 4 ? 4 : NL == 8 ? (W == 32 ? 4 : 3) : NL == 16 ? 2 : 1;
+
+template <int W, int NL, int kScore>
+__global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_backward_kernel(const RouteArgs a) {
+  constexpr int kGroups = kRouteThreads / W;
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = threadIdx.x & (W - 1);
   if (!sequences_ok(a)) return;
   const int64_t hi = min(a.T, static_cast<int64_t>(blockIdx.x + 1) * a.chunk);
   int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
@@ -442,12 +526,6 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_backward_
   const float up = a.dloss == nullptr ? 0.0f
                                       : __ldg(a.dloss) * (a.alpha / static_cast<float>(a.S)) *
                                             (static_cast<float>(a.E) / static_cast<float>(a.k));
-  auto store = [&](int64_t at, float v) {
-    if (a.bf16)
-      static_cast<__nv_bfloat16*>(a.dlogits)[at] = __float2bfloat16_rn(v);
-    else
-      static_cast<float*>(a.dlogits)[at] = v;
-  };
   while (lo < hi) {
     const int64_t end = min(hi, sequence_end(a, s));
     const int32_t* counts = a.dloss == nullptr ? nullptr : a.counts + static_cast<int64_t>(s) * a.E;
@@ -456,53 +534,100 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_backward_
       const float per = 1.0f / static_cast<float>(max(a.tokens[s], 1));
       unit = up * per * per;
     }
-    float coef[NL];
+    float coef[NL];      // g_i
 #pragma unroll
     for (int i = 0; i < NL; ++i)
-      coef[i] = counts != nullptr && 32 * i + lane < a.E ? static_cast<float>(counts[32 * i + lane]) * unit : 0.0f;
-    for (int64_t t = lo + warp; t < end; t += kRouteWarps) {
-      if (a.valid != nullptr && a.valid[t] == 0) {
-        for (int e = lane; e < a.E; e += 32) store(t * a.ldd + e, 0.0f);
-        continue;
-      }
-      float z[NL], sc[NL], slope[NL];
-      int mine = -1;
-      float dw = 0.0f, zm = -INFINITY;
-      if (lane < a.k) {
-        const int e = a.idx[t * a.k + lane];
-        if (e >= 0 && e < a.E) {
-          mine = e;
-          dw = a.dw[t * a.k + lane];
-        }
-      }
-      load_token<NL>(a, t, lane, z);
+      coef[i] = counts != nullptr && W * i + g < a.E ? static_cast<float>(counts[W * i + g]) * unit : 0.0f;
+    // the mask, the choice and its gradient are read a step ahead, so that no
+    // load of a step waits for another
+    bool valid_next = false;
+    int mine_next = -1;
+    float dw_next = 0.0f;
+    auto ahead = [&](int64_t t) {
+      valid_next = t < end && (a.valid == nullptr || a.valid[t] != 0);
+      mine_next = t < end && g < a.k ? a.idx[t * a.k + g] : -1;
+      dw_next = t < end && g < a.k ? a.dw[t * a.k + g] : 0.0f;
+    };
+    ahead(lo + threadIdx.x / W);
+    for (int64_t t0 = lo + warp * (32 / W); t0 < end; t0 += kGroups) {
+      const int64_t t = t0 + lane / W;
+      const bool here = t < end, valid = valid_next;
+      const int mine = valid && mine_next >= 0 && mine_next < a.E ? mine_next : -1;
+      const float dw = mine >= 0 ? dw_next : 0.0f;
+      float zm = -INFINITY;
+      ahead(t + kGroups);
+      // softmax: v = e^(z - top), 0 where not eligible.  sigmoid: v = q (see
+      // sigmoid_part) with the logit's sign, -0 where not eligible.
+      float v[NL];
+      load_token<W, NL>(a, here ? t : lo, g, valid ? a.E : 0, v);
       if (mine >= 0) zm = load_logit(a.logits, a.bf16, t * a.ld + mine);
-      const float top = kScore == 0 ? token_max(z) : 0.0f;
-      const float inv = scores_of<NL, kScore>(z, top, sc, slope);
-      float ws = 0.0f, slope_m = 0.0f;
-      if (eligible(zm)) ws = kScore == 0 ? fast_exp(zm - top) * inv : fast_sigmoid(zm, slope_m);
-      float dws = a.scale * dw;
-      if (a.normalize) {
-        const float r = fast_rcp(warp_sum(ws) + kScoreEps);
-        dws = a.scale * r * (dw - warp_sum(dw * ws) * r);
-      }
-      float dot = 0.0f;
+      float top = 0.0f;
+      if (kScore == 0) {
+        top = v[0];
 #pragma unroll
-      for (int i = 0; i < NL; ++i) dot += coef[i] * sc[i];
-      dot *= inv;
-      if (kScore == 0) dot += dws * ws;
-      dot = warp_sum(dot);
+        for (int i = 1; i < NL; ++i) top = fmaxf(top, v[i]);   // ignores NaN
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      }
+      float sum = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        float dz = kScore == 0 ? sc[i] * inv * (coef[i] - dot) : (coef[i] - dot) * inv * slope[i];
-        dz = eligible(z[i]) ? dz : 0.0f;
-        if (32 * i + lane < a.E) store(t * a.ldd + 32 * i + lane, dz);
+        float score;
+        if (kScore == 0) {
+          v[i] = score = fmaxf(fast_exp(v[i] - top), 0.0f);
+        } else {
+          const float q = fmaxf(sigmoid_part(v[i]), 0.0f);
+          score = v[i] >= 0.0f ? 1.0f - q : q;
+          v[i] = v[i] >= 0.0f ? q : -q;
+        }
+        sum += score;
+        dot = fmaf(coef[i], score, dot);
+      }
+      const float inv = fast_rcp(group_sum<W>(sum) + kScoreEps);
+      float ws = 0.0f, slope = 0.0f;
+      if (eligible(zm)) {
+        if (kScore == 0) {
+          ws = fast_exp(zm - top) * inv;
+        } else {
+          const float q = sigmoid_part(zm);
+          ws = zm >= 0.0f ? 1.0f - q : q;
+          slope = q * (1.0f - q);
+        }
+      }
+      float dws = a.scale * dw;
+      if (a.normalize) {
+        const float r = fast_rcp(group_sum<W>(ws) + kScoreEps);
+        dws = a.scale * r * (dw - group_sum<W>(dw * ws) * r);
+      }
+      dot *= inv;
+      if (kScore == 0) dot = fmaf(dws, ws, dot);
+      dot = group_sum<W>(dot);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const float q = fabsf(v[i]);
+        v[i] = (coef[i] - dot) * inv * (kScore == 0 ? q : q * (1.0f - q));
+      }
+      if (here) {
+        if (a.bf16) {
+          __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.dlogits) + t * a.ldd + g;
+#pragma unroll
+          for (int i = 0; i < NL; ++i)
+            if (W * i + g < a.E) row[W * i] = __float2bfloat16_rn(v[i]);
+        } else {
+          float* row = static_cast<float*>(a.dlogits) + t * a.ldd + g;
+#pragma unroll
+          for (int i = 0; i < NL; ++i)
+            if (W * i + g < a.E) row[W * i] = v[i];
+        }
       }
       __syncwarp();   // orders the stores of one address
       if (mine >= 0) {
-        const float g = counts != nullptr ? static_cast<float>(__ldg(counts + mine)) * unit : 0.0f;
-        const float dz = kScore == 0 ? ws * (g + dws - dot) : (dws + (g - dot) * inv) * slope_m;
-        store(t * a.ldd + mine, eligible(zm) ? dz : 0.0f);
+        const float gm = counts != nullptr ? static_cast<float>(__ldg(counts + mine)) * unit : 0.0f;
+        const float dz = kScore == 0 ? ws * (gm + dws - dot) : (dws + (gm - dot) * inv) * slope;
+        if (a.bf16)
+          static_cast<__nv_bfloat16*>(a.dlogits)[t * a.ldd + mine] = __float2bfloat16_rn(dz);
+        else
+          static_cast<float*>(a.dlogits)[t * a.ldd + mine] = dz;
       }
     }
     lo = end;
@@ -512,17 +637,17 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_backward_
 
 // ------------------------------------------------------------------ layout
 // A counting sort of the T k choices by expert, stable in token order.  The
-// choices are cut into chunks of one CTA each: layout_count leaves the chunks'
-// histograms, expert by expert; layout_scan, a warp per expert, turns each
-// expert's into the sum of the chunks before; layout_place ranks a chunk's
+// choices are cut into chunks of 2048, one CTA each: layout_count leaves the
+// chunks' histograms, expert by expert; layout_scan, a warp per expert, turns
+// each expert's into the sum of the chunks before; layout_place ranks a chunk's
 // choices (each warp its stretch, equal experts among 32 choices found with
 // match_any, the warps' counts summed in order) and writes them.  One chunk
 // needs the last alone.
 constexpr int kLayoutThreads = 512;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kMaxExperts = 1024;
-constexpr int kChunkPairs = 2048;           // smallest chunk
-constexpr int kMaxLayoutChunks = 512;
+constexpr int kChunkPairs = 2048;
+constexpr int kWarpSteps = kChunkPairs / kLayoutThreads;   // choices of a lane
 
 __global__ void __launch_bounds__(kLayoutThreads) layout_count_kernel(const LayoutArgs a) {
   __shared__ int s_n[kMaxExperts];
@@ -530,9 +655,11 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_count_kernel(const Layo
   for (int e = threadIdx.x; e < a.E; e += kLayoutThreads) s_n[e] = 0;
   __syncthreads();
   griddep_wait();
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk, hi = min(a.pairs, lo + a.chunk);
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kLayoutThreads) {
-    const int e = a.idx[i];
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kChunkPairs;
+#pragma unroll
+  for (int j = 0; j < kWarpSteps; ++j) {
+    const int64_t i = lo + j * kLayoutThreads + threadIdx.x;
+    const int e = i < a.pairs ? a.idx[i] : -1;
     if (e >= 0 && e < a.E) atomicAdd(&s_n[e], 1);
   }
   __syncthreads();
@@ -546,21 +673,21 @@ __global__ void __launch_bounds__(32) layout_scan_kernel(const LayoutArgs a, int
   griddep_wait();
   int* h = a.hist + static_cast<int64_t>(blockIdx.x) * (chunks + 1);
   const int lane = threadIdx.x;
-  constexpr int kPer = kMaxLayoutChunks / 32;
-  int v[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = 32 * i + lane < chunks ? h[32 * i + lane] : 0;
+  constexpr int kPer = 8;   // loads in flight
   int run = 0;
+  for (int c0 = 0; c0 < chunks; c0 += 32 * kPer) {
+    int v[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (32 * i < chunks) {
+    for (int i = 0; i < kPer; ++i) v[i] = c0 + 32 * i + lane < chunks ? h[c0 + 32 * i + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
       int x = v[i];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, x, o);
         if (lane >= o) x += y;
       }
-      if (32 * i + lane < chunks) h[32 * i + lane] = run + x - v[i];
+      if (c0 + 32 * i + lane < chunks) h[c0 + 32 * i + lane] = run + x - v[i];
       run += __shfl_sync(kFull, x, 31);
     }
   }
@@ -569,44 +696,47 @@ __global__ void __launch_bounds__(32) layout_scan_kernel(const LayoutArgs a, int
 
 __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const LayoutArgs a) {
   __shared__ uint16_t s_w[kLayoutWarps][kMaxExperts];   // counts of a warp, then of the warps before it
-  __shared__ int s_base[kMaxExperts];                   // first row of this chunk's choices
+  __shared__ int s_base[kMaxExperts];                   // first row of an expert, then of this chunk's choices
   __shared__ int s_total[kMaxExperts];                  // choices of an expert
   __shared__ int s_scan[kLayoutWarps];
   griddep_launch_dependents();
-  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = gridDim.x;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
-  const int64_t per_warp = (a.chunk + kLayoutWarps * 32 - 1) / (kLayoutWarps * 32) * 32;
-  const int64_t wlo = lo + warp * per_warp;
-  const int64_t whi = min(min(a.pairs, lo + a.chunk), wlo + per_warp);
   for (int e = lane; e < a.E; e += 32) s_w[warp][e] = 0;
   __syncwarp();
-  // choices of this warp by expert
-  for (int64_t i0 = wlo; i0 < whi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < whi ? a.idx[i] : -1;
-    const uint32_t same = __match_any_sync(kFull, e);
-    if (e >= 0 && e < a.E && lane == __ffs(same) - 1) s_w[warp][e] += static_cast<uint16_t>(__popc(same));
+  griddep_wait();
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * kChunkPairs + warp * (kChunkPairs / kLayoutWarps) + lane;
+  int e[kWarpSteps], before[kWarpSteps];   // expert; choices of it earlier in the warp's stretch
+#pragma unroll
+  for (int j = 0; j < kWarpSteps; ++j) {
+    e[j] = lo + 32 * j < a.pairs ? a.idx[lo + 32 * j] : -1;
+    if (e[j] < 0 || e[j] >= a.E) e[j] = -1;
+  }
+#pragma unroll
+  for (int j = 0; j < kWarpSteps; ++j) {
+    const uint32_t same = __match_any_sync(kFull, e[j]);
+    const int seen = e[j] >= 0 ? s_w[warp][e[j]] : 0;
+    before[j] = seen + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e[j] >= 0 && lane == __ffs(same) - 1) s_w[warp][e[j]] = static_cast<uint16_t>(seen + __popc(same));
     __syncwarp();
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kLayoutThreads) {
+  for (int x = threadIdx.x; x < a.E; x += kLayoutThreads) {
     int run = 0;
+#pragma unroll
     for (int w = 0; w < kLayoutWarps; ++w) {
-      const int n = s_w[w][e];
-      s_w[w][e] = static_cast<uint16_t>(run);
+      const int n = s_w[w][x];
+      s_w[w][x] = static_cast<uint16_t>(run);
       run += n;
     }
-    const int* h = a.hist + static_cast<int64_t>(e) * (chunks + 1);
-    s_base[e] = chunks > 1 ? h[blockIdx.x] : 0;
-    s_total[e] = chunks > 1 ? h[chunks] : run;
+    s_total[x] = chunks > 1 ? a.hist[static_cast<int64_t>(x) * (chunks + 1) + chunks] : run;
   }
   __syncthreads();
   // first rows: exclusive sum of the padded counts, two experts per thread
   const int e0 = 2 * threadIdx.x;
-  const int n0 = e0 < a.E ? s_total[e0] : 0, n1 = e0 + 1 < a.E ? s_total[e0 + 1] : 0;
-  const int p0 = (n0 + 127) / 128 * 128, p1 = (n1 + 127) / 128 * 128;
+  const int p0 = e0 < a.E ? (s_total[e0] + 127) / 128 * 128 : 0;
+  const int p1 = e0 + 1 < a.E ? (s_total[e0 + 1] + 127) / 128 * 128 : 0;
   int x = p0 + p1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -615,89 +745,105 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
   }
   if (lane == 31) s_scan[warp] = x;
   __syncthreads();
-  int first = x - p0 - p1;
-  for (int w = 0; w < warp; ++w) first += s_scan[w];
-  int end = 0;
-  for (int w = 0; w < kLayoutWarps; ++w) end += s_scan[w];
-  if (e0 < a.E) s_base[e0] += first;
-  if (e0 + 1 < a.E) s_base[e0 + 1] += first + p0;
-  if (blockIdx.x == 0) {
-    if (e0 < a.E) a.offsets[e0] = first;
-    if (e0 + 1 < a.E) a.offsets[e0 + 1] = first + p0;
-    if (threadIdx.x == 0) a.offsets[a.E] = end;
-  }
-  // padding rows: those of experts e = blockIdx.x, blockIdx.x + chunks, ... and the rows past the segments
+  int first = x - p0 - p1, end = 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int e = e0 + j, f = j == 0 ? first : first + p0, n = j == 0 ? n0 : n1, p = j == 0 ? p0 : p1;
-    if (e < a.E && e % chunks == static_cast<int>(blockIdx.x))
-      for (int r = f + n; r < f + p; ++r) a.row_token[r] = -1;
+  for (int w = 0; w < kLayoutWarps; ++w) {
+    if (w < warp) first += s_scan[w];
+    end += s_scan[w];
+  }
+  if (e0 < a.E) s_base[e0] = first;
+  if (e0 + 1 < a.E) s_base[e0 + 1] = first + p0;
+  __syncthreads();
+  // padding: a warp per expert, the experts dealt over the CTAs' warps; then the rows past the segments
+  for (int y = blockIdx.x * kLayoutWarps + warp; y < a.E; y += chunks * kLayoutWarps) {
+    const int from = s_base[y] + s_total[y], to = s_base[y] + (s_total[y] + 127) / 128 * 128;
+    for (int r = from + lane; r < to; r += 32) a.row_token[r] = -1;
   }
   for (int64_t r = end + static_cast<int64_t>(blockIdx.x) * kLayoutThreads + threadIdx.x; r < a.rows;
        r += static_cast<int64_t>(chunks) * kLayoutThreads)
     a.row_token[r] = -1;
-  __syncthreads();
-  // place: the running count of a warp moves on as its stretch is walked
-  for (int64_t i0 = wlo; i0 < whi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < whi ? a.idx[i] : -1;
-    const uint32_t same = __match_any_sync(kFull, e);
-    const bool ok = e >= 0 && e < a.E;
+  if (blockIdx.x == 0) {
+    for (int y = threadIdx.x; y < a.E; y += kLayoutThreads) a.offsets[y] = s_base[y];
+    if (threadIdx.x == 0) a.offsets[a.E] = end;
+  }
+#pragma unroll
+  for (int j = 0; j < kWarpSteps; ++j) {
+    const int64_t i = lo + 32 * j;
     int row = -1;
-    if (ok) row = s_base[e] + s_w[warp][e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (ok && lane == __ffs(same) - 1) s_w[warp][e] += static_cast<uint16_t>(__popc(same));
-    __syncwarp();
-    if (i < whi) a.row_of[i] = row;
-    if (ok) a.row_token[row] = static_cast<int32_t>(i / a.k);
+    if (e[j] >= 0) {
+      row = s_base[e[j]] + s_w[warp][e[j]] + before[j];
+      if (chunks > 1) row += a.hist[static_cast<int64_t>(e[j]) * (chunks + 1) + blockIdx.x];
+      a.row_token[row] = static_cast<int32_t>(i / a.k);
+    }
+    if (i < a.pairs) a.row_of[i] = row;
   }
 }
 
-template <int NL>
-cudaError_t run_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, (a.T + a.chunk - 1) / a.chunk));
-  if (backward)
-    return a.score == 0 ? launch_behind(route_backward_kernel<NL, 0>, grid, kRouteThreads, stream, a)
-                        : launch_behind(route_backward_kernel<NL, 1>, grid, kRouteThreads, stream, a);
+unsigned route_grid(const RouteArgs& a) {
+  return static_cast<unsigned>(std::max<int64_t>(1, (a.T + a.chunk - 1) / a.chunk));
+}
+
+template <int W, int NL>
+cudaError_t run_forward(const RouteArgs& a, cudaStream_t stream) {
+  const unsigned grid = route_grid(a);
   if (a.loss != nullptr)
-    return a.score == 0 ? launch_behind(route_kernel<NL, 0, true>, grid, kRouteThreads, stream, a)
-                        : launch_behind(route_kernel<NL, 1, true>, grid, kRouteThreads, stream, a);
-  return a.score == 0 ? launch_behind(route_kernel<NL, 0, false>, grid, kRouteThreads, stream, a)
-                      : launch_behind(route_kernel<NL, 1, false>, grid, kRouteThreads, stream, a);
+    return a.score == 0 ? launch_behind(route_kernel<W, NL, 0, true>, grid, kRouteThreads, stream, a)
+                        : launch_behind(route_kernel<W, NL, 1, true>, grid, kRouteThreads, stream, a);
+  return a.score == 0 ? launch_behind(route_kernel<W, NL, 0, false>, grid, kRouteThreads, stream, a)
+                      : launch_behind(route_kernel<W, NL, 1, false>, grid, kRouteThreads, stream, a);
+}
+
+template <int W, int NL>
+cudaError_t run_route(RouteArgs a, bool backward, cudaStream_t stream) {
+  if (!backward) return run_forward<W, NL>(a, stream);
+  // one wave: a CTA looks up its sequence and that one's counts first
+  constexpr int64_t kCtas = 152 * kBackwardCtas<W, NL>;
+  a.chunk = std::max<int64_t>(8, (a.T + kCtas - 1) / kCtas);
+  return a.score == 0 ? launch_behind(route_backward_kernel<W, NL, 0>, route_grid(a), kRouteThreads, stream, a)
+                      : launch_behind(route_backward_kernel<W, NL, 1>, route_grid(a), kRouteThreads, stream, a);
 }
 
 cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
-  if (a.E <= 32) return run_route<1>(a, backward, stream);
-  if (a.E <= 64) return run_route<2>(a, backward, stream);
-  if (a.E <= 128) return run_route<4>(a, backward, stream);
-  if (a.E <= 256) return run_route<8>(a, backward, stream);
-  if (a.E <= 512) return run_route<16>(a, backward, stream);
-  return run_route<32>(a, backward, stream);
+  // Half a warp per token where k lanes can reach the candidates' bound and the
+  // registers hold it (the backward pass spills at 16 logits a lane: 84 us for
+  // 131072 tokens of 256 logits against 62.5 with a whole warp).
+  if (a.k <= 16) {
+    if (a.E <= 16) return run_route<16, 1>(a, backward, stream);
+    if (a.E <= 32) return run_route<16, 2>(a, backward, stream);
+    if (a.E <= 64) return run_route<16, 4>(a, backward, stream);
+    if (a.E <= 128) return run_route<16, 8>(a, backward, stream);
+    if (a.E <= 256 && !backward) return run_forward<16, 16>(a, stream);
+  }
+  if (a.E <= 64) return run_route<32, 2>(a, backward, stream);
+  if (a.E <= 256) return run_route<32, 8>(a, backward, stream);
+  if (a.E <= 512) return run_route<32, 16>(a, backward, stream);
+  return run_route<32, 32>(a, backward, stream);
 }
 
-// Tokens per CTA: at most 608 CTAs, and at most 24 + T / 64 (the partial sums
-// stay small beside the logits).
-int64_t route_chunk(int64_t T) {
-  const int64_t chunks = std::min<int64_t>(kMaxChunks, 24 + T / 64);
-  const int64_t c = (T + chunks - 1) / chunks;
-  return std::max<int64_t>(kRouteWarps, (c + kRouteWarps - 1) / kRouteWarps * kRouteWarps);
+// Tokens per CTA with statistics: at most as many CTAs as are resident at
+// once, and at most 30 + T / 64 (the partial sums stay small beside the logits).
+constexpr int kMaxChunks = 456;
+int64_t stats_chunk(int64_t T) {
+  const int64_t chunks = std::min<int64_t>(kMaxChunks, 30 + T / 64);
+  return std::max<int64_t>(8, (T + chunks - 1) / chunks);
+}
+// Without: at most 64, so that the last CTAs to start are short.
+int64_t plain_chunk(int64_t T) {
+  return std::min<int64_t>(64, std::max<int64_t>(16, (T / kMaxChunks + 15) / 16 * 16));
 }
 
-int64_t layout_chunk(int64_t pairs) {
-  const int64_t c = (pairs + kMaxLayoutChunks - 1) / kMaxLayoutChunks;
-  return std::max<int64_t>(kChunkPairs, (c + kChunkPairs - 1) / kChunkPairs * kChunkPairs);
-}
+int64_t layout_chunks(int64_t pairs) { return std::max<int64_t>(1, (pairs + kChunkPairs - 1) / kChunkPairs); }
 
 }  // namespace
 
 int64_t route_workspace_bytes(int64_t T, int E, int64_t S) {
-  const int64_t rows = (T + route_chunk(T) - 1) / route_chunk(T) + S;
+  const int64_t rows = (T + stats_chunk(T) - 1) / stats_chunk(T) + S;
   const int64_t slices = (E + 31) / 32;
   return 4 * (rows * (2 * static_cast<int64_t>(E) + 1) + slices * S + 1);
 }
 
 cudaError_t launch_route(RouteArgs a, void* ws, cudaStream_t stream) {
-  a.chunk = route_chunk(a.T);
+  a.chunk = a.loss == nullptr ? plain_chunk(a.T) : stats_chunk(a.T);
   if (a.loss == nullptr) return pick_route(a, false, stream);
   const int64_t rows = (a.T + a.chunk - 1) / a.chunk + a.S;
   a.part_p = static_cast<float*>(ws);
@@ -711,20 +857,15 @@ cudaError_t launch_route(RouteArgs a, void* ws, cudaStream_t stream) {
   return launch_behind(route_finish_kernel, dim3(slices, static_cast<unsigned>(a.S)), kFinishThreads, stream, a);
 }
 
-cudaError_t launch_route_backward(RouteArgs a, cudaStream_t stream) {
-  a.chunk = route_chunk(a.T);
-  return pick_route(a, true, stream);
-}
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream) { return pick_route(a, true, stream); }
 
 int64_t layout_workspace_bytes(int64_t T, int k, int E) {
-  const int64_t pairs = T * k, chunk = layout_chunk(pairs);
-  const int64_t chunks = (pairs + chunk - 1) / chunk;
+  const int64_t chunks = layout_chunks(T * k);
   return chunks > 1 ? 4 * (chunks + 1) * E : 4;
 }
 
-cudaError_t launch_layout(LayoutArgs a, cudaStream_t stream) {
-  a.chunk = layout_chunk(a.pairs);
-  const unsigned chunks = static_cast<unsigned>(std::max<int64_t>(1, (a.pairs + a.chunk - 1) / a.chunk));
+cudaError_t launch_layout(const LayoutArgs& a, cudaStream_t stream) {
+  const unsigned chunks = static_cast<unsigned>(layout_chunks(a.pairs));
   if (chunks > 1) {
     cudaError_t e = launch_behind(layout_count_kernel, chunks, kLayoutThreads, stream, a);
     if (e != cudaSuccess) return e;
