@@ -474,6 +474,30 @@ def quantize_act_weight(x, w, pow2: bool = False, stream=None):
     return xq, sx, wq, sw
 
 
+def _checked(t, name: str, dtypes, dim: int | None = None, rows: bool = False):
+    """A tensor of one of the given types (and number of dimensions), its last
+    dimension dense; all of it dense unless ``rows``.  The C entry points see
+    pointers only."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    if t.dtype not in dtypes or (dim is not None and t.dim() != dim):
+        raise ValueError(f"{name}: {t.dim()}-d {t.dtype}; expected {dim}-d {' or '.join(map(str, dtypes))}")
+    if (t.stride(-1) != 1 and t.shape[-1] > 1) if rows else not t.is_contiguous():
+        raise ValueError(f"{name}: strides {tuple(t.stride())} of shape {tuple(t.shape)}")
+    return t
+
+
+def _row_stride(t) -> int:
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def _used_on(t, stream):
+    """Keeps a scratch tensor's memory until the work queued on ``stream`` is done."""
+    if stream is not None:
+        import torch
+        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _fp4_outputs(lead, K, fmt, device):
     import torch
     q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=device)
@@ -488,20 +512,24 @@ def quantize_fp4(x, fmt: int = FP4_E4M3X16, rows=None, stream=None):
     the scales in 512-byte blocks of 128 rows; g float32, a scale per row, None
     for FP4_UE8M0X32).  ``rows``: int32 [M'], quantise x[rows[i]] as row i (a
     row of zeros where rows[i] < 0)."""
+    import torch
     K = x.shape[-1]
     if x.dim() == 3:
+        _checked(x, "x", (torch.bfloat16,), 3)
         G, N, _ = x.shape
         q, sf, g = _fp4_outputs((G, N), K, fmt, x.device)
         if N % 128 == 0:      # the experts' scale blocks follow one another
-            fp8bs_quantize_fp4(x, G * N, K, x.stride(1), None, G * N, fmt, q, sf, g, stream)
+            fp8bs_quantize_fp4(x, G * N, K, K, None, G * N, fmt, q, sf, g, stream)
         else:
             for i in range(G):
-                fp8bs_quantize_fp4(x[i], N, K, x.stride(1), None, N, fmt, q[i], sf[i], None if g is None else g[i],
-                                   stream)
+                fp8bs_quantize_fp4(x[i], N, K, K, None, N, fmt, q[i], sf[i], None if g is None else g[i], stream)
         return q, sf, g
+    _checked(x, "x", (torch.bfloat16,), 2, rows=True)
+    if rows is not None:
+        _checked(rows, "rows", (torch.int32,), 1)
     M = x.shape[0] if rows is None else rows.shape[0]
     q, sf, g = _fp4_outputs((M,), K, fmt, x.device)
-    fp8bs_quantize_fp4(x, x.shape[0], K, x.stride(0), rows, M, fmt, q, sf, g, stream)
+    fp8bs_quantize_fp4(x, x.shape[0], K, _row_stride(x), rows, M, fmt, q, sf, g, stream)
     return q, sf, g
 
 
@@ -509,31 +537,57 @@ def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     """h: [M, 2I] bfloat16 CUDA tensor (gate | up).  Returns the 4-bit codes and
     scales of BF16(silu(gate) * up), as quantize_fp4; rows with live[i] < 0
     (int32 [M]) are rows of zeros."""
+    import torch
+    _checked(h, "h", (torch.bfloat16,), 2, rows=True)
     M, two_i = h.shape
+    if live is not None and _checked(live, "live", (torch.int32,), 1).shape[0] != M:
+        raise ValueError("live: one value per row of h")
     q, sf, g = _fp4_outputs((M,), two_i // 2, fmt, h.device)
-    fp8bs_swiglu_quantize_fp4(h, M, two_i // 2, h.stride(0), live, fmt, q, sf, g, stream)
+    fp8bs_swiglu_quantize_fp4(h, M, two_i // 2, _row_stride(h), live, fmt, q, sf, g, stream)
     return q, sf, g
 
 
 def dequantize_fp4(q, sf, g=None, fmt: int = FP4_E4M3X16, out_dtype=None, stream=None):
     """The values [M, K] of 4-bit codes, bfloat16 (default) or float32."""
     import torch
+    _fp4_operand((q, sf, g), "codes", fmt, 2)
     M, K = q.shape[0], 2 * q.shape[1]
     out = torch.empty((M, K), dtype=out_dtype or torch.bfloat16, device=q.device)
     fp8bs_dequantize_fp4(q, sf, g, M, K, fmt, out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, K, stream)
     return out
 
 
+def _fp4_operand(t, name: str, fmt: int, dim: int):
+    """Codes, scales and row scales that fit one another."""
+    import torch
+    q, sf, g = t
+    _checked(q, name + " codes", (torch.uint8,), dim)
+    _checked(sf, name + " scales", (torch.uint8,))
+    need = fp8bs_fp4_scale_bytes(q.shape[-2], 2 * q.shape[-1], fmt) * (q.shape[0] if dim == 3 else 1)
+    if sf.numel() != need or (fmt == FP4_E4M3X16 and (g is None or _checked(g, name + " row scales", (torch.float32,)).shape
+                                                      != q.shape[:-1])):
+        raise ValueError(f"{name}: scales do not fit codes of shape {tuple(q.shape)}")
+    return q, sf, g
+
+
+def _fp4_product_out(out, out_dtype, M, N, device):
+    import torch
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=device)
+    if tuple(_checked(out, "out", (torch.bfloat16, torch.float32), 2).shape) != (M, N):
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(M, N)}")
+    return out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32
+
+
 def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
     """D = A B^T of 4-bit operands; a = (q [M, K/2], sf, g) and b = (q [N, K/2], sf, g) as
     quantize_fp4 returns them."""
-    import torch
-    (qa, sfa, ga), (qb, sfb, gb) = a, b
+    (qa, sfa, ga), (qb, sfb, gb) = _fp4_operand(a, "a", fmt, 2), _fp4_operand(b, "b", fmt, 2)
     M, N, K = qa.shape[0], qb.shape[0], 2 * qa.shape[1]
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=qa.device)
-    fp8bs_gemm_fp4(qa, sfa, ga, qb, sfb, gb, fmt, out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, M, N, K,
-                   stream)
+    if qb.shape[1] != qa.shape[1]:
+        raise ValueError(f"K differs: {K} and {2 * qb.shape[1]}")
+    out, d_dtype = _fp4_product_out(out, out_dtype, M, N, qa.device)
+    fp8bs_gemm_fp4(qa, sfa, ga, qb, sfb, gb, fmt, out, d_dtype, M, N, K, stream)
     return out
 
 
@@ -541,14 +595,26 @@ def grouped_gemm_fp4(a, offsets, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=
     """Per-expert D rows = A rows of the expert x B[g]^T; offsets int32 CUDA tensor [G+1], b as
     quantize_fp4 returns it for weights [G, N, K]."""
     import torch
-    (qa, sfa, ga), (qb, sfb, gb) = a, b
+    (qa, sfa, ga), (qb, sfb, gb) = _fp4_operand(a, "a", fmt, 2), _fp4_operand(b, "b", fmt, 3)
     M, K = qa.shape[0], 2 * qa.shape[1]
     G, N, _ = qb.shape
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=qa.device)
-    fp8bs_grouped_gemm_fp4(qa, sfa, ga, M, offsets, G, qb, sfb, gb, fmt, out,
-                           OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, N, K, stream)
+    if qb.shape[2] != qa.shape[1] or _checked(offsets, "offsets", (torch.int32,), 1).shape[0] != G + 1:
+        raise ValueError(f"a {tuple(qa.shape)}, b {tuple(qb.shape)} and {offsets.shape[0]} offsets do not fit")
+    out, d_dtype = _fp4_product_out(out, out_dtype, M, N, qa.device)
+    fp8bs_grouped_gemm_fp4(qa, sfa, ga, M, offsets, G, qb, sfb, gb, fmt, out, d_dtype, N, K, stream)
     return out
+
+
+def _route_inputs(logits, bias, valid, seq):
+    import torch
+    _checked(logits, "logits", (torch.float32, torch.bfloat16), 2, rows=True)
+    T, E = logits.shape
+    if bias is not None and _checked(bias, "bias", (torch.float32,), 1).shape[0] != E:
+        raise ValueError("bias: one value per expert")
+    if valid is not None and _checked(valid, "valid", (torch.uint8, torch.bool), 1).shape[0] != T:
+        raise ValueError("valid: one value per token")
+    if seq is not None:
+        _checked(seq, "seq", (torch.int32,), 1)
 
 
 def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None, seq=None, normalize: bool = True,
@@ -558,14 +624,16 @@ def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None,
     loss's factor) also (counts [S, E] int32, tokens [S] int32, loss [1]).
     ``valid``: uint8 [T]; ``seq``: int32 [S + 1], the sequences' first tokens."""
     import torch
+    S = 1 if seq is None else seq.shape[0] - 1
+    _route_inputs(logits, bias, valid, seq)
     T, E = logits.shape
     dev = logits.device
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
     in_dtype = IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32
-    S = 1 if seq is None else seq.shape[0] - 1
+    ld = _row_stride(logits)
     if alpha is None:
-        fp8bs_moe_route(logits, in_dtype, T, E, logits.stride(0), score, bias, valid, None, 1, k, normalize, scale, 0.0,
+        fp8bs_moe_route(logits, in_dtype, T, E, ld, score, bias, valid, None, 1, k, normalize, scale, 0.0,
                         idx, w, None, None, None, None, 0, stream)
         return idx, w
     counts = torch.empty((S, E), dtype=torch.int32, device=dev)
@@ -573,8 +641,9 @@ def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None,
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     n = moe_route_workspace_bytes(T, E, S)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    fp8bs_moe_route(logits, in_dtype, T, E, logits.stride(0), score, bias, valid, seq, S, k, normalize, scale, alpha,
-                    idx, w, counts, tokens, loss, ws, n, stream)
+    fp8bs_moe_route(logits, in_dtype, T, E, ld, score, bias, valid, seq, S, k, normalize, scale, alpha, idx, w, counts,
+                    tokens, loss, ws, n, stream)
+    _used_on(ws, stream)
     return idx, w, counts, tokens, loss
 
 
@@ -584,11 +653,19 @@ def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, 
     with counts and tokens; None leaves the loss out) with respect to the
     logits, in their type."""
     import torch
+    _route_inputs(logits, None, valid, seq)
     T, E = logits.shape
+    S = 1 if seq is None else seq.shape[0] - 1
+    if _checked(idx, "idx", (torch.int32,), 2).shape != _checked(dw, "dw", (torch.float32,), 2).shape or idx.shape[0] != T:
+        raise ValueError(f"idx {tuple(idx.shape)} and dw {tuple(dw.shape)}: one row per token each")
+    if dloss is not None:
+        _checked(dloss, "dloss", (torch.float32,))
+        if tuple(_checked(counts, "counts", (torch.int32,), 2).shape) != (S, E) or tokens.shape[0] != S:
+            raise ValueError("counts and tokens: those of moe_route")
     dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    fp8bs_moe_route_backward(logits, IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32, T, E, logits.stride(0),
-                             score, valid, seq, 1 if seq is None else seq.shape[0] - 1, idx.shape[1], normalize, scale,
-                             alpha, idx, counts, tokens, dw, dloss, dlogits, E, stream)
+    fp8bs_moe_route_backward(logits, IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32, T, E, _row_stride(logits),
+                             score, valid, seq, S, idx.shape[1], normalize, scale, alpha, idx, counts, tokens, dw,
+                             dloss, dlogits, E, stream)
     return dlogits
 
 
@@ -596,7 +673,7 @@ def moe_layout(idx, E: int, stream=None):
     """Row layout of the choices idx [T, k] among E experts: (offsets [E + 1], row_token
     [rows], row_of [T, k]), int32, as fp8bs_moe_layout describes them."""
     import torch
-    T, k = idx.shape
+    T, k = _checked(idx, "idx", (torch.int32,), 2).shape
     rows = moe_layout_rows(T, k, E)
     offsets = torch.empty(E + 1, dtype=torch.int32, device=idx.device)
     row_token = torch.empty(rows, dtype=torch.int32, device=idx.device)
@@ -604,4 +681,5 @@ def moe_layout(idx, E: int, stream=None):
     n = moe_layout_workspace_bytes(T, k, E)
     ws = torch.empty(n, dtype=torch.uint8, device=idx.device)
     fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, n, stream)
+    _used_on(ws, stream)
     return offsets, row_token, row_of

@@ -32,6 +32,12 @@ one launch that moves the tokens (or the expert rows) through the composed
 indices.  The movement and exchange steps are parameters of dispatch() and
 combine() so that the exchange protocol can be exercised with other
 implementations of them.
+
+With one rank and 4-bit experts the whole layer stays on the device:
+moe_layer_fp4() routes the tokens (fp8bs_moe_route), lays the choices out
+(fp8bs_moe_layout, the same segments as RecvPlan's), quantises the tokens'
+rows into them, runs the two grouped 4-bit GEMMs around the SwiGLU and
+combines, without reading anything back, so it can be captured in a CUDA graph.
 """
 from __future__ import annotations
 
@@ -215,3 +221,27 @@ def combine(y, weights, plan: MoePlan, recv: RecvPlan, gather_bf16=None, combine
     ret = back.new_empty((int(plan.send_counts.sum()), back.shape[1]))
     (all_to_all or _a2a)(ret, back, plan.send_counts, recv.recv_per_src)
     return cb(ret, ix(plan.send_pos), w)
+
+
+def quantize_experts_fp4(w_gate_up, w_down, fmt: int = 0):
+    """The experts' weights in 4 bits, once: w_gate_up [E, 2I, H] (gate | up) and w_down [E, H, I]
+    bfloat16 CUDA tensors -> what moe_layer_fp4 takes."""
+    from . import quantize_fp4
+    return quantize_fp4(w_gate_up, fmt), quantize_fp4(w_down, fmt)
+
+
+def moe_layer_fp4(x, logits, experts, k: int, fmt: int = 0, score: int = 0, bias=None, valid=None, scale: float = 1.0,
+                  seq=None, alpha: float | None = None):
+    """One MoE layer with 4-bit experts on one rank: x [T, H] bfloat16, logits
+    [T, E] (float32 or bfloat16, the router's product), experts from
+    quantize_experts_fp4.  Returns (out [T, H] bfloat16, route), route being
+    moe_route's result: (idx, w), or with ``alpha`` also the counts, tokens
+    and balance loss that moe_route_backward takes.  Every launch is on the
+    current stream; nothing is read back."""
+    from . import grouped_gemm_fp4, moe_layout, moe_route, quantize_fp4, swiglu_quantize_fp4
+    gate_up, down = experts
+    route = moe_route(logits, k, score, bias=bias, valid=valid, seq=seq, scale=scale, alpha=alpha)
+    offsets, row_token, row_of = moe_layout(route[0], logits.shape[1])
+    h = grouped_gemm_fp4(quantize_fp4(x, fmt, rows=row_token), offsets, gate_up, fmt)
+    y = grouped_gemm_fp4(swiglu_quantize_fp4(h, fmt, live=row_token), offsets, down, fmt)
+    return _kernel_combine(y, row_of, route[1]), route
