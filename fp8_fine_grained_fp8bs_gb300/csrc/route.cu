@@ -165,13 +165,14 @@ __device__ __forceinline__ int64_t sequence_end(const RouteArgs& a, int s) { ret
 
 // The largest key of the group's keys key[i] (expert W i + g; -inf or NaN
 // where not eligible) in `most` (0: none is eligible), and candidates for the
-// k largest of them: all keys from a bound on that k lane maxima reach, less
-// `slack`.  No key among the k largest lies below such a bound.  It is found by
-// bisection on the lane maxima, to where k or k + 1 of them reach it; of 256
-// random keys and k = 8, eleven pass on average, so that the exact order is
-// worked out on one key per lane.  Leaves the candidates' experts in `list`
-// (lanes' first ones before their second ones) and returns their number, which
-// may be above 32 (ties, k near W): only the first 32 are in the list then.
+// k largest of them: all keys from the k-th largest lane maximum on, less
+// `slack`; no key among the k largest lies below it.  Of 256 random keys and
+// k = 8 about eleven pass, so that the exact order is worked out on one key per
+// lane.  (The bound by sorting the maxima, ten exchanges: 32749 tokens in 18.6
+// us; by bisection between the least and the largest of them, 22.0.)  Leaves the
+// candidates' experts in `list` (lanes' first ones before their second ones)
+// and returns their number, which may be above 32 (ties, k near W): only the
+// first 32 are in the list then.
 template <int W, int NL>
 __device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool slack, int lane, uint16_t* list,
                                           uint32_t& most) {
@@ -179,23 +180,19 @@ __device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool sl
 #pragma unroll
   for (int i = 1; i < NL; ++i) m = fmaxf(m, key[i]);
   const uint32_t mine = eligible(m) ? order_key(m) : 0u;
-  most = group_max<W>(mine);
-  // at least k lanes reach `low`, fewer than k reach `high`
-  uint32_t low = group_min<W>(mine), high = most + 1u;
-  bool go = high - low > 1u;
-  while (__any_sync(kFull, go)) {
-    const uint32_t mid = low + (high - low) / 2u;
-    const int n = __popc(group_ballot<W>(mine >= mid, lane));
-    if (go) {
-      if (n >= k) {
-        low = mid;
-        go = n > k + 1;
-      } else {
-        high = mid;
-      }
-      go = go && high - low > 1u;
+  // bitonic sort of the lanes' maxima, largest first
+  uint32_t sorted = mine;
+#pragma unroll
+  for (int size = 2; size <= W; size *= 2) {
+#pragma unroll
+    for (int d = size / 2; d > 0; d /= 2) {
+      const uint32_t other = __shfl_xor_sync(kFull, sorted, d);
+      const bool upper = ((lane & d) == 0) == (size == W || (lane & size) == 0);
+      sorted = upper ? max(sorted, other) : min(sorted, other);
     }
   }
+  most = __shfl_sync(kFull, sorted, lane & ~(W - 1));
+  const uint32_t low = __shfl_sync(kFull, sorted, (lane & ~(W - 1)) + k - 1);
   float bound = low == 0u ? kLowest : from_key(low);   // 0: fewer than k lanes hold an eligible key
   if (slack) bound = fmaxf(bound - (1e-5f + 1e-6f * fabsf(bound)), kLowest);
   uint32_t mask = 0;
@@ -215,9 +212,11 @@ __device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool sl
   return n;
 }
 
-// CTAs that an SM should hold, which bounds the registers of a thread.
-template <int NL>
-constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? 3 : 1;
+// CTAs that an SM should hold, which bounds the registers of a thread (32749
+// tokens of 256 logits: 15.2 us with four CTAs, 18.6 with three; with the
+// statistics' sums four would spill: 36 us against 27).
+template <int NL, bool kStats>
+constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? (kStats ? 3 : 4) : 1;
 
 // CTA c routes tokens [c * chunk, (c + 1) * chunk).  With statistics, each
 // stretch of one sequence inside the chunk leaves its sums in row c + s of
@@ -227,11 +226,11 @@ constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? 3 : 1;
 // Bound by instructions (about 330 a token of 256 logits, 500 with statistics
 // and biased sigmoids, two thirds of the issue slots busy).  131072 tokens: 154
 // us choosing the k experts one by one from all keys, two warp reductions and a
-// pass over the keys each; 86 with candidates, a warp per token; 65 with half a
+// pass over the keys each; 86 with candidates, a warp per token; 61 with half a
 // warp, which shares the per-token steps between two tokens (with statistics
-// 166, 108 and 85 us).
+// 166, 108 and 80 us).
 template <int W, int NL, int kScore, bool kStats>
-__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL>) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_kernel(const RouteArgs a) {
   constexpr int kGroups = kRouteThreads / W;          // tokens at a time
   constexpr int kPerLane = 32 / W;                    // candidates of a lane
   __shared__ float s_p[kStats ? kGroups * W * NL : 1];
@@ -696,8 +695,9 @@ __global__ void __launch_bounds__(32) layout_scan_kernel(const LayoutArgs a, int
 
 __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const LayoutArgs a) {
   __shared__ uint16_t s_w[kLayoutWarps][kMaxExperts];   // counts of a warp, then of the warps before it
-  __shared__ int s_base[kMaxExperts];                   // first row of an expert, then of this chunk's choices
+  __shared__ int s_base[kMaxExperts];                   // first row of an expert
   __shared__ int s_total[kMaxExperts];                  // choices of an expert
+  __shared__ int s_before[kMaxExperts];                 // choices of it in earlier chunks
   __shared__ int s_scan[kLayoutWarps];
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -711,6 +711,13 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
   for (int j = 0; j < kWarpSteps; ++j) {
     e[j] = lo + 32 * j < a.pairs ? a.idx[lo + 32 * j] : -1;
     if (e[j] < 0 || e[j] >= a.E) e[j] = -1;
+  }
+  if (chunks > 1) {
+    for (int x = threadIdx.x; x < a.E; x += kLayoutThreads) {
+      const int* h = a.hist + static_cast<int64_t>(x) * (chunks + 1);
+      s_before[x] = h[blockIdx.x];
+      s_total[x] = h[chunks];
+    }
   }
 #pragma unroll
   for (int j = 0; j < kWarpSteps; ++j) {
@@ -730,7 +737,10 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
       s_w[w][x] = static_cast<uint16_t>(run);
       run += n;
     }
-    s_total[x] = chunks > 1 ? a.hist[static_cast<int64_t>(x) * (chunks + 1) + chunks] : run;
+    if (chunks == 1) {
+      s_before[x] = 0;
+      s_total[x] = run;
+    }
   }
   __syncthreads();
   // first rows: exclusive sum of the padded counts, two experts per thread
@@ -771,8 +781,7 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_place_kernel(const Layo
     const int64_t i = lo + 32 * j;
     int row = -1;
     if (e[j] >= 0) {
-      row = s_base[e[j]] + s_w[warp][e[j]] + before[j];
-      if (chunks > 1) row += a.hist[static_cast<int64_t>(e[j]) * (chunks + 1) + blockIdx.x];
+      row = s_base[e[j]] + s_before[e[j]] + s_w[warp][e[j]] + before[j];
       a.row_token[row] = static_cast<int32_t>(i / a.k);
     }
     if (i < a.pairs) a.row_of[i] = row;
@@ -820,11 +829,13 @@ cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
   return run_route<32, 32>(a, backward, stream);
 }
 
-// Tokens per CTA with statistics: at most as many CTAs as are resident at
-// once, and at most 30 + T / 64 (the partial sums stay small beside the logits).
+// Tokens per CTA with statistics: as many CTAs as are resident at once (131072
+// tokens of 128 logits: 51.8 us with 608, 59.1 with 456), and at most 30 + T / 64
+// (the partial sums stay small beside the logits).
 constexpr int kMaxChunks = 456;
-int64_t stats_chunk(int64_t T) {
-  const int64_t chunks = std::min<int64_t>(kMaxChunks, 30 + T / 64);
+int64_t stats_chunk(int64_t T, int E) {
+  const int64_t resident = E <= 128 ? 152 * 4 : kMaxChunks;
+  const int64_t chunks = std::min<int64_t>(resident, 30 + T / 64);
   return std::max<int64_t>(8, (T + chunks - 1) / chunks);
 }
 // Without: at most 64, so that the last CTAs to start are short.
@@ -837,13 +848,13 @@ int64_t layout_chunks(int64_t pairs) { return std::max<int64_t>(1, (pairs + kChu
 }  // namespace
 
 int64_t route_workspace_bytes(int64_t T, int E, int64_t S) {
-  const int64_t rows = (T + stats_chunk(T) - 1) / stats_chunk(T) + S;
+  const int64_t chunk = stats_chunk(T, E), rows = (T + chunk - 1) / chunk + S;
   const int64_t slices = (E + 31) / 32;
   return 4 * (rows * (2 * static_cast<int64_t>(E) + 1) + slices * S + 1);
 }
 
 cudaError_t launch_route(RouteArgs a, void* ws, cudaStream_t stream) {
-  a.chunk = a.loss == nullptr ? plain_chunk(a.T) : stats_chunk(a.T);
+  a.chunk = a.loss == nullptr ? plain_chunk(a.T) : stats_chunk(a.T, a.E);
   if (a.loss == nullptr) return pick_route(a, false, stream);
   const int64_t rows = (a.T + a.chunk - 1) / a.chunk + a.S;
   a.part_p = static_cast<float*>(ws);
