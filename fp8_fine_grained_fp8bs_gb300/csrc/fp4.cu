@@ -15,7 +15,10 @@
 // All memory-bound streams: a row is read once into registers (16 elements,
 // a "unit", per thread and step; rows longer than the registers hold are read
 // twice, from L2 the second time), its maximum is reduced across the row's
-// warps, and codes and scales leave with 8-byte and 4-byte stores.
+// warps, and codes and scales leave with 8-byte and 4-byte stores.  [16384][7168]
+// in 48.4 us with E4M3 scales (301 MB, 0.92 of the copy bandwidth) and 42.6 with
+// UE8M0 ones (1.0); the SwiGLU form is bound by instructions (27 an element, expf
+// above all): [8191][2048] in 18.3 us, 0.62 of the copy bandwidth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -291,8 +294,9 @@ __global__ void __launch_bounds__(kWarps * rows_per_cta(kWarps) * 32) fp4_quant_
 // the second rounds once, BF16 output once more.  A lane turns 4 bytes of
 // codes into 8 consecutive values, so a warp writes 512 (BF16) or 1024
 // consecutive bytes; kPieces such pieces of a row are in flight per warp.
-// (16 elements a lane, 32 bytes written in two halves: 63 us for [16384][7168]
-// and 2.7 times the L2 sectors that the bytes make.)
+// [16384][7168] in 45.7 us, 0.97 of the copy bandwidth (16 elements a lane, 32
+// bytes written in two halves: 63 us and 2.7 times the L2 sectors that the bytes
+// make).
 constexpr int kPieces = 4;
 constexpr int kPieceK = 256;   // elements of a row that a warp takes at once
 

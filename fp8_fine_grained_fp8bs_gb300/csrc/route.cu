@@ -119,8 +119,9 @@ __device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int g,
 }
 
 // e^x and 1 / x by the hardware's base-2 exponential and reciprocal, for the
-// scores that only enter sums and gradients (relative error below 2^-21 where
-// the result matters); the weights and biased keys use expf and IEEE division.
+// scores that only enter sums and gradients and for the sums they are divided by
+// (relative error below 2^-21 where the result matters); the chosen scores and
+// biased keys use expf and IEEE division.
 __device__ __forceinline__ float fast_exp(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -223,7 +224,7 @@ constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? (kStats ? 3 : 4) : 1;
 // the partial arrays: along the tokens every step from one (chunk, sequence)
 // to the next raises c or s, so the rows are distinct.
 //
-// Bound by instructions (about 330 a token of 256 logits, 500 with statistics
+// Bound by instructions (about 290 a token of 256 logits, 430 with statistics
 // and biased sigmoids, two thirds of the issue slots busy).  131072 tokens: 154
 // us choosing the k experts one by one from all keys, two warp reductions and a
 // pass over the keys each; 86 with candidates, a warp per token; 61 with half a
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_k
 // Sums the partial rows of a sequence for 32 experts (32 threads share an
 // expert, each taking every 32nd chunk), writes its counts and tokens, and
 // leaves the slice's share of the loss; the last CTA to finish adds the
-// shares in their order.
+// shares in their order.  About 3 us behind the router.
 constexpr int kFinishThreads = 1024;
 __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const RouteArgs a) {
   __shared__ float s_p[32][33];
@@ -499,6 +500,12 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
   }
 }
 
+// CTAs on an SM, more of them against more registers a thread: 131072 tokens of
+// 256 logits 62.5 us with four, 71.2 with three; of 128 logits (half a warp a
+// token) 43.1 and 38.5.
+template <int W, int NL>
+constexpr int kBackwardCtas = NL <= 4 ? 4 : NL == 8 ? (W == 32 ? 4 : 3) : NL == 16 ? 2 : 1;
+
 // d logits from the gradients of the gate weights and of the balance loss.
 // With g_i = d loss / d p_i (the sequence's constants) and d_j the gradients
 // of the chosen scores,
@@ -506,12 +513,9 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
 //   sigmoid: dz_i = s_i (1 - s_i) (d_i + (g_i - sum_l p_l g_l) / sum_l s_l).
 // Every lane first stores its experts' dz without d_i; the lanes that hold the
 // token's choices then store theirs whole over those k.
-// CTAs on an SM, more of them against more registers a thread: 131072 tokens of
-// 256 logits 62.5 us with four, 71.2 with three; of 128 logits (half a warp a
-// token) 43.1 and 38.5.
-template <int W, int NL>
-constexpr int kBackwardCtas = NL <= 4 ? 4 : NL == 8 ? (W == 32 ? 4 : 3) : NL == 16 ? 2 : 1;
-
+// Reads and writes T E values: 268 MB for 131072 tokens of 256, 40 us at the
+// copy bandwidth; 64 us measured, instructions (about 400 a token) and loads
+// waited for in equal parts.
 template <int W, int NL, int kScore>
 __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_backward_kernel(const RouteArgs a) {
   constexpr int kGroups = kRouteThreads / W;
@@ -643,7 +647,8 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
 // writes them.  A single chunk needs the last kernel alone; its CTAs all rank
 // it, the first writes it, and they share the padding (up to 127 rows an
 // expert: 256 tokens, 8 of 256 experts, took 9.1 us with one CTA, 5.8 with 16).
-// A few chunks get CTAs that only fill, too.
+// A few chunks get CTAs that only fill, too.  Bound by latency: three launches
+// and a few dependent reads, 15 us for 261992 choices (3 MB).
 constexpr int kLayoutThreads = 512;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kMaxExperts = 1024;
@@ -827,9 +832,9 @@ cudaError_t run_route(RouteArgs a, bool backward, cudaStream_t stream) {
 }
 
 cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
-  // Half a warp per token where k lanes can reach the candidates' bound and the
-  // registers hold it (the backward pass spills at 16 logits a lane: 84 us for
-  // 131072 tokens of 256 logits against 62.5 with a whole warp).
+  // Half a warp per token where k lanes can reach the candidates' bound; the
+  // backward pass has less to share and needs more registers (131072 tokens of
+  // 256 logits: 66.4 us with half a warp, 63.9 with a whole one).
   if (a.k <= 16) {
     if (a.E <= 16) return run_route<16, 1>(a, backward, stream);
     if (a.E <= 32) return run_route<16, 2>(a, backward, stream);

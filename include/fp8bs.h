@@ -50,12 +50,12 @@ extern "C" {
 typedef enum {
   FP8BS_OK = 0,
   FP8BS_ERR_INVALID_ARG = 1,      /* NULL pointer, negative size, unknown enum value */
-  FP8BS_ERR_SHAPE = 2,            /* a size breaks a multiple-of-128 rule */
+  FP8BS_ERR_SHAPE = 2,            /* a size breaks a multiple-of rule or a limit of the call */
   FP8BS_ERR_ALIGNMENT = 3,        /* pointer or leading dimension not 16-byte aligned */
   FP8BS_ERR_UNSUPPORTED_ARCH = 4, /* current device is not sm_103 */
   FP8BS_ERR_CUDA = 5,             /* a CUDA runtime or driver call failed */
   FP8BS_ERR_TIMEOUT = 6,          /* a bounded device wait expired */
-  FP8BS_ERR_DEVICE_ARG = 7        /* a device-resident argument (group offsets) was invalid */
+  FP8BS_ERR_DEVICE_ARG = 7        /* a device-resident argument (group offsets, sequences) was invalid */
 } fp8bs_status;
 
 typedef enum { FP8BS_OUT_F32 = 0, FP8BS_OUT_BF16 = 1 } fp8bs_out_dtype;

@@ -265,6 +265,16 @@ def test_grouped_gemm_refuses_bad_offsets(offsets):
     assert torch.all(y == 3.0) and fp8bs.fp8bs_get_device_status() == 0
 
 
+def test_grouped_gemm_without_rows():
+    torch, fp8bs = require_gpu()
+    a, _ = _operand(fp8bs, 256, 128, 0, 1)
+    b = fp8bs.quantize_fp4(to_dev_bf16(synth.normal_bf16((3, 136, 128), 1.0, 2, 5)), 0)
+    y = torch.full((256, 136), 3.0, dtype=torch.bfloat16, device="cuda:0")
+    for offsets in ([0, 0, 0, 0], [128, 128, 128, 128]):
+        fp8bs.grouped_gemm_fp4(a, to_dev(np.array(offsets, np.int32)), b, 0, out=y)
+    assert fp8bs.fp8bs_get_device_status() == 0 and torch.all(y == 3.0)
+
+
 def test_gemm_repeats_bit_for_bit():
     torch, fp8bs = require_gpu()
     a, _ = _operand(fp8bs, 5, 7168, 0, 1)
