@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   __syncthreads();
   tc_fence_after_sync();
   if (kPair) cluster_sync();
+  griddep_launch_dependents();  // the next kernel may start on the SMs that this one leaves first
   griddep_wait();  // operands, scales and D are touched only after the preceding kernel
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, misc[0], 0);
   const int total_tiles = static_cast<int>(misc[2]);

@@ -119,9 +119,8 @@ __device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int g,
 }
 
 // e^x and 1 / x by the hardware's base-2 exponential and reciprocal, for the
-// scores that only enter sums and gradients and for the sums they are divided by
-// (relative error below 2^-21 where the result matters); the chosen scores and
-// biased keys use expf and IEEE division.
+// scores that only enter sums and gradients (relative error below 2^-21 where
+// the result matters); the weights and biased keys use expf and IEEE division.
 __device__ __forceinline__ float fast_exp(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_k
         }
       }
       float unit = a.scale;
-      if (a.normalize) unit *= fast_rcp(group_sum<W>(chosen) + kScoreEps);
+      if (a.normalize) unit /= group_sum<W>(chosen) + kScoreEps;
       if (here) {
 #pragma unroll
         for (int r = 0; r < kPerLane; ++r) {
