@@ -547,13 +547,25 @@ def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     return q, sf, g
 
 
+def _out_type(dtype):
+    """(torch type, fp8bs_out_dtype) of an output: bfloat16 (default) or float32.
+    The kernels write two or four bytes an element, so any other type is
+    refused before it is allocated."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype: {dtype}; expected torch.bfloat16 or torch.float32")
+    return dtype, OUT_BF16 if dtype == torch.bfloat16 else OUT_F32
+
+
 def dequantize_fp4(q, sf, g=None, fmt: int = FP4_E4M3X16, out_dtype=None, stream=None):
     """The values [M, K] of 4-bit codes, bfloat16 (default) or float32."""
     import torch
     _fp4_operand((q, sf, g), "codes", fmt, 2)
     M, K = q.shape[0], 2 * q.shape[1]
-    out = torch.empty((M, K), dtype=out_dtype or torch.bfloat16, device=q.device)
-    fp8bs_dequantize_fp4(q, sf, g, M, K, fmt, out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32, K, stream)
+    out_dtype, code = _out_type(out_dtype)
+    out = torch.empty((M, K), dtype=out_dtype, device=q.device)
+    fp8bs_dequantize_fp4(q, sf, g, M, K, fmt, out, code, K, stream)
     return out
 
 

@@ -1,0 +1,51 @@
+"""The allocating functions refuse what the C entry points could not see, before they launch anything.
+
+Runs without a GPU: CPU tensors that claim to be CUDA ones, and entry points that record their calls
+instead of making them.
+"""
+import pytest
+
+import fp8_fine_grained_fp8bs_gb300 as fp8bs
+
+torch = pytest.importorskip("torch")
+
+
+class ClaimsCuda(torch.Tensor):
+    """A CPU tensor that the wrappers take for a CUDA one."""
+    is_cuda = True
+
+
+def claim(t):
+    return t.as_subclass(ClaimsCuda)
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    """The entry points called; none of them runs."""
+    fp8bs.build()
+    fp8bs.load_library()
+    calls = []
+    for name in fp8bs.__all__:
+        if name.startswith("fp8bs_") and not name.endswith(("_bytes", "_string")):
+            monkeypatch.setattr(fp8bs, name, lambda *a, _name=name, **k: calls.append(_name))
+    return calls
+
+
+def _codes(M, K, fmt, G=None):
+    lead = (M,) if G is None else (G, M)
+    n = fp8bs.fp4_scale_bytes(M, K, fmt)
+    return (claim(torch.zeros((*lead, K // 2), dtype=torch.uint8)), claim(torch.zeros((*lead[:-1], n), dtype=torch.uint8)),
+            claim(torch.ones(lead)) if fmt == 0 else None)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float8_e4m3fn, torch.uint8, torch.float64])
+def test_dequantize_writes_float32_or_bfloat16_only(launched, dtype, fmt):
+    """The kernel writes two or four bytes an element, whatever the output was allocated as."""
+    q, sf, g = _codes(5, 128, fmt)
+    with pytest.raises(ValueError):
+        fp8bs.dequantize_fp4(q, sf, g, fmt, out_dtype=dtype)
+    assert launched == []
+    for dtype in (None, torch.bfloat16, torch.float32):
+        assert fp8bs.dequantize_fp4(q, sf, g, fmt, out_dtype=dtype).shape == (5, 128)
+    assert launched == ["fp8bs_dequantize_fp4"] * 3
