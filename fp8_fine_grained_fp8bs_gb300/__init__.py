@@ -363,6 +363,41 @@ fp4_scale_bytes = fp8bs_fp4_scale_bytes
 
 # ------------------------------------------------------ allocating conveniences
 
+def _checked(t, name: str, dtypes, dim: int | None = None, rows: bool = False):
+    """A tensor of one of the given types (and number of dimensions), its last
+    dimension dense; all of it dense unless ``rows``.  The C entry points see
+    pointers only."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    if t.dtype not in dtypes or (dim is not None and t.dim() != dim):
+        raise ValueError(f"{name}: {t.dim()}-d {t.dtype}; expected {dim}-d {' or '.join(map(str, dtypes))}")
+    if (t.stride(-1) != 1 and t.shape[-1] > 1) if rows else not t.is_contiguous():
+        raise ValueError(f"{name}: strides {tuple(t.stride())} of shape {tuple(t.shape)}")
+    return t
+
+
+def _out_type(dtype):
+    """(torch type, fp8bs_out_dtype) of an output: bfloat16 (default) or float32.
+    The kernels write two or four bytes an element, so any other type is
+    refused before it is allocated."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype: {dtype}; expected torch.bfloat16 or torch.float32")
+    return dtype, OUT_BF16 if dtype == torch.bfloat16 else OUT_F32
+
+
+def _product_out(out, out_dtype, M, N, device):
+    """(output [M, N], its fp8bs_out_dtype): the given one, checked, or a new one."""
+    import torch
+    if out is None:
+        dtype, code = _out_type(out_dtype)
+        return torch.empty((M, N), dtype=dtype, device=device), code
+    if tuple(_checked(out, "out", (torch.bfloat16, torch.float32), 2).shape) != (M, N):
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(M, N)}")
+    return out, _out_type(out.dtype)[1]
+
+
 def quantize_act(x, transposed: bool = False, pow2: bool = False, stream=None):
     """x: [M, K] bfloat16 CUDA tensor (row-major, K % 128 == 0).
 
@@ -423,12 +458,9 @@ def gemm(a, sa, b, sb, sb_kind: int = SCALE_BLOCK128x128, out_dtype=None, out=No
          stream=None, pow2: bool = False):
     """D = A B^T with per-128-K-block scales; A [M,K], B [N,K] uint8 E4M3.
     ``pow2``: power-of-two scales applied by the tensor core (fp8bs_gemm_pow2)."""
-    import torch
     M, K = a.shape
     N = b.shape[0]
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
-    d_dtype = OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32
+    out, d_dtype = _product_out(out, out_dtype, M, N, a.device)
     fn = fp8bs_gemm_pow2 if pow2 else fp8bs_gemm
     fn(a, sa, b, sb, sb_kind, out, d_dtype, M, N, K, int(accumulate), stream)
     return out
@@ -437,12 +469,9 @@ def gemm(a, sa, b, sb, sb_kind: int = SCALE_BLOCK128x128, out_dtype=None, out=No
 def grouped_gemm(a, sa, offsets, b, sb, out_dtype=None, out=None, stream=None, pow2: bool = False):
     """Per-expert D rows = A rows of the expert x B[g]^T; offsets: int32 CUDA tensor [G+1].
     ``pow2``: power-of-two scales applied by the tensor core (fp8bs_grouped_gemm_pow2)."""
-    import torch
     M, K = a.shape
     G, N, _ = b.shape
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
-    d_dtype = OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32
+    out, d_dtype = _product_out(out, out_dtype, M, N, a.device)
     fn = fp8bs_grouped_gemm_pow2 if pow2 else fp8bs_grouped_gemm
     fn(a, sa, M, offsets, G, b, sb, out, d_dtype, N, K, stream)
     return out
@@ -472,19 +501,6 @@ def quantize_act_weight(x, w, pow2: bool = False, stream=None):
     fp8bs_quantize_act_weight(x, M, K, x.stride(0), xq, sx, w, N, Kw, w.stride(0), wq, sw,
                               SCALE_POW2 if pow2 else SCALE_ABSMAX, stream)
     return xq, sx, wq, sw
-
-
-def _checked(t, name: str, dtypes, dim: int | None = None, rows: bool = False):
-    """A tensor of one of the given types (and number of dimensions), its last
-    dimension dense; all of it dense unless ``rows``.  The C entry points see
-    pointers only."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not a CUDA tensor")
-    if t.dtype not in dtypes or (dim is not None and t.dim() != dim):
-        raise ValueError(f"{name}: {t.dim()}-d {t.dtype}; expected {dim}-d {' or '.join(map(str, dtypes))}")
-    if (t.stride(-1) != 1 and t.shape[-1] > 1) if rows else not t.is_contiguous():
-        raise ValueError(f"{name}: strides {tuple(t.stride())} of shape {tuple(t.shape)}")
-    return t
 
 
 def _row_stride(t) -> int:
@@ -547,17 +563,6 @@ def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     return q, sf, g
 
 
-def _out_type(dtype):
-    """(torch type, fp8bs_out_dtype) of an output: bfloat16 (default) or float32.
-    The kernels write two or four bytes an element, so any other type is
-    refused before it is allocated."""
-    import torch
-    dtype = dtype or torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"out_dtype: {dtype}; expected torch.bfloat16 or torch.float32")
-    return dtype, OUT_BF16 if dtype == torch.bfloat16 else OUT_F32
-
-
 def dequantize_fp4(q, sf, g=None, fmt: int = FP4_E4M3X16, out_dtype=None, stream=None):
     """The values [M, K] of 4-bit codes, bfloat16 (default) or float32."""
     import torch
@@ -582,15 +587,6 @@ def _fp4_operand(t, name: str, fmt: int, dim: int):
     return q, sf, g
 
 
-def _fp4_product_out(out, out_dtype, M, N, device):
-    import torch
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=device)
-    if tuple(_checked(out, "out", (torch.bfloat16, torch.float32), 2).shape) != (M, N):
-        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(M, N)}")
-    return out, OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32
-
-
 def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
     """D = A B^T of 4-bit operands; a = (q [M, K/2], sf, g) and b = (q [N, K/2], sf, g) as
     quantize_fp4 returns them."""
@@ -598,7 +594,7 @@ def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None
     M, N, K = qa.shape[0], qb.shape[0], 2 * qa.shape[1]
     if qb.shape[1] != qa.shape[1]:
         raise ValueError(f"K differs: {K} and {2 * qb.shape[1]}")
-    out, d_dtype = _fp4_product_out(out, out_dtype, M, N, qa.device)
+    out, d_dtype = _product_out(out, out_dtype, M, N, qa.device)
     fp8bs_gemm_fp4(qa, sfa, ga, qb, sfb, gb, fmt, out, d_dtype, M, N, K, stream)
     return out
 
@@ -612,7 +608,7 @@ def grouped_gemm_fp4(a, offsets, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=
     G, N, _ = qb.shape
     if qb.shape[2] != qa.shape[1] or _checked(offsets, "offsets", (torch.int32,), 1).shape[0] != G + 1:
         raise ValueError(f"a {tuple(qa.shape)}, b {tuple(qb.shape)} and {offsets.shape[0]} offsets do not fit")
-    out, d_dtype = _fp4_product_out(out, out_dtype, M, N, qa.device)
+    out, d_dtype = _product_out(out, out_dtype, M, N, qa.device)
     fp8bs_grouped_gemm_fp4(qa, sfa, ga, M, offsets, G, qb, sfb, gb, fmt, out, d_dtype, N, K, stream)
     return out
 

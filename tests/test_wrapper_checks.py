@@ -49,3 +49,34 @@ def test_dequantize_writes_float32_or_bfloat16_only(launched, dtype, fmt):
     for dtype in (None, torch.bfloat16, torch.float32):
         assert fp8bs.dequantize_fp4(q, sf, g, fmt, out_dtype=dtype).shape == (5, 128)
     assert launched == ["fp8bs_dequantize_fp4"] * 3
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_products_write_float32_or_bfloat16_only(launched, grouped, pow2):
+    """An output of another type, of another shape or with gaps between its rows is refused."""
+    M, N, K = 128, 256, 128
+    a, sa = claim(torch.zeros((M, K), dtype=torch.uint8)), claim(torch.zeros((K // 128, M)))
+    b, sb = claim(torch.zeros((N, K), dtype=torch.uint8)), claim(torch.zeros((N // 128, K // 128)))
+    offsets = claim(torch.tensor([0, M], dtype=torch.int32))
+
+    def call(**kw):
+        if grouped:
+            return fp8bs.grouped_gemm(a, sa, offsets, b[None], sb[None], pow2=pow2, **kw)
+        return fp8bs.gemm(a, sa, b, sb, pow2=pow2, **kw)
+
+    for dtype in (torch.float16, torch.uint8, torch.float64):
+        with pytest.raises(ValueError):
+            call(out_dtype=dtype)
+        with pytest.raises(ValueError):
+            call(out=claim(torch.zeros((M, N), dtype=dtype)))
+    for out in (torch.zeros((M, N - 8)), torch.zeros((M - 1, N)), torch.zeros((M, 2 * N))[:, :N]):
+        with pytest.raises(ValueError):
+            call(out=claim(out))
+    with pytest.raises(ValueError):
+        call(out=torch.zeros((M, N)))
+    assert launched == []
+    for kw in ({}, dict(out_dtype=torch.float32), dict(out=claim(torch.zeros((M, N)))),
+               dict(out=claim(torch.zeros((M, N), dtype=torch.bfloat16)))):
+        assert call(**kw).shape == (M, N)
+    assert len(launched) == 4
