@@ -657,9 +657,9 @@ def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None,
 
 def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, seq=None, normalize: bool = True,
                        scale: float = 1.0, alpha: float = 0.0, counts=None, tokens=None, dloss=None, stream=None):
-    """Gradient of moe_route's weights (dw [T, k]) and balance loss (dloss [1]
-    with counts and tokens; None leaves the loss out) with respect to the
-    logits, in their type."""
+    """Gradient of moe_route's weights (dw [T, k]) and balance loss (dloss, one
+    float32, with moe_route's counts [S, E] and tokens [S]; None leaves the
+    loss out) with respect to the logits, in their type."""
     import torch
     _route_inputs(logits, None, valid, seq)
     T, E = logits.shape
@@ -667,9 +667,13 @@ def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, 
     if _checked(idx, "idx", (torch.int32,), 2).shape != _checked(dw, "dw", (torch.float32,), 2).shape or idx.shape[0] != T:
         raise ValueError(f"idx {tuple(idx.shape)} and dw {tuple(dw.shape)}: one row per token each")
     if dloss is not None:
-        _checked(dloss, "dloss", (torch.float32,))
-        if tuple(_checked(counts, "counts", (torch.int32,), 2).shape) != (S, E) or tokens.shape[0] != S:
-            raise ValueError("counts and tokens: those of moe_route")
+        if _checked(dloss, "dloss", (torch.float32,)).numel() != 1:
+            raise ValueError(f"dloss: {dloss.numel()} values; expected one")
+        if counts is None or tokens is None:
+            raise ValueError("dloss: needs moe_route's counts and tokens")
+        if (tuple(_checked(counts, "counts", (torch.int32,), 2).shape) != (S, E)
+                or tuple(_checked(tokens, "tokens", (torch.int32,), 1).shape) != (S,)):
+            raise ValueError(f"counts {tuple(counts.shape)} and tokens {tuple(tokens.shape)}: expected {(S, E)} and {(S,)}")
     dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     fp8bs_moe_route_backward(logits, IN_BF16 if logits.dtype == torch.bfloat16 else IN_F32, T, E, _row_stride(logits),
                              score, valid, seq, S, idx.shape[1], normalize, scale, alpha, idx, counts, tokens, dw,

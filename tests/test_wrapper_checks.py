@@ -80,3 +80,24 @@ def test_products_write_float32_or_bfloat16_only(launched, grouped, pow2):
                dict(out=claim(torch.zeros((M, N), dtype=torch.bfloat16)))):
         assert call(**kw).shape == (M, N)
     assert len(launched) == 4
+
+
+def test_router_gradient_checks_what_the_loss_reads(launched):
+    """counts, tokens and dloss are read as int32 [S, E], int32 [S] and one float32."""
+    T, E, k, S = 6, 16, 2, 3
+    z, seq = claim(torch.zeros((T, E))), claim(torch.tensor([0, 2, 4, T], dtype=torch.int32))
+    idx, dw = claim(torch.zeros((T, k), dtype=torch.int32)), claim(torch.zeros((T, k)))
+    good = dict(seq=seq, counts=claim(torch.ones((S, E), dtype=torch.int32)), tokens=claim(torch.ones(S, dtype=torch.int32)),
+                dloss=claim(torch.ones(1)))
+    for bad in (dict(tokens=good["tokens"].long()), dict(tokens=torch.ones(S, dtype=torch.int32)),
+                dict(tokens=claim(torch.ones(2 * S, dtype=torch.int32))[::2]), dict(tokens=good["tokens"][:2]),
+                dict(tokens=good["tokens"][:, None]), dict(tokens=None), dict(counts=None),
+                dict(counts=good["counts"].float()), dict(counts=good["counts"][:2]), dict(counts=good["counts"][:, :15]),
+                dict(dloss=claim(torch.ones(0))), dict(dloss=claim(torch.ones(2))), dict(dloss=claim(torch.ones(1).double())),
+                dict(dloss=torch.ones(1))):
+        with pytest.raises(ValueError):
+            fp8bs.moe_route_backward(z, idx, dw, **{**good, **bad})
+    assert launched == []
+    for dloss in (good["dloss"], claim(torch.tensor(1.0)), None):
+        assert fp8bs.moe_route_backward(z, idx, dw, **{**good, "dloss": dloss}).shape == (T, E)
+    assert fp8bs.moe_route_backward(z, idx, dw, seq=seq).shape == (T, E)
