@@ -239,6 +239,8 @@ def moe_layer_fp4(x, logits, experts, k: int, fmt: int = 0, score: int = 0, bias
     and balance loss that moe_route_backward takes.  Every launch is on the
     current stream; nothing is read back."""
     from . import grouped_gemm_fp4, moe_layout, moe_route, quantize_fp4, swiglu_quantize_fp4
+    if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and logits {tuple(logits.shape)}: one row per token each")
     gate_up, down = experts
     route = moe_route(logits, k, score, bias=bias, valid=valid, seq=seq, scale=scale, alpha=alpha)
     offsets, row_token, row_of = moe_layout(route[0], logits.shape[1])

@@ -101,3 +101,15 @@ def test_router_gradient_checks_what_the_loss_reads(launched):
     for dloss in (good["dloss"], claim(torch.tensor(1.0)), None):
         assert fp8bs.moe_route_backward(z, idx, dw, **{**good, "dloss": dloss}).shape == (T, E)
     assert fp8bs.moe_route_backward(z, idx, dw, seq=seq).shape == (T, E)
+
+
+@pytest.mark.parametrize("rows", [5, 7])
+def test_layer_takes_one_row_of_logits_per_token(launched, rows):
+    """Missing tokens became rows of zeros, surplus ones were dropped."""
+    from fp8_fine_grained_fp8bs_gb300 import moe
+    T, E, H, I, fmt = 6, 4, 64, 64, 0
+    experts = _codes(2 * I, H, fmt, E), _codes(H, I, fmt, E)
+    x, z = claim(torch.zeros((rows, H), dtype=torch.bfloat16)), claim(torch.zeros((T, E)))
+    with pytest.raises(ValueError):
+        moe.moe_layer_fp4(x, z, experts, 2, fmt)
+    assert launched == []
