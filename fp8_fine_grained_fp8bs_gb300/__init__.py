@@ -527,10 +527,12 @@ def quantize_fp4(x, fmt: int = FP4_E4M3X16, rows=None, stream=None):
     (contiguous).  Returns (q [..., K/2] uint8, two E2M1 codes a byte; sf uint8,
     the scales in 512-byte blocks of 128 rows; g float32, a scale per row, None
     for FP4_UE8M0X32).  ``rows``: int32 [M'], quantise x[rows[i]] as row i (a
-    row of zeros where rows[i] < 0)."""
+    row of zeros where rows[i] < 0); x is a matrix then."""
     import torch
     K = x.shape[-1]
     if x.dim() == 3:
+        if rows is not None:
+            raise ValueError("rows: picks rows of a matrix [M, K], not of expert weights")
         _checked(x, "x", (torch.bfloat16,), 3)
         G, N, _ = x.shape
         q, sf, g = _fp4_outputs((G, N), K, fmt, x.device)

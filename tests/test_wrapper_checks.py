@@ -113,3 +113,13 @@ def test_layer_takes_one_row_of_logits_per_token(launched, rows):
     with pytest.raises(ValueError):
         moe.moe_layer_fp4(x, z, experts, 2, fmt)
     assert launched == []
+
+
+@pytest.mark.parametrize("N", [128, 72])
+def test_quantize_gathers_rows_of_a_matrix_only(launched, N):
+    """``rows`` was ignored for expert weights [G, N, K]."""
+    w = claim(torch.zeros((2, N, 64), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        fp8bs.quantize_fp4(w, rows=claim(torch.zeros(3, dtype=torch.int32)))
+    assert launched == []
+    assert fp8bs.quantize_fp4(w)[0].shape == (2, N, 32)
