@@ -558,6 +558,8 @@ def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     import torch
     _checked(h, "h", (torch.bfloat16,), 2, rows=True)
     M, two_i = h.shape
+    if two_i % 2 != 0:
+        raise ValueError(f"h: {two_i} columns; expected as many of the gate as of up")
     if live is not None and _checked(live, "live", (torch.int32,), 1).shape[0] != M:
         raise ValueError("live: one value per row of h")
     q, sf, g = _fp4_outputs((M,), two_i // 2, fmt, h.device)

@@ -123,3 +123,12 @@ def test_quantize_gathers_rows_of_a_matrix_only(launched, N):
         fp8bs.quantize_fp4(w, rows=claim(torch.zeros(3, dtype=torch.int32)))
     assert launched == []
     assert fp8bs.quantize_fp4(w)[0].shape == (2, N, 32)
+
+
+def test_swiglu_takes_two_halves(launched):
+    """A strided view of odd width lost its last column."""
+    wide = claim(torch.zeros((3, 136), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        fp8bs.swiglu_quantize_fp4(wide[:, :129])
+    assert launched == []
+    assert fp8bs.swiglu_quantize_fp4(wide[:, :128])[0].shape == (3, 32)
