@@ -9,11 +9,17 @@ missing or fails to load, every call raises.
 
 The functions named ``fp8bs_*`` mirror the C entry points one to one and
 take tensors or raw device pointers.  ``quantize_act``, ``quantize_weight``,
-``gemm`` and ``grouped_gemm`` additionally allocate their outputs with torch.
+``gemm`` and ``grouped_gemm`` additionally allocate their outputs with torch,
+as the 4-bit and routing functions do.  ``stream`` (a torch stream or a handle)
+is the one launched on, torch's current stream by default; outputs belong to
+it, and reading them on another one takes the caller's wait, as with any
+tensor computed on another stream.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -363,6 +369,35 @@ fp4_scale_bytes = fp8bs_fp4_scale_bytes
 
 # ------------------------------------------------------ allocating conveniences
 
+def _allocates_on_its_stream(fn):
+    """For a function that allocates tensors and launches on ``stream``: where
+    that is not torch's current stream, the tensors are allocated for it.  A
+    block that the current stream freed may still be written by work queued
+    there, which orders nothing on another stream; and scratch freed on return
+    goes back to the stream that still uses it.  The outputs are then marked as
+    used on the current stream too, where the caller most likely reads them, so
+    that the allocator keeps them for what is queued there when they are freed."""
+    place = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[place] if len(args) > place else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        import torch
+        current, handle = torch.cuda.current_stream(), _stream(stream)
+        if handle == current.cuda_stream:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)):
+            out = fn(*args, **kwargs)
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(current)
+        return out
+
+    return call
+
+
 def _checked(t, name: str, dtypes, dim: int | None = None, rows: bool = False):
     """A tensor of one of the given types (and number of dimensions), its last
     dimension dense; all of it dense unless ``rows``.  The C entry points see
@@ -398,6 +433,7 @@ def _product_out(out, out_dtype, M, N, device):
     return out, _out_type(out.dtype)[1]
 
 
+@_allocates_on_its_stream
 def quantize_act(x, transposed: bool = False, pow2: bool = False, stream=None):
     """x: [M, K] bfloat16 CUDA tensor (row-major, K % 128 == 0).
 
@@ -417,6 +453,7 @@ def quantize_act(x, transposed: bool = False, pow2: bool = False, stream=None):
     return (xq, sx, xq_t, sx_t) if transposed else (xq, sx)
 
 
+@_allocates_on_its_stream
 def quantize_weight(w, transposed: bool = False, pow2: bool = False, stream=None):
     """w: [N, K] bfloat16 CUDA tensor.  Returns (wq, sw[, wq_t, sw_t])."""
     import torch
@@ -431,6 +468,7 @@ def quantize_weight(w, transposed: bool = False, pow2: bool = False, stream=None
     return (wq, sw, wq_t, sw_t) if transposed else (wq, sw)
 
 
+@_allocates_on_its_stream
 def swiglu_quantize(h, pow2: bool = False, stream=None):
     """h: [M, 2I] bfloat16 CUDA tensor (gate | up).  Returns (q [M, I] uint8,
     s [I/128, M] float32): the 1x128 quantisation of BF16(silu(gate) * up)."""
@@ -443,6 +481,7 @@ def swiglu_quantize(h, pow2: bool = False, stream=None):
     return q, s
 
 
+@_allocates_on_its_stream
 def requant_1x128_to_128x1(xq, sx, pow2: bool = True, stream=None):
     """Re-tile 1x128-quantised activations (xq [M,K] uint8, sx [K/128, M]) into
     128x1 groups: returns (xq_t [K,M] uint8, sx_t [M/128, K] float32)."""
@@ -454,6 +493,7 @@ def requant_1x128_to_128x1(xq, sx, pow2: bool = True, stream=None):
     return xq_t, sx_t
 
 
+@_allocates_on_its_stream
 def gemm(a, sa, b, sb, sb_kind: int = SCALE_BLOCK128x128, out_dtype=None, out=None, accumulate: bool = False,
          stream=None, pow2: bool = False):
     """D = A B^T with per-128-K-block scales; A [M,K], B [N,K] uint8 E4M3.
@@ -466,6 +506,7 @@ def gemm(a, sa, b, sb, sb_kind: int = SCALE_BLOCK128x128, out_dtype=None, out=No
     return out
 
 
+@_allocates_on_its_stream
 def grouped_gemm(a, sa, offsets, b, sb, out_dtype=None, out=None, stream=None, pow2: bool = False):
     """Per-expert D rows = A rows of the expert x B[g]^T; offsets: int32 CUDA tensor [G+1].
     ``pow2``: power-of-two scales applied by the tensor core (fp8bs_grouped_gemm_pow2)."""
@@ -477,6 +518,7 @@ def grouped_gemm(a, sa, offsets, b, sb, out_dtype=None, out=None, stream=None, p
     return out
 
 
+@_allocates_on_its_stream
 def diag_gemm_unpromoted(a, b, stream=None):
     """Diagnostic: FP32 D = A B^T of E4M3 codes (A [M,K], B [N,K] uint8) with all
     of K accumulated by the tensor core alone, no promotion and no scales."""
@@ -488,6 +530,7 @@ def diag_gemm_unpromoted(a, b, stream=None):
     return out
 
 
+@_allocates_on_its_stream
 def quantize_act_weight(x, w, pow2: bool = False, stream=None):
     """X [M,K] and W [N,Kw] bfloat16 CUDA tensors quantised in one launch:
     returns (xq, sx [K/128, M], wq, sw [N/128, Kw/128])."""
@@ -507,13 +550,6 @@ def _row_stride(t) -> int:
     return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
 
 
-def _used_on(t, stream):
-    """Keeps a scratch tensor's memory until the work queued on ``stream`` is done."""
-    if stream is not None:
-        import torch
-        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-
-
 def _fp4_outputs(lead, K, fmt, device):
     import torch
     q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=device)
@@ -522,6 +558,7 @@ def _fp4_outputs(lead, K, fmt, device):
     return q, sf, g
 
 
+@_allocates_on_its_stream
 def quantize_fp4(x, fmt: int = FP4_E4M3X16, rows=None, stream=None):
     """x: [M, K] bfloat16 CUDA tensor (K % 64 == 0), or expert weights [G, N, K]
     (contiguous).  Returns (q [..., K/2] uint8, two E2M1 codes a byte; sf uint8,
@@ -551,6 +588,7 @@ def quantize_fp4(x, fmt: int = FP4_E4M3X16, rows=None, stream=None):
     return q, sf, g
 
 
+@_allocates_on_its_stream
 def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     """h: [M, 2I] bfloat16 CUDA tensor (gate | up).  Returns the 4-bit codes and
     scales of BF16(silu(gate) * up), as quantize_fp4; rows with live[i] < 0
@@ -567,6 +605,7 @@ def swiglu_quantize_fp4(h, fmt: int = FP4_E4M3X16, live=None, stream=None):
     return q, sf, g
 
 
+@_allocates_on_its_stream
 def dequantize_fp4(q, sf, g=None, fmt: int = FP4_E4M3X16, out_dtype=None, stream=None):
     """The values [M, K] of 4-bit codes, bfloat16 (default) or float32."""
     import torch
@@ -591,6 +630,7 @@ def _fp4_operand(t, name: str, fmt: int, dim: int):
     return q, sf, g
 
 
+@_allocates_on_its_stream
 def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
     """D = A B^T of 4-bit operands; a = (q [M, K/2], sf, g) and b = (q [N, K/2], sf, g) as
     quantize_fp4 returns them."""
@@ -603,6 +643,7 @@ def gemm_fp4(a, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None
     return out
 
 
+@_allocates_on_its_stream
 def grouped_gemm_fp4(a, offsets, b, fmt: int = FP4_E4M3X16, out_dtype=None, out=None, stream=None):
     """Per-expert D rows = A rows of the expert x B[g]^T; offsets int32 CUDA tensor [G+1], b as
     quantize_fp4 returns it for weights [G, N, K]."""
@@ -629,6 +670,7 @@ def _route_inputs(logits, bias, valid, seq):
         _checked(seq, "seq", (torch.int32,), 1)
 
 
+@_allocates_on_its_stream
 def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None, seq=None, normalize: bool = True,
               scale: float = 1.0, alpha: float | None = None, stream=None):
     """Expert choice of each token: logits [T, E] float32 or bfloat16.  Returns
@@ -655,10 +697,10 @@ def moe_route(logits, k: int, score: int = SCORE_SOFTMAX, bias=None, valid=None,
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     fp8bs_moe_route(logits, in_dtype, T, E, ld, score, bias, valid, seq, S, k, normalize, scale, alpha, idx, w, counts,
                     tokens, loss, ws, n, stream)
-    _used_on(ws, stream)
     return idx, w, counts, tokens, loss
 
 
+@_allocates_on_its_stream
 def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, seq=None, normalize: bool = True,
                        scale: float = 1.0, alpha: float = 0.0, counts=None, tokens=None, dloss=None, stream=None):
     """Gradient of moe_route's weights (dw [T, k]) and balance loss (dloss, one
@@ -685,6 +727,7 @@ def moe_route_backward(logits, idx, dw, score: int = SCORE_SOFTMAX, valid=None, 
     return dlogits
 
 
+@_allocates_on_its_stream
 def moe_layout(idx, E: int, stream=None):
     """Row layout of the choices idx [T, k] among E experts: (offsets [E + 1], row_token
     [rows], row_of [T, k]), int32, as fp8bs_moe_layout describes them."""
@@ -697,5 +740,4 @@ def moe_layout(idx, E: int, stream=None):
     n = moe_layout_workspace_bytes(T, k, E)
     ws = torch.empty(n, dtype=torch.uint8, device=idx.device)
     fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, n, stream)
-    _used_on(ws, stream)
     return offsets, row_token, row_of
