@@ -118,24 +118,103 @@ __device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int g,
   for (int i = 0; i < NL; ++i) z[i] = __uint_as_float(bits[i] << shift);
 }
 
-// e^x and 1 / x by the hardware's base-2 exponential and reciprocal, for the
-// scores that only enter sums and gradients (relative error below 2^-21 where
-// the result matters); the weights and biased keys use expf and IEEE division.
-__device__ __forceinline__ float fast_exp(float x) {
+// Two float32 operations in one instruction, each rounded as its scalar form.
+#define FP8BS_F32X2_2(name, op)                                                                       \
+  __device__ __forceinline__ float2 name(float2 a, float2 b) {                                        \
+    float2 d;                                                                                         \
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t" op              \
+        " z, x, y;\n\tmov.b64 {%0, %1}, z;\n}\n"                                                      \
+        : "=f"(d.x), "=f"(d.y)                                                                        \
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                    \
+    return d;                                                                                         \
+  }
+FP8BS_F32X2_2(add2, "add.rn.f32x2")
+FP8BS_F32X2_2(mul2, "mul.rn.f32x2")
+#undef FP8BS_F32X2_2
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 w, x, y, z;\n\tmov.b64 w, {%2, %3};\n\tmov.b64 x, {%4, %5};\n\tmov.b64 y, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, w, x, y;\n\tmov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float ex2(float t) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
+// 1 / x within one ulp, for the scores that only enter sums and gradients and
+// for their sums; the weights and the keys of the choice are divided.  (Rounded
+// correctly, __frcp_rn: gradient of 131072 x 256 68.7 us against 65.6.)
 __device__ __forceinline__ float fast_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// e^x for x <= 0, as 2^t (1 + d) with t = fl(x log2 e) and d = x - t ln 2, at most
+// |x| 2^-24: the instruction's 2^-22 of relative error and a rounding, at any x.
+// (t alone loses that |x| 2^-24: 2^-19.5 for a logit 22 to 30 below the top.)  d
+// is what cancellation leaves of an exact product, with ln 2 in two parts (Cody
+// and Waite, Software Manual for the Elementary Functions, 1980).  NaN for
+// NaN, -inf and x whose t overflows: the callers' maximum with 0 makes it 0.
+// Two at a time as costly as one hardware exponential was (131072 x 256 with
+// statistics and biased sigmoids 79.4 us, 79.9 before; the gradient 64.4 and
+// 64.0; with expf 83.2 and 73.3).
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2Hi = 0.693147182464599609375f;            // fl(ln 2)
+constexpr float kLn2Lo = -1.904654299957767e-9f;              // fl(ln 2 - kLn2Hi)
+__device__ __forceinline__ float2 exp_pair(float2 x) {
+  const float2 t = mul2(x, both(kLog2e));
+  const float2 d = fma2(t, both(-kLn2Lo), fma2(t, both(-kLn2Hi), x));
+  const float2 p = make_float2(ex2(t.x), ex2(t.y));
+  return fma2(p, d, p);
+}
+__device__ __forceinline__ float exp_one(float x) {
+  const float t = x * kLog2e;
+  const float p = ex2(t);
+  return fmaf(p, fmaf(t, -kLn2Lo, fmaf(t, -kLn2Hi, x)), p);
+}
+
+// f(pair) over NL values two at a time; a single value is paired with itself.
+template <int NL, typename F>
+__device__ __forceinline__ void in_pairs(float (&v)[NL], F f) {
+#pragma unroll
+  for (int i = 0; i < NL; i += 2) {
+    const float2 r = f(make_float2(v[i], v[i + 1 < NL ? i + 1 : i]));
+    v[i] = r.x;
+    if (i + 1 < NL) v[i + 1] = r.y;
+  }
+}
+
 // sigmoid(z) is 1 - q or q, with q = e^-|z| / (1 + e^-|z|) <= 1/2, which cannot
 // overflow and loses nothing to cancellation; its derivative is q (1 - q).
-__device__ __forceinline__ float sigmoid_part(float z) {
-  const float t = fast_exp(-fabsf(z));
+// 0 where z is not eligible.  Relative error below 2^-21.4 (exponential,
+// reciprocal, sum and product).
+__device__ __forceinline__ float part_of(float e) {
+  const float t = fmaxf(e, 0.0f);
   return t * fast_rcp(1.0f + t);
+}
+__device__ __forceinline__ float sigmoid_part(float z) { return part_of(exp_one(-fabsf(z))); }
+__device__ __forceinline__ float2 sigmoid_parts(float2 z) {
+  const float2 e = exp_pair(make_float2(-fabsf(z.x), -fabsf(z.y)));
+  return make_float2(part_of(e.x), part_of(e.y));
+}
+
+// sigmoid of two logits for the statistics, negated: 1 / (1 + 2^t), moved by
+// the exponent's rest: s' = s - s (1 - s) d.  Half of t is what d is computed
+// from, so that nothing is infinite but 2^t, for any finite z.  NaN where z is
+// not eligible (z * 0 is NaN for NaN and the infinities).
+__device__ __forceinline__ float2 minus_sigmoid_pair(float2 z) {
+  const float2 half = mul2(z, both(-0.5f * kLog2e));
+  const float2 t = add2(half, half);
+  const float2 d = fma2(half, both(2.0f * kLn2Lo), fma2(half, both(2.0f * kLn2Hi), z));   // of opposite sign
+  const float2 n = fma2(make_float2(ex2(t.x), ex2(t.y)), both(-1.0f), both(-1.0f));
+  const float2 s = make_float2(fast_rcp(n.x), fast_rcp(n.y));
+  return fma2(z, both(0.0f), fma2(fma2(s, s, s), d, s));
 }
 
 // The sequences of a launch: [seq[s], seq[s + 1]) covers 0 .. T in order.
@@ -275,29 +354,31 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_k
       // Scores of all experts for the statistics, for softmax weights that are
       // not normalised over the chosen, and (approximate) for biased keys.
       const bool all = kStats || biased || (kScore == 0 && !a.normalize);
-      float inv = 1.0f;
+      float total = 1.0f;
       uint32_t most = 0;
       int n = 0;
       if (!biased) n = candidates<W, NL>(v, a.k, false, lane, list, most);
       const float top = from_key(most);   // softmax; not used where most is 0
       if (all) {
+        if (kScore == 1 && !kStats) {
+          // keys that narrow the candidates, with a margin
+#pragma unroll
+          for (int i = 0; i < NL; ++i) v[i] = fmaf(v[i], 0.0f, fast_rcp(1.0f + ex2(v[i] * -kLog2e)));
+        } else {
+          in_pairs(v, [&](float2 z) { return kScore == 0 ? exp_pair(add2(z, both(-top))) : minus_sigmoid_pair(z); });
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-          if (kScore == 0) {
-            v[i] = fast_exp(v[i] - top);
-          } else {
-            // z * 0 is NaN for NaN and the infinities: not eligible
-            v[i] = fmaf(v[i], 0.0f, fast_rcp(1.0f + fast_exp(-v[i])));
-          }
+          if (kScore == 1 && kStats) v[i] = -v[i];
           sum += fmaxf(v[i], 0.0f);   // 0 for NaN
         }
-        inv = fast_rcp(group_sum<W>(sum) + kScoreEps);
+        total = group_sum<W>(sum) + kScoreEps;
         if (kStats) {
+          const float inv = fast_rcp(total);
 #pragma unroll
           for (int i = 0; i < NL; ++i) acc[i] = fmaf(fmaxf(v[i], 0.0f), inv, acc[i]);
         }
-        if (kScore == 0 && most == 0u) inv = 1.0f;
       }
       if (biased) {
 #pragma unroll
@@ -383,12 +464,12 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_k
 #pragma unroll
       for (int r = 0; r < kPerLane; ++r) {
         if (slot[r] < a.k) {
-          if (kScore == 0) sm[r] = expf(zm[r] - top) * (a.normalize ? 1.0f : inv);
+          if (kScore == 0) sm[r] = expf(zm[r] - top);
           chosen += sm[r];
         }
       }
-      float unit = a.scale;
-      if (a.normalize) unit /= group_sum<W>(chosen) + kScoreEps;
+      // a sigmoid is a weight as it stands
+      const float unit = a.normalize ? a.scale / (group_sum<W>(chosen) + kScoreEps) : kScore == 0 ? a.scale / total : a.scale;
       if (here) {
 #pragma unroll
         for (int r = 0; r < kPerLane; ++r) {
@@ -571,16 +652,19 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
 #pragma unroll
         for (int o = W / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
       }
+      float q[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) q[i] = v[i];
+      in_pairs(q, [&](float2 z) { return kScore == 0 ? exp_pair(add2(z, both(-top))) : sigmoid_parts(z); });
       float sum = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         float score;
         if (kScore == 0) {
-          v[i] = score = fmaxf(fast_exp(v[i] - top), 0.0f);
+          v[i] = score = fmaxf(q[i], 0.0f);   // 0 for NaN
         } else {
-          const float q = fmaxf(sigmoid_part(v[i]), 0.0f);
-          score = v[i] >= 0.0f ? 1.0f - q : q;
-          v[i] = v[i] >= 0.0f ? q : -q;
+          score = v[i] >= 0.0f ? 1.0f - q[i] : q[i];
+          v[i] = v[i] >= 0.0f ? q[i] : -q[i];
         }
         sum += score;
         dot = fmaf(coef[i], score, dot);
@@ -589,7 +673,7 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
       float ws = 0.0f, slope = 0.0f;
       if (eligible(zm)) {
         if (kScore == 0) {
-          ws = fast_exp(zm - top) * inv;
+          ws = fmaxf(exp_one(zm - top), 0.0f) * inv;
         } else {
           const float q = sigmoid_part(zm);
           ws = zm >= 0.0f ? 1.0f - q : q;
@@ -605,9 +689,13 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
       if (kScore == 0) dot = fmaf(dws, ws, dot);
       dot = group_sum<W>(dot);
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const float q = fabsf(v[i]);
-        v[i] = (coef[i] - dot) * inv * (kScore == 0 ? q : q * (1.0f - q));
+      for (int i = 0; i < NL; i += 2) {   // (coef - dot) inv q, sigmoid: times 1 - q
+        const int j = i + 1 < NL ? i + 1 : i;
+        const float2 q = make_float2(fabsf(v[i]), fabsf(v[j]));
+        float2 x = mul2(mul2(add2(make_float2(coef[i], coef[j]), both(-dot)), both(inv)), q);
+        if (kScore == 1) x = fma2(x, make_float2(-q.x, -q.y), x);
+        v[i] = x.x;
+        v[j] = x.y;
       }
       if (here) {
         if (a.bf16) {
