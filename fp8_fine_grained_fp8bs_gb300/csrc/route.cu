@@ -695,11 +695,17 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
       }
       float dws = a.scale * dw;
       if (a.normalize) {
+        // d_j = scale / sum (dw_j - sum_l w_l dw_l), the w_l summing to one but for
+        // the guard's share of the sum: taken from the first choice's dw, which
+        // leaves nothing of a part that all dw share.  (From dw itself: a single
+        // choice kept 2^-23 of its dw, more than the loss's gradient has digits.)
+        const float first = __shfl_sync(kFull, dw, lane & ~(W - 1));
         const float r = fast_rcp(group_sum<W>(ws) + kScoreEps);
-        dws = a.scale * r * (dw - group_sum<W>(dw * ws) * r);
+        const float d = dw - first, guard = kScoreEps * r;
+        dws = a.scale * r * (d - group_sum<W>(d * ws) * r + (guard > 1e-7f ? first * guard : 0.0f));
       }
       dot *= inv;
-      if (kScore == 0) dot = fmaf(dws, ws, dot);
+      if (kScore == 0 && !a.normalize) dot = fmaf(dws, ws, dot);   // normalised: these add up to zero
       dot = group_sum<W>(dot);
 #pragma unroll
       for (int i = 0; i < NL; i += 2) {   // (coef - dot) inv q, sigmoid: times 1 - q
