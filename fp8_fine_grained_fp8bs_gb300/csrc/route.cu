@@ -625,15 +625,22 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
     const int64_t end = min(hi, sequence_end(a, s));
     if (end <= lo) break;   // invalid sequences
     const int32_t* counts = a.dloss == nullptr ? nullptr : a.counts + static_cast<int64_t>(s) * a.E;
-    float unit = 0.0f;   // g_i per count
+    // g_i = count_i unit, taken from that of the mean count: the p_l sum to one
+    // (but for the guard's share), so a part that all g_l share has no effect, and
+    // the counts' differences are exact.  (From g_i itself the sum of p_l g_l kept
+    // 2^-23 of it, 1.5e-3 of the gradient of loads a thousandth apart.)
+    float unit = 0.0f;
+    int mean = 0;
     if (counts != nullptr) {
-      const float per = 1.0f / static_cast<float>(max(a.tokens[s], 1));
+      const float tokens = static_cast<float>(max(a.tokens[s], 1)), per = 1.0f / tokens;
       unit = up * per * per;
+      mean = __float2int_rn(tokens * static_cast<float>(a.k) / static_cast<float>(a.E));
     }
-    float coef[NL];      // g_i
+    const float guard = kScore == 0 ? 0.0f : kScoreEps * (static_cast<float>(mean) * unit);   // softmax: the sum is 1 or more
+    float coef[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i)
-      coef[i] = counts != nullptr && W * i + g < a.E ? static_cast<float>(counts[W * i + g]) * unit : 0.0f;
+      coef[i] = counts != nullptr && W * i + g < a.E ? static_cast<float>(counts[W * i + g] - mean) * unit : 0.0f;
     // the mask, the choice and its gradient are read a step ahead, so that no
     // load of a step waits for another
     bool valid_next = false;
@@ -707,6 +714,7 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
       dot *= inv;
       if (kScore == 0 && !a.normalize) dot = fmaf(dws, ws, dot);   // normalised: these add up to zero
       dot = group_sum<W>(dot);
+      if (kScore == 1) dot = fmaf(-guard, inv, dot);
 #pragma unroll
       for (int i = 0; i < NL; i += 2) {   // (coef - dot) inv q, sigmoid: times 1 - q
         const int j = i + 1 < NL ? i + 1 : i;
@@ -731,7 +739,7 @@ __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_bac
       }
       __syncwarp();   // orders the stores of one address
       if (mine >= 0) {
-        const float gm = counts != nullptr ? static_cast<float>(__ldg(counts + mine)) * unit : 0.0f;
+        const float gm = counts != nullptr ? static_cast<float>(__ldg(counts + mine) - mean) * unit : 0.0f;
         const float dz = kScore == 0 ? ws * (gm + dws - dot) : (dws + (gm - dot) * inv) * slope;
         if (a.bf16)
           static_cast<__nv_bfloat16*>(a.dlogits)[t * a.ldd + mine] = __float2bfloat16_rn(dz);

@@ -2,12 +2,14 @@
 
 Normalised weights do not change when all chosen scores grow together, so a part that all of a token's dw
 share has no effect (with one choice, all of dw), and under softmax scores experts that were not chosen get
-nothing from the weights.  (Up to the 1e-20 that is added to the sums.)  What is left has to be as exact as if the
+nothing from the weights.  The probabilities of the loss sum to one, so a part that all experts' loads share
+has no effect.  (Up to the 1e-20 that is added to the sums.)  What is left has to be as exact as if the
 shared part were not there: differences below 4 x 2^-24 of the larger result, two roundings on either side.
 """
 import numpy as np
 import pytest
 
+from oracle import route
 from _gpu import require_gpu, to_dev, to_host
 from test_route_gpu import _logits
 
@@ -49,3 +51,32 @@ def test_softmax_weights_give_nothing_to_experts_not_chosen(E, k):
     chosen = np.zeros((T, E), bool)
     np.put_along_axis(chosen, to_host(idx).astype(np.int64), True, 1)
     assert np.all(np.abs(dz[~chosen]) <= 1e-18)
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,k", SIZES)
+def test_a_shared_part_of_the_loads_has_no_effect(E, k, score):
+    """Loads of 5000 and a few more or less: the gradient of the few, to 2e-6 of its largest, as the float64 form
+    has it (seven roundings of the sums and products, 2^-24 each, four times over)."""
+    torch, fp8bs = require_gpu()
+    T = 150
+    z = _logits(T, E, E)
+    counts = 5000 + np.random.default_rng(E).integers(-5, 6, (1, E))
+    tokens = np.array([5000 * E // k])
+    none = np.full((T, k), -1, np.int32)
+    got = to_host(fp8bs.moe_route_backward(to_dev(z), to_dev(none), torch.zeros((T, k), device="cuda:0"), score, alpha=0.5,
+                                           counts=to_dev(counts.astype(np.int32)), tokens=to_dev(tokens.astype(np.int32)),
+                                           dloss=torch.ones(1, device="cuda:0")))
+    g = 0.5 * E * counts[0] / k / tokens[0] ** 2
+    ref = np.zeros((T, E))
+    for t in range(T):
+        s, _ = route.scores(z[t].astype(np.float64), score)
+        p = s / s.sum()
+        dp = g - (p * g).sum()
+        ref[t] = p * dp if score == 0 else s * (1 - s) * dp / s.sum()
+    big = np.abs(ref).max(axis=1, keepdims=True)
+    assert np.all(np.abs(got - ref) <= 2e-6 * big), (np.abs(got - ref) / big).max()
+    even = to_host(fp8bs.moe_route_backward(to_dev(z), to_dev(none), torch.zeros((T, k), device="cuda:0"), score, alpha=0.5,
+                                            counts=torch.full((1, E), 5000, dtype=torch.int32, device="cuda:0"),
+                                            tokens=to_dev(tokens.astype(np.int32)), dloss=torch.ones(1, device="cuda:0")))
+    assert np.all(np.abs(even) <= 1e-18)
