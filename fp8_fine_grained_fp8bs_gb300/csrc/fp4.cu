@@ -17,8 +17,9 @@
 // twice, from L2 the second time), its maximum is reduced across the row's
 // warps, and codes and scales leave with 8-byte and 4-byte stores.  [16384][7168]
 // in 48.4 us with E4M3 scales (301 MB, 0.92 of the copy bandwidth) and 42.6 with
-// UE8M0 ones (1.0); the SwiGLU form is bound by instructions (27 an element, expf
-// above all): [8191][2048] in 18.3 us, 0.62 of the copy bandwidth.
+// UE8M0 ones (1.0); the SwiGLU form is bound by instructions (27 an element, 11 of
+// them the plain rows', the rest scalar: expf and the corrected quotient):
+// [8191][2048] in 18.3 us, 0.62 of the copy bandwidth.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -59,8 +60,9 @@ __device__ __forceinline__ int64_t sf_word_offset(int64_t row, int64_t word, int
 // with expf and the IEEE quotient; below -64 (kLow), where 1 adds nothing to
 // e^-gate and e^-gate overflows in the end, gate e^(gate/2) e^(gate/2).
 // The quotient is Markstein's correction of gate * rcp(1 + e^-gate) on negated
-// operands, which keep the sign of a zero; it has the bits of the IEEE division
-// for every BF16 gate from -64 up (checked for all of them).
+// operands, which keep the sign of a zero; for every finite BF16 gate from -64
+// up the result is the IEEE division's (tests/test_fp4_paths_gpu.py goes through
+// them).
 template <bool kLow>
 __device__ __forceinline__ uint32_t swiglu_pair(uint32_t gate, uint32_t up) {
   float v[2];
@@ -163,8 +165,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
 // and y = 1 / b of its row.  amax / b is Markstein's corrected quotient (IBM J.
 // Res. Develop. 34(1), 1990): from a correctly rounded y one correction gives
 // the IEEE quotient wherever the remainder is exact, which holds for every
-// quotient above 2^-10, half the smallest scale (checked for all BF16
-// mantissas of amax and of the row's maximum, 26 binades apart).
+// quotient above 2^-10, half the smallest scale (tests/test_fp4_paths_gpu.py
+// goes through all BF16 mantissas of amax and of the row's maximum, up to 26
+// binades apart).
 template <int kFmt>
 __device__ __forceinline__ uint32_t group_scale(float amax, float g, float b, float y, float& r) {
   if (kFmt == 0) {

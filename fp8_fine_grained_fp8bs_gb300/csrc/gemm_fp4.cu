@@ -23,17 +23,20 @@
 // K (128 bytes, one swizzle row) deep; the last may be shorter: elements past
 // K are zero-filled by TMA and their MMAs are not issued.
 //
-// Large products run 256x256 tiles on CTA pairs (2-SM MMA).  4096x7168x7168
-// takes 67 us (6250 TFLOP/s) with E4M3 scales and 61 (6920) with UE8M0 ones.
+// Large products run 256x256 tiles on CTA pairs (2-SM MMA).  4096x7168x7168 back
+// to back takes 72 us (5850 TFLOP/s) with E4M3 scales; in a run too short for the
+// power limit to lower the clock 67 us (6250), and 61 (6920) with UE8M0 ones.
 // What bounds it, from variants that leave parts out (4864x4096, four tiles a
 // pair, time per stage of four MMAs): the MMAs alone 0.263 us, 545 cycles for
 // 512 of tensor work; with the operands' TMA writes, which share shared
 // memory's bandwidth with the MMA's reads, 0.30; with the scale copies 0.32; and
 // about 10 us a launch outside the stages (start, first loads, accumulators
-// handed over between tiles, the last store).  An MMA of K = 96 would not
-// change the bytes a stage moves through shared memory, which is what the
-// stages are short of.  Two staging boxes per epilogue warp (a stage less in the
-// ring), stores straight from registers and prefetching B into L2 were slower.
+// handed over between tiles, the last store).  So the rate of the K = 64 MMA is
+// the largest part; MMAs of K = 96 were not measured.  A 256-wide tile has one
+// accumulator (two would take all of tensor memory and leave none for scales), so
+// the next tile's MMAs wait until the epilogue has read it.  Two staging boxes per
+// epilogue warp (a stage less in the ring), stores straight from registers and
+// prefetching B into L2 were slower.
 //
 // Grouped products of few rows stream B: 32 experts of [4096][7168], 128 choices,
 // 90 us for 520 MB of DRAM traffic (0.85 of the copy bandwidth).

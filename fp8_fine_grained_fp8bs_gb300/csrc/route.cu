@@ -302,8 +302,8 @@ __device__ __forceinline__ int candidates(const float (&key)[NL], int k, bool sl
 }
 
 // CTAs that an SM should hold, which bounds the registers of a thread (32749
-// tokens of 256 logits: 15.2 us with four CTAs, 18.6 with three; with the
-// statistics' sums four would spill: 36 us against 27).
+// tokens of 256 logits: 15.4 us with four CTAs, 19.3 with three; with the
+// statistics' sums four would spill: 31.2 us against 27.0).
 template <int NL, bool kStats>
 constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? (kStats ? 3 : 4) : 1;
 
@@ -312,12 +312,12 @@ constexpr int kRouteCtas = NL <= 8 ? 4 : NL == 16 ? (kStats ? 3 : 4) : 1;
 // the partial arrays: along the tokens every step from one (chunk, sequence)
 // to the next raises c or s, so the rows are distinct.
 //
-// Bound by instructions (about 290 a token of 256 logits, 430 with statistics
+// Bound by instructions (about 290 a token of 256 logits, 450 with statistics
 // and biased sigmoids, two thirds of the issue slots busy).  131072 tokens: 154
 // us choosing the k experts one by one from all keys, two warp reductions and a
 // pass over the keys each; 86 with candidates, a warp per token; 61 with half a
 // warp, which shares the per-token steps between two tokens (with statistics
-// 166, 108 and 80 us).
+// 166, 108 and 79 us).
 template <int W, int NL, int kScore, bool kStats>
 __global__ void __launch_bounds__(kRouteThreads, kRouteCtas<NL, kStats>) route_kernel(const RouteArgs a) {
   constexpr int kGroups = kRouteThreads / W;          // tokens at a time
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const Rout
 }
 
 // CTAs on an SM, more of them against more registers a thread: 131072 tokens of
-// 256 logits 62.5 us with four, 71.2 with three; of 128 logits (half a warp a
-// token) 43.1 and 38.5.
+// 256 logits 65.6 us with four, 72.4 with three; of 128 logits (half a warp a
+// token) 40.6 and 36.6.
 template <int W, int NL>
 constexpr int kBackwardCtas = NL <= 4 ? 4 : NL == 8 ? (W == 32 ? 4 : 3) : NL == 16 ? 2 : 1;
 
@@ -606,7 +606,7 @@ constexpr int kBackwardCtas = NL <= 4 ? 4 : NL == 8 ? (W == 32 ? 4 : 3) : NL == 
 // Every lane first stores its experts' dz without d_i; the lanes that hold the
 // token's choices then store theirs whole over those k.
 // Reads and writes T E values: 268 MB for 131072 tokens of 256, 40 us at the
-// copy bandwidth; 64 us measured, instructions (about 400 a token) and loads
+// copy bandwidth; 66 us measured, instructions (about 400 a token) and loads
 // waited for in equal parts.
 template <int W, int NL, int kScore>
 __global__ void __launch_bounds__(kRouteThreads, kBackwardCtas<W, NL>) route_backward_kernel(const RouteArgs a) {
@@ -951,7 +951,8 @@ cudaError_t run_route(RouteArgs a, bool backward, cudaStream_t stream) {
 cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
   // Half a warp per token where k lanes can reach the candidates' bound; the
   // backward pass has less to share and needs more registers (131072 tokens of
-  // 256 logits: 66.4 us with half a warp, 63.9 with a whole one).
+  // 256 logits: 66.8 us with half a warp, 65.6 with a whole one; BF16 63.2 and
+  // 65.0).
   if (a.k <= 16) {
     if (a.E <= 16) return run_route<16, 1>(a, backward, stream);
     if (a.E <= 32) return run_route<16, 2>(a, backward, stream);
@@ -966,7 +967,7 @@ cudaError_t pick_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
 }
 
 // Tokens per CTA with statistics: as many CTAs as are resident at once (131072
-// tokens of 128 logits: 51.8 us with 608, 59.1 with 456), and at most 30 + T / 64
+// tokens of 128 logits: 52.5 us with 608, 60.3 with 456), and at most 30 + T / 64
 // (the partial sums stay small beside the logits).
 constexpr int kMaxChunks = 456;
 int64_t stats_chunk(int64_t T, int E) {

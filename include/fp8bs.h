@@ -470,10 +470,14 @@ typedef enum { FP8BS_SCORE_SOFTMAX = 0, FP8BS_SCORE_SIGMOID = 1 } fp8bs_score_ki
  *   loss = alpha / S * sum_q sum_i f_qi P_qi   over the sequences q,
  *     f_qi = E counts[q][i] / (k tokens[q]),  P_qi = sum_t p_i / tokens[q],
  *   tokens[q] the sequence's tokens with an eligible expert (one without any
- *   adds nothing).
+ *   adds nothing).  counts are those of the experts chosen: with a bias, of the
+ *   biased choice, which the bias's own update goes by as well.  (A loss whose
+ *   f counts the k largest scores without the bias differs from this one
+ *   wherever the bias moves a choice.)  Nothing limits a choice to groups of
+ *   experts.
  *
  *   logits [T][ld] float32 or BF16 (fp8bs_in_dtype), E columns.       (in)
- *   bias   [E] float32 or NULL.  valid [T] bytes or NULL.              (in)
+ *   bias   [E] float32, finite, or NULL.  valid [T] bytes or NULL.     (in)
  *   seq    DEVICE int32 [S + 1], 0 = seq[0] <= ... <= seq[S] = T, or NULL with
  *          S = 1.  Checked on the device where it is read: a violation
  *          records FP8BS_ERR_DEVICE_ARG and leaves the outputs undefined. (in)
@@ -485,7 +489,8 @@ typedef enum { FP8BS_SCORE_SOFTMAX = 0, FP8BS_SCORE_SIGMOID = 1 } fp8bs_score_ki
  * Rules: 1 <= E <= 1024, 1 <= k <= min(E, 32), ld >= E, 1 <= S <= 65535,
  * T < 2^31; pointers aligned to their elements, ws to 16 bytes.  Sums are taken
  * in a fixed order: the same inputs give the same bits.  Logits of +inf are
- * outside the contract.
+ * outside the contract.  Weights and biased keys are formed with expf and IEEE
+ * divisions; the scores in the sums, here and in the gradient, to 2^-21 relative.
  */
 int fp8bs_moe_route(const void* logits, int in_dtype, int64_t T, int E, int64_t ld, int score, const float* bias,
                     const uint8_t* valid, const int32_t* seq, int64_t S, int k, int normalize, float scale,
