@@ -882,7 +882,7 @@ def main():
     line["quantize_roofline"] = {
         "bound": "hbm", "achieved": q_gbs, "peak": peaks["hbm_gbs"], "unit": "GB/s",
         "frac": q_gbs / peaks["hbm_gbs"],
-        "traffic": _traffic("quantize_act_1x128_16384x7168", *(CSRC + f for f in ("quantize.cu", "common.cuh"))),
+        "traffic": _traffic("quantize_act_1x128_16384x7168", *(CSRC + f for f in ("quantize.cu", "group_quant.cuh", "common.cuh"))),
         "peak_source": peak_src, "frac_of_nominal_hbm": q_gbs / NOMINAL_HBM_GBS,
         "nominal_hbm_gbs": NOMINAL_HBM_GBS}
     line["quantize"] = {"gbs": q_gbs, "ms": q_ms, "frac_of_hbm": q_gbs / peaks["hbm_gbs"],
