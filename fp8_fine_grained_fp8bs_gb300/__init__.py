@@ -42,6 +42,11 @@ __all__ = [
     "moe_route", "moe_route_backward", "moe_layout", "moe_layout_rows", "moe_route_workspace_bytes",
     "moe_layout_workspace_bytes", "FP4_E4M3X16", "FP4_UE8M0X32", "IN_F32", "IN_BF16", "SCORE_SOFTMAX",
     "SCORE_SIGMOID",
+    "fp8bs_rmsnorm_quantize", "fp8bs_rmsnorm_backward", "fp8bs_rmsnorm_backward_workspace_bytes",
+    "fp8bs_swiglu_backward_quantize", "fp8bs_moe_combine_backward", "fp8bs_moe_dispatch_backward",
+    "fp8bs_grouped_wgrad_pow2",
+    "rmsnorm_quantize", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "swiglu_backward_quantize",
+    "moe_combine_backward", "moe_dispatch_backward", "grouped_wgrad",
 ]
 
 OUT_F32, OUT_BF16 = 0, 1
@@ -108,12 +113,24 @@ _SIGNATURES = {
     "fp8bs_moe_layout": [_c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp],
     "fp8bs_moe_layout_rows": [_c_i64, _c_int, _c_int],
     "fp8bs_moe_layout_workspace_bytes": [_c_i64, _c_int, _c_int],
+    "fp8bs_rmsnorm_quantize": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_int, _c_f32, _c_vp, _c_vp, _c_vp,
+                               _c_vp, _c_int, _c_vp, _c_vp],
+    "fp8bs_rmsnorm_backward": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_vp,
+                               _c_vp, _c_int, _c_vp, _c_i64, _c_vp],
+    "fp8bs_rmsnorm_backward_workspace_bytes": [_c_i64, _c_i64],
+    "fp8bs_swiglu_backward_quantize": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_int,
+                                       _c_vp],
+    "fp8bs_moe_combine_backward": [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp,
+                                   _c_vp, _c_int, _c_vp, _c_vp],
+    "fp8bs_moe_dispatch_backward": [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_vp],
+    "fp8bs_grouped_wgrad_pow2": [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_int, _c_vp, _c_int, _c_i64, _c_i64, _c_int,
+                                 _c_vp],
 }
 
 # Results other than a status: sizes in bytes or rows (-1: refused), text.
 _RESULTS = {"fp8bs_status_string": ctypes.c_char_p, "fp8bs_fp4_scale_bytes": _c_i64,
             "fp8bs_moe_route_workspace_bytes": _c_i64, "fp8bs_moe_layout_rows": _c_i64,
-            "fp8bs_moe_layout_workspace_bytes": _c_i64}
+            "fp8bs_moe_layout_workspace_bytes": _c_i64, "fp8bs_rmsnorm_backward_workspace_bytes": _c_i64}
 
 
 def build(force: bool = False) -> str:
@@ -340,6 +357,43 @@ def fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, ws_byte
                                            _ptr(ws), ws_bytes, _stream(stream)), "fp8bs_moe_layout")
 
 
+def fp8bs_rmsnorm_quantize(x, M, K, ldx, residual, ldr, gain, gain_dtype, eps, r, y, q, s, scale_mode=SCALE_ABSMAX,
+                           rstd=None, stream=None):
+    _check(load_library().fp8bs_rmsnorm_quantize(_ptr(x), M, K, ldx, _ptr(residual), ldr, _ptr(gain), int(gain_dtype), eps,
+                                                 _ptr(r), _ptr(y), _ptr(q), _ptr(s), int(scale_mode), _ptr(rstd),
+                                                 _stream(stream)), "fp8bs_rmsnorm_quantize")
+
+
+def fp8bs_rmsnorm_backward(dy, M, K, lddy, r, ldr, gain, gain_dtype, rstd, dres, lddres, dx, dgain, accumulate, ws,
+                           ws_bytes, stream=None):
+    _check(load_library().fp8bs_rmsnorm_backward(_ptr(dy), M, K, lddy, _ptr(r), ldr, _ptr(gain), int(gain_dtype),
+                                                 _ptr(rstd), _ptr(dres), lddres, _ptr(dx), _ptr(dgain), int(accumulate),
+                                                 _ptr(ws), ws_bytes, _stream(stream)), "fp8bs_rmsnorm_backward")
+
+
+def fp8bs_swiglu_backward_quantize(h, M, I, ldh, dv, lddv, live, dh, q, s, scale_mode=SCALE_ABSMAX, stream=None):
+    _check(load_library().fp8bs_swiglu_backward_quantize(_ptr(h), M, I, ldh, _ptr(dv), lddv, _ptr(live), _ptr(dh), _ptr(q),
+                                                         _ptr(s), int(scale_mode), _stream(stream)),
+           "fp8bs_swiglu_backward_quantize")
+
+
+def fp8bs_moe_combine_backward(dout, T, N, ldo, y, rows, row_of, row_token, w, k, dy, q, s, scale_mode, dw, stream=None):
+    _check(load_library().fp8bs_moe_combine_backward(_ptr(dout), T, N, ldo, _ptr(y), rows, _ptr(row_of), _ptr(row_token),
+                                                     _ptr(w), int(k), _ptr(dy), _ptr(q), _ptr(s), int(scale_mode),
+                                                     _ptr(dw), _stream(stream)), "fp8bs_moe_combine_backward")
+
+
+def fp8bs_moe_dispatch_backward(d, rows, N, row_of, T, k, add, dx, stream=None):
+    _check(load_library().fp8bs_moe_dispatch_backward(_ptr(d), rows, N, _ptr(row_of), T, int(k), _ptr(add), _ptr(dx),
+                                                      _stream(stream)), "fp8bs_moe_dispatch_backward")
+
+
+def fp8bs_grouped_wgrad_pow2(a_t, sa_t, b_t, sb_t, R, offsets, num_groups, d, d_dtype, N, K, accumulate=0, stream=None):
+    _check(load_library().fp8bs_grouped_wgrad_pow2(_ptr(a_t), _ptr(sa_t), _ptr(b_t), _ptr(sb_t), R, _ptr(offsets),
+                                                   num_groups, _ptr(d), d_dtype, N, K, int(accumulate), _stream(stream)),
+           "fp8bs_grouped_wgrad_pow2")
+
+
 def _size(name: str, *args) -> int:
     n = getattr(load_library(), name)(*args)
     if n < 0:
@@ -365,6 +419,13 @@ def moe_layout_workspace_bytes(T: int, k: int, E: int) -> int:
 
 
 fp4_scale_bytes = fp8bs_fp4_scale_bytes
+
+
+def fp8bs_rmsnorm_backward_workspace_bytes(M: int, K: int) -> int:
+    return _size("fp8bs_rmsnorm_backward_workspace_bytes", M, K)
+
+
+rmsnorm_backward_workspace_bytes = fp8bs_rmsnorm_backward_workspace_bytes
 
 
 # ------------------------------------------------------ allocating conveniences
@@ -741,3 +802,176 @@ def moe_layout(idx, E: int, stream=None):
     ws = torch.empty(n, dtype=torch.uint8, device=idx.device)
     fp8bs_moe_layout(idx, T, k, E, offsets, row_token, rows, row_of, ws, n, stream)
     return offsets, row_token, row_of
+
+
+def _on_one_device(*tensors):
+    """Launches go to the current device: tensors of another one are refused, which a kernel could not read."""
+    import torch
+    for t in tensors:
+        if t is not None and t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor on {t.device}; the current device is {torch.cuda.current_device()}")
+
+
+def _gain(gain, K):
+    """(gain, its fp8bs_in_dtype): one value per column."""
+    import torch
+    if _checked(gain, "gain", (torch.bfloat16, torch.float32), 1).shape[0] != K:
+        raise ValueError(f"gain: {gain.shape[0]} values for {K} columns")
+    return gain, IN_BF16 if gain.dtype == torch.bfloat16 else IN_F32
+
+
+def _like(t, name, shape, rows=False):
+    """A bfloat16 matrix of the given shape, or None."""
+    import torch
+    if t is not None and tuple(_checked(t, name, (torch.bfloat16,), 2, rows=rows).shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _scale_mode(pow2):
+    return SCALE_POW2 if pow2 else SCALE_ABSMAX
+
+
+def _codes(M, K, device):
+    import torch
+    return (torch.empty((M, K), dtype=torch.uint8, device=device),
+            torch.empty((K // 128, M), dtype=torch.float32, device=device))
+
+
+@_allocates_on_its_stream
+def rmsnorm_quantize(x, gain, residual=None, eps: float = 1e-6, pow2: bool = False, bf16: bool = False, stream=None):
+    """Root-mean-square norm of r = x + residual (bfloat16 [M, K]; without a residual r is x), quantised
+    1x128.  gain: [K] bfloat16 or float32.  Returns (q [M, K] uint8, s [K/128, M] float32, y, r, rstd [M]
+    float32): y is the normed bfloat16 matrix that q and s stand for with ``bf16``, else None; r and rstd
+    are what rmsnorm_backward takes."""
+    import torch
+    _checked(x, "x", (torch.bfloat16,), 2, rows=True)
+    M, K = x.shape
+    _on_one_device(x, gain, residual)
+    gain, kind = _gain(gain, K)
+    _like(residual, "residual", (M, K), rows=True)
+    r = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if residual is not None else None
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if bf16 else None
+    q, s = _codes(M, K, x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    fp8bs_rmsnorm_quantize(x, M, K, _row_stride(x), residual, K if residual is None else _row_stride(residual), gain, kind,
+                           eps, r, y, q, s, _scale_mode(pow2), rstd, stream)
+    return q, s, y, x if r is None else r, rstd
+
+
+@_allocates_on_its_stream
+def rmsnorm_backward(dy, r, gain, rstd, dres=None, dgain=None, stream=None):
+    """Gradient of rmsnorm_quantize's y (dy [M, K] bfloat16): (dx [M, K] bfloat16, the gradient of x and of
+    the residual, with ``dres`` added; dgain [K] float32).  A ``dgain`` given is added to and returned."""
+    import torch
+    _checked(dy, "dy", (torch.bfloat16,), 2, rows=True)
+    M, K = dy.shape
+    _on_one_device(dy, r, gain, rstd, dres, dgain)
+    gain, kind = _gain(gain, K)
+    if r is None:
+        raise ValueError("r: the normed rows are needed")
+    _like(r, "r", (M, K), rows=True)
+    _like(dres, "dres", (M, K), rows=True)
+    if _checked(rstd, "rstd", (torch.float32,), 1).shape[0] != M:
+        raise ValueError(f"rstd: {rstd.shape[0]} values for {M} rows")
+    accumulate = dgain is not None
+    if accumulate and _checked(dgain, "dgain", (torch.float32,), 1).shape[0] != K:
+        raise ValueError(f"dgain: {dgain.shape[0]} values for {K} columns")
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+    dgain = dgain if accumulate else torch.empty(K, dtype=torch.float32, device=dy.device)
+    n = rmsnorm_backward_workspace_bytes(M, K)
+    ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
+    fp8bs_rmsnorm_backward(dy, M, K, _row_stride(dy), r, _row_stride(r), gain, kind, rstd, dres,
+                           K if dres is None else _row_stride(dres), dx, dgain, accumulate, ws, n, stream)
+    return dx, dgain
+
+
+@_allocates_on_its_stream
+def swiglu_backward_quantize(h, dv, live=None, pow2: bool = False, bf16: bool = False, stream=None):
+    """Gradient of silu(gate) * up with respect to h [M, 2I] bfloat16 (gate | up), dv [M, I] bfloat16,
+    quantised 1x128.  Returns (q [M, 2I] uint8, s [2I/128, M] float32, dh), dh the bfloat16 gradient with
+    ``bf16``, else None; rows with live[i] < 0 (int32 [M]) are zeros."""
+    import torch
+    _checked(h, "h", (torch.bfloat16,), 2, rows=True)
+    M, two_i = h.shape
+    if two_i % 2 != 0:
+        raise ValueError(f"h: {two_i} columns; expected as many of the gate as of up")
+    _on_one_device(h, dv, live)
+    if dv is None:
+        raise ValueError("dv: the gradient of the SwiGLU's output is needed")
+    _like(dv, "dv", (M, two_i // 2), rows=True)
+    if live is not None and _checked(live, "live", (torch.int32,), 1).shape[0] != M:
+        raise ValueError("live: one value per row of h")
+    dh = torch.empty((M, two_i), dtype=torch.bfloat16, device=h.device) if bf16 else None
+    q, s = _codes(M, two_i, h.device)
+    fp8bs_swiglu_backward_quantize(h, M, two_i // 2, _row_stride(h), dv, _row_stride(dv), live, dh, q, s,
+                                   _scale_mode(pow2), stream)
+    return q, s, dh
+
+
+@_allocates_on_its_stream
+def moe_combine_backward(dout, y, row_of, row_token, w, pow2: bool = False, bf16: bool = False, stream=None):
+    """Gradient of the combine: dout [T, N] bfloat16, y [rows, N] bfloat16 the experts' outputs, row_of
+    [T, k] and row_token [rows] from moe_layout, w [T, k] the gate weights.  Returns (q [rows, N] uint8, s
+    [N/128, rows] float32, dy, dw [T, k] float32): the outputs' gradients quantised 1x128 (dy in bfloat16
+    with ``bf16``, else None), zeros in rows without a token, and the weights' gradient."""
+    import torch
+    _checked(dout, "dout", (torch.bfloat16,), 2, rows=True)
+    T, N = dout.shape
+    _on_one_device(dout, y, row_of, row_token, w)
+    rows = _checked(row_token, "row_token", (torch.int32,), 1).shape[0]
+    if y is None:
+        raise ValueError("y: the experts' outputs are needed")
+    _like(y, "y", (rows, N))
+    if (_checked(row_of, "row_of", (torch.int32,), 2).shape != _checked(w, "w", (torch.float32,), 2).shape
+            or row_of.shape[0] != T):
+        raise ValueError(f"row_of {tuple(row_of.shape)} and w {tuple(w.shape)}: one row per token each")
+    k = row_of.shape[1]
+    dy = torch.empty((rows, N), dtype=torch.bfloat16, device=dout.device) if bf16 else None
+    q, s = _codes(rows, N, dout.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    fp8bs_moe_combine_backward(dout, T, N, _row_stride(dout), y, rows, row_of, row_token, w, k, dy, q, s, _scale_mode(pow2),
+                               dw, stream)
+    return q, s, dy, dw
+
+
+@_allocates_on_its_stream
+def moe_dispatch_backward(d, row_of, add=None, stream=None):
+    """Gradient of the dispatch: dx [T, N] bfloat16 = add + the rows of d [rows, N] bfloat16 that row_of
+    [T, k] names."""
+    import torch
+    rows, N = _checked(d, "d", (torch.bfloat16,), 2).shape
+    T, k = _checked(row_of, "row_of", (torch.int32,), 2).shape
+    _on_one_device(d, row_of, add)
+    _like(add, "add", (T, N))
+    dx = torch.empty((T, N), dtype=torch.bfloat16, device=d.device)
+    fp8bs_moe_dispatch_backward(d, rows, N, row_of, T, k, add, dx, stream)
+    return dx
+
+
+@_allocates_on_its_stream
+def grouped_wgrad(a_t, sa_t, b_t, sb_t, offsets, out_dtype=None, out=None, accumulate: bool = False, stream=None):
+    """Gradients of the experts' weights [G, N, K]: a_t [N, R] and b_t [K, R] E4M3 codes of the outputs'
+    gradients and of the inputs in 128x1 groups, sa_t [R/128, N] and sb_t [R/128, K] their power-of-two
+    scales, offsets [G + 1] int32 the experts' rows.  float32 (default) or bfloat16; ``accumulate`` adds to
+    the float32 ``out``."""
+    import torch
+    N, R = _checked(a_t, "a_t", (torch.uint8,), 2).shape
+    K = _checked(b_t, "b_t", (torch.uint8,), 2).shape[0]
+    G = _checked(offsets, "offsets", (torch.int32,), 1).shape[0] - 1
+    _on_one_device(a_t, sa_t, b_t, sb_t, offsets, out)
+    if (b_t.shape[1] != R or tuple(_checked(sa_t, "sa_t", (torch.float32,), 2).shape) != (R // 128, N)
+            or tuple(_checked(sb_t, "sb_t", (torch.float32,), 2).shape) != (R // 128, K)):
+        raise ValueError(f"a_t {tuple(a_t.shape)}, b_t {tuple(b_t.shape)} and scales {tuple(sa_t.shape)}, "
+                         f"{tuple(sb_t.shape)} do not fit")
+    if accumulate and (out is None or out.dtype != torch.float32):
+        raise ValueError("accumulate: adds to a float32 out")
+    if out is None:
+        dtype, code = _out_type(out_dtype or torch.float32)
+        out = torch.empty((G, N, K), dtype=dtype, device=a_t.device)
+    else:
+        if tuple(_checked(out, "out", (torch.bfloat16, torch.float32), 3).shape) != (G, N, K):
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {(G, N, K)}")
+        code = _out_type(out.dtype)[1]
+    fp8bs_grouped_wgrad_pow2(a_t, sa_t, b_t, sb_t, R, offsets, G, out, code, N, K, accumulate, stream)
+    return out

@@ -551,6 +551,163 @@ int fp8bs_moe_layout(const int32_t* idx, int64_t T, int k, int E, int32_t* offse
   return from_cuda(fp8bs::launch_layout(a, static_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- training
+static bool in_dtype_ok(int t) { return t == FP8BS_IN_F32 || t == FP8BS_IN_BF16; }
+static bool scale_mode_ok(int m) { return m == FP8BS_SCALE_ABSMAX || m == FP8BS_SCALE_POW2; }
+
+int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* gain, int gain_dtype, float eps, void* r, void* y, uint8_t* q, float* s,
+                           int scale_mode, float* rstd, void* stream) {
+  if (M < 0 || K < 0 || ldx < K || (residual != nullptr && ldr < K)) return FP8BS_ERR_INVALID_ARG;
+  if (!in_dtype_ok(gain_dtype) || !scale_mode_ok(scale_mode)) return FP8BS_ERR_INVALID_ARG;
+  if (!(eps >= FP8BS_RMSNORM_MIN_EPS && eps <= 1e30f)) return FP8BS_ERR_INVALID_ARG;   // NaN too
+  if ((q == nullptr) != (s == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (K % 8 != 0 || (q != nullptr && K % 128 != 0)) return FP8BS_ERR_SHAPE;
+  if (M > (int64_t(1) << 31) || K > fp8bs::rmsnorm_max_columns()) return FP8BS_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8BS_OK;
+  if (x == nullptr || gain == nullptr || (q == nullptr && y == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (r == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(r) || !aligned16(y) || !aligned16(q) ||
+      !aligned4(s) || !aligned4(rstd) || (ldx * 2) % 16 != 0 || (residual != nullptr && (ldr * 2) % 16 != 0))
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x); a.res = static_cast<const uint16_t*>(residual); a.gain = gain;
+  a.gain_f32 = gain_dtype == FP8BS_IN_F32; a.M = M; a.K = K; a.ldx = ldx; a.ldr = ldr; a.eps = eps;
+  a.pow2 = scale_mode == FP8BS_SCALE_POW2; a.r = static_cast<uint16_t*>(r); a.y = static_cast<uint16_t*>(y);
+  a.q = q; a.s = s; a.rstd = rstd;
+  return from_cuda(fp8bs::launch_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp8bs_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || K % 8 != 0 || M > (int64_t(1) << 31) || K > fp8bs::rmsnorm_max_columns()) return -1;
+  return fp8bs::rmsnorm_backward_workspace_bytes(M, K);
+}
+
+int fp8bs_rmsnorm_backward(const void* dy, int64_t M, int64_t K, int64_t lddy, const void* r, int64_t ldr,
+                           const void* gain, int gain_dtype, const float* rstd, const void* dres, int64_t lddres,
+                           void* dx, float* dgain, int accumulate, void* ws, int64_t ws_bytes, void* stream) {
+  if (M < 0 || K < 0 || lddy < K || ldr < K || (dres != nullptr && lddres < K)) return FP8BS_ERR_INVALID_ARG;
+  if (!in_dtype_ok(gain_dtype)) return FP8BS_ERR_INVALID_ARG;
+  if (K % 8 != 0 || M > (int64_t(1) << 31) || K > fp8bs::rmsnorm_max_columns()) return FP8BS_ERR_SHAPE;
+  if (K == 0) return FP8BS_OK;
+  if (M > 0 && (dy == nullptr || r == nullptr || gain == nullptr || rstd == nullptr || dx == nullptr))
+    return FP8BS_ERR_INVALID_ARG;
+  if (M > 0 && dgain != nullptr && (ws == nullptr || ws_bytes < fp8bs::rmsnorm_backward_workspace_bytes(M, K)))
+    return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(r) || !aligned16(gain) || !aligned4(rstd) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned4(dgain) || !aligned16(ws) || (lddy * 2) % 16 != 0 || (ldr * 2) % 16 != 0 ||
+      (dres != nullptr && (lddres * 2) % 16 != 0))
+    return FP8BS_ERR_ALIGNMENT;
+  if (M == 0) {   // no rows: a gradient of zeros
+    if (dgain == nullptr || accumulate) return FP8BS_OK;
+    return from_cuda(cudaMemsetAsync(dgain, 0, static_cast<size_t>(K) * 4, static_cast<cudaStream_t>(stream)));
+  }
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::NormBackwardArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy); a.r = static_cast<const uint16_t*>(r); a.gain = gain;
+  a.gain_f32 = gain_dtype == FP8BS_IN_F32; a.rstd = rstd; a.dres = static_cast<const uint16_t*>(dres);
+  a.M = M; a.K = K; a.lddy = lddy; a.ldr = ldr; a.lddres = lddres; a.dx = static_cast<uint16_t*>(dx);
+  a.dgain = dgain; a.accumulate = accumulate != 0;
+  return from_cuda(fp8bs::launch_rmsnorm_backward(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_swiglu_backward_quantize(const void* h, int64_t M, int64_t I, int64_t ldh, const void* dv, int64_t lddv,
+                                   const int32_t* live, void* dh, uint8_t* q, float* s, int scale_mode, void* stream) {
+  if (M < 0 || I < 0 || ldh < 2 * I || lddv < I || !scale_mode_ok(scale_mode)) return FP8BS_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (I % 128 != 0) return FP8BS_ERR_SHAPE;
+  if (M > (int64_t(1) << 31) || I > (int64_t(1) << 23)) return FP8BS_ERR_SHAPE;
+  if (M == 0 || I == 0) return FP8BS_OK;
+  if (h == nullptr || dv == nullptr || (q == nullptr && dh == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(h) || !aligned16(dv) || !aligned4(live) || !aligned16(dh) || !aligned16(q) || !aligned4(s) ||
+      (ldh * 2) % 16 != 0 || (lddv * 2) % 16 != 0)
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::SwigluBackwardArgs a{};
+  a.h = static_cast<const uint16_t*>(h); a.dv = static_cast<const uint16_t*>(dv); a.live = live; a.M = M; a.I = I;
+  a.ldh = ldh; a.lddv = lddv; a.pow2 = scale_mode == FP8BS_SCALE_POW2; a.dh = static_cast<uint16_t*>(dh); a.q = q; a.s = s;
+  return from_cuda(fp8bs::launch_swiglu_backward(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_moe_combine_backward(const void* dout, int64_t T, int64_t N, int64_t ldo, const void* y, int64_t rows,
+                               const int32_t* row_of, const int32_t* row_token, const float* w, int k, void* dy,
+                               uint8_t* q, float* s, int scale_mode, float* dw, void* stream) {
+  if (T < 0 || N < 0 || ldo < N || rows < 0 || k < 1 || k > 64 || !scale_mode_ok(scale_mode)) return FP8BS_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr) || (dw != nullptr && rows > 0 && y == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (N % 8 != 0 || (q != nullptr && N % 128 != 0)) return FP8BS_ERR_SHAPE;
+  if (T > (int64_t(1) << 24) / k || rows > (int64_t(1) << 30) || N > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
+  if (N == 0 || (T == 0 && rows == 0)) return FP8BS_OK;
+  if (rows > 0 && (row_token == nullptr || (q == nullptr && dy == nullptr))) return FP8BS_ERR_INVALID_ARG;
+  if (T > 0 && (dout == nullptr || row_of == nullptr || w == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(y) || !aligned4(row_of) || !aligned4(row_token) || !aligned4(w) || !aligned16(dy) ||
+      !aligned16(q) || !aligned4(s) || !aligned4(dw) || (ldo * 2) % 16 != 0)
+    return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::CombineBackwardArgs a{};
+  a.dout = static_cast<const uint16_t*>(dout); a.T = T; a.N = N; a.ldo = ldo; a.y = static_cast<const uint16_t*>(y);
+  a.rows = rows; a.row_of = row_of; a.row_token = row_token; a.w = w; a.k = k; a.pow2 = scale_mode == FP8BS_SCALE_POW2;
+  a.dy = static_cast<uint16_t*>(dy); a.q = q; a.s = s; a.dw = dw;
+  return from_cuda(fp8bs::launch_combine_backward(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_moe_dispatch_backward(const void* d, int64_t rows, int64_t N, const int32_t* row_of, int64_t T, int k,
+                                const void* add, void* dx, void* stream) {
+  if (rows < 0 || N < 0 || T < 0 || k < 1 || k > 64) return FP8BS_ERR_INVALID_ARG;
+  if (N % 8 != 0) return FP8BS_ERR_SHAPE;
+  if (rows > (int64_t(1) << 31) - 1 || T > (int64_t(1) << 31) / 64 || N > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
+  if (T == 0 || N == 0) return FP8BS_OK;
+  if (row_of == nullptr || dx == nullptr || (rows > 0 && d == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(d) || !aligned4(row_of) || !aligned16(add) || !aligned16(dx)) return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  return from_cuda(fp8bs::launch_moe_dispatch_backward(static_cast<const uint16_t*>(d), rows, N, row_of, T, k,
+                                                       static_cast<const uint16_t*>(add), static_cast<uint16_t*>(dx), sms,
+                                                       static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_grouped_wgrad_pow2(const uint8_t* a_t, const float* sa_t, const uint8_t* b_t, const float* sb_t, int64_t R,
+                             const int32_t* offsets, int num_groups, void* d, int d_dtype, int64_t N, int64_t K,
+                             int accumulate, void* stream) {
+  if (R < 0 || N < 0 || K < 0 || num_groups < 1 || num_groups > 512) return FP8BS_ERR_INVALID_ARG;
+  if (d_dtype != FP8BS_OUT_F32 && d_dtype != FP8BS_OUT_BF16) return FP8BS_ERR_INVALID_ARG;
+  if (accumulate && d_dtype != FP8BS_OUT_F32) return FP8BS_ERR_INVALID_ARG;
+  if (R % 128 != 0 || N % 128 != 0 || K % 128 != 0) return FP8BS_ERR_SHAPE;
+  if (R > (int64_t(1) << 30) || N > (int64_t(1) << 24) || K > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
+  if (N == 0 || K == 0) return FP8BS_OK;
+  // rows of D and tile numbers are 32-bit in the kernel
+  if (N * num_groups >= (int64_t(1) << 31) || N / 128 * (K / 128) * num_groups >= (int64_t(1) << 31)) return FP8BS_ERR_SHAPE;
+  if (offsets == nullptr || d == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned4(offsets) || !aligned16(d)) return FP8BS_ERR_ALIGNMENT;
+  if (R == 0) {   // no rows at all: gradients of zeros
+    if (accumulate) return FP8BS_OK;
+    return from_cuda(cudaMemsetAsync(d, 0, static_cast<size_t>(N) * K * num_groups * (d_dtype == FP8BS_OUT_F32 ? 4 : 2),
+                                     static_cast<cudaStream_t>(stream)));
+  }
+  if (a_t == nullptr || sa_t == nullptr || b_t == nullptr || sb_t == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned16(a_t) || !aligned4(sa_t) || !aligned16(b_t) || !aligned16(sb_t)) return FP8BS_ERR_ALIGNMENT;
+  int sms = 0;
+  const int st = current_device(&sms);
+  if (st != FP8BS_OK) return st;
+  fp8bs::GemmArgs g{};
+  g.a = a_t; g.sa = sa_t; g.b = b_t; g.sb = sb_t; g.d = d; g.offsets = offsets;
+  g.M = N; g.N = K; g.K = R; g.num_groups = num_groups; g.grouped = true; g.sb_row = true;
+  g.out_bf16 = d_dtype == FP8BS_OUT_BF16; g.accumulate = accumulate != 0; g.timeout_ns = g_timeout_ns.load();
+  bool tmap_failed = false, reg_failed = false;
+  const cudaError_t e = fp8bs::launch_wgrad_pow2(g, sms, static_cast<cudaStream_t>(stream), &tmap_failed, &reg_failed);
+  if (tmap_failed) return FP8BS_ERR_ALIGNMENT;
+  return from_cuda(e);
+}
+
 int fp8bs_selftest_wait_timeout(int64_t timeout_us, void* stream) {
   if (timeout_us < 1 || timeout_us > 10000000) return FP8BS_ERR_INVALID_ARG;
   int sms = 0;
@@ -578,14 +735,15 @@ int fp8bs_diag_gemm_unpromoted(const uint8_t* a, const uint8_t* b, float* d, int
 
 int fp8bs_get_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8BS_ERR_CUDA;
-  int v = 0, mx = 0, q = 0, f4 = 0, rt = 0, dg = 0;
+  int v = 0, mx = 0, q = 0, f4 = 0, rt = 0, tr = 0, dg = 0;
   if (fp8bs::gemm_take_status(&v) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::gemm_mx_take_status(&mx) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::quant_take_status(&q) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::gemm_fp4_take_status(&f4) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::route_take_status(&rt) != cudaSuccess) return FP8BS_ERR_CUDA;
+  if (fp8bs::train_take_status(&tr) != cudaSuccess) return FP8BS_ERR_CUDA;
   if (fp8bs::diag_take_status(&dg) != cudaSuccess) return FP8BS_ERR_CUDA;
-  for (const int st : {v, mx, q, f4, rt})
+  for (const int st : {v, mx, q, f4, rt, tr})
     if (st != FP8BS_OK) return st;
   return dg;
 }

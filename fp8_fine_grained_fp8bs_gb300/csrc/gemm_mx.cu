@@ -179,7 +179,30 @@ __device__ __forceinline__ uint32_t ue8m0_of(float s, uint32_t& bad) {
   return pow2 ? e : 0u;
 }
 
-template <int BN, bool kRowScale, bool kGrouped, bool kPair>
+// Work unit t of the weight gradients: group-major, each group's output tiles
+// (rows [0, M) x columns [0, N) of its D) in the order of tile_coords.  The
+// group's rows are the k-blocks [kb0, kb0 + nkb) of both operands, none for an
+// expert without rows.
+struct SegTile {
+  int g, row0, n0, kb0, nkb;
+};
+template <int BN, bool kPair>
+__device__ __forceinline__ SegTile seg_tile(int t, int ntn, int tiles, const int* s_off, uint32_t rank) {
+  SegTile s;
+  s.g = t / tiles;
+  const int u = t - s.g * tiles;
+  const int mu = u / ntn;
+  s.n0 = (u - mu * ntn) * BN;
+  s.row0 = (kPair ? 2 * mu + static_cast<int>(rank) : mu) * kBlockM;
+  s.kb0 = s_off[s.g] / kBlockK;
+  s.nkb = s_off[s.g + 1] / kBlockK - s.kb0;
+  return s;
+}
+
+// kSegK: the weight gradients of the experts.  A [M][K] and B [N][K] hold all
+// experts' rows along K (p.nkb blocks in all), group g those of its segment, and
+// D is [groups][M][N]; every role takes a tile's k-blocks from seg_tile.
+template <int BN, bool kRowScale, bool kGrouped, bool kPair, bool kSegK = false>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmD, const KParams p) {
@@ -211,7 +234,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const int unit0 = kPair ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int nunits = kPair ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
   const int nnb = (p.N + kGroup - 1) / kGroup;
-  const int nsl = (p.nkb + kStepsPerSlot - 1) / kStepsPerSlot;  // scale slots per tile
+  // kSegK: work units per group
+  const int seg_tiles = static_cast<int>((p.M + (kPair ? 2 : 1) * kBlockM - 1) / ((kPair ? 2 : 1) * kBlockM)) * ntn;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -235,15 +259,18 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     griddep_wait();  // the group table below may come from the preceding kernel
     int total_mt = 0;
     bool ok = true;
-    if (kGrouped) {
+    if (kGrouped || kSegK) {
+      const int64_t rows = kSegK ? static_cast<int64_t>(p.nkb) * kBlockK : p.M;
       int prev = 0;
       for (int g = 0; g <= p.num_groups; ++g) {
         const int o = p.offsets[g];
-        ok = ok && (o >= prev || g == 0) && o >= 0 && (o % kBlockM) == 0 && o <= p.M;
+        ok = ok && (o >= prev || g == 0) && o >= 0 && (o % kBlockM) == 0 && o <= rows;
         s_off[g] = o;
         prev = o;
       }
-      if (ok) {
+      if (ok && kSegK) {
+        total_mt = p.num_groups * (seg_tiles / ntn);
+      } else if (ok) {
         for (int g = 0; g < p.num_groups; ++g) {
           s_cum[g] = total_mt;
           const int mt = (s_off[g + 1] - s_off[g]) / kBlockM;
@@ -285,6 +312,20 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const uint32_t tmem_base = misc[0];
   const int total_tiles = static_cast<int>(misc[2]);
   volatile uint32_t* abort_flag = &misc[1];
+  // tile of unit t, with its k-blocks; g carries the group of the previous unit in
+  auto coords = [&](int t, int& row0, int& n0, int& g, int64_t& row_end, int& kb0, int& nkb) {
+    if (kSegK) {
+      const SegTile s = seg_tile<BN, kPair>(t, ntn, seg_tiles, s_off, rank);
+      g = s.g;
+      row0 = s.row0;
+      n0 = s.n0;
+      row_end = p.M;
+      kb0 = s.kb0;
+      nkb = s.nkb;
+    } else {
+      tile_coords<BN, kPair>(t, ntn, kGrouped, s_off, s_cum, p.num_groups, rank, p.M, row0, n0, g, row_end);
+    }
+  };
 
   if (warp < kMxEpiWarp0) {
     setmaxnreg_dec<C::kRegsProducer>();
@@ -297,10 +338,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int g = 0;
       uint32_t gs = 0;   // scale slots (the leader waits for each before loading its first k-block)
       for (int t = unit0; t < total_tiles && live; t += nunits) {
-        int row0, n0;
+        int row0, n0, kb0 = 0, nkb = p.nkb;
         int64_t row_end;
-        tile_coords<BN, kPair>(t, ntn, kGrouped, s_off, s_cum, p.num_groups, rank, p.M, row0, n0, g, row_end);
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        coords(t, row0, n0, g, row_end, kb0, nkb);
+        for (int kb = 0; kb < nkb; ++kb) {
           if (!warp_wait(&empty[stage], phase ^ 1, p.timeout_ns)) { live = false; break; }
           // The slot's scales are in shared memory (both CTAs') before its
           // first stage is loaded: a full stage then implies ready scales,
@@ -318,20 +359,20 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             if (kPair) {
               if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::kABytes + C::kBBytes));
               const uint32_t leader_full = mapa_shared(&full[stage], 0);
-              tma_load_2d_pair(sA + stage * C::kABytes, &tmA, leader_full, kb * kBlockK, row0);
+              tma_load_2d_pair(sA + stage * C::kABytes, &tmA, leader_full, (kb0 + kb) * kBlockK, row0);
               if (kGrouped)
                 tma_load_3d_pair(sB + stage * C::kBBytes, &tmB, leader_full, kb * kBlockK,
                                  n0 + static_cast<int>(rank) * (BN / 2), g);
               else
-                tma_load_2d_pair(sB + stage * C::kBBytes, &tmB, leader_full, kb * kBlockK,
+                tma_load_2d_pair(sB + stage * C::kBBytes, &tmB, leader_full, (kb0 + kb) * kBlockK,
                                  n0 + static_cast<int>(rank) * (BN / 2));
             } else {
               mbar_arrive_expect_tx(&full[stage], C::kABytes + C::kBBytes);
-              tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kBlockK, row0);
+              tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], (kb0 + kb) * kBlockK, row0);
               if (kGrouped)
                 tma_load_3d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * kBlockK, n0, g);
               else
-                tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * kBlockK, n0);
+                tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], (kb0 + kb) * kBlockK, n0);
             }
           }
           __syncwarp();
@@ -356,12 +397,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       uint32_t gs = 0;           // scale slots used so far (ring position and phase)
       uint32_t tiles_done = 0;
       bool live = true;
-      for (int t = unit0; t < total_tiles && live; t += nunits, ++tiles_done) {
+      for (int t = unit0; t < total_tiles && live; t += nunits) {
+        const int nkb = kSegK ? seg_tile<BN, kPair>(t, ntn, seg_tiles, s_off, rank).nkb : p.nkb;
+        if (kSegK && nkb == 0) continue;   // the epilogue writes zeros by itself
         const uint32_t abuf = tiles_done % C::kAccBufs;
         const uint32_t aphase = (tiles_done / C::kAccBufs) & 1u;
         if (!warp_wait(&acc_empty[abuf], aphase ^ 1u, p.timeout_ns)) { live = false; break; }
+        ++tiles_done;
         const uint32_t dtmem = tmem_base + abuf * BN;
-        for (int kk = 0; kk < p.nkb; ++kk) {
+        for (int kk = 0; kk < nkb; ++kk) {
           const uint32_t ring = gs % C::kSfSlots;
           // a full stage implies its slot's scales are in shared memory (the
           // producer waited for them before loading the slot's first stage)
@@ -399,13 +443,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             } else {
               mma_commit(&empty[stage]);
             }
-            if (kk % kStepsPerSlot == kStepsPerSlot - 1 || kk + 1 == p.nkb) {
+            if (kk % kStepsPerSlot == kStepsPerSlot - 1 || kk + 1 == nkb) {
               if (kPair)
                 mma_commit_pair(&sf_empty[ring], 0x3);
               else
                 mma_commit(&sf_empty[ring]);
             }
-            if (kk + 1 == p.nkb) {
+            if (kk + 1 == nkb) {
               if (kPair)
                 mma_commit_pair(&acc_full[abuf], 0x3);
               else
@@ -413,7 +457,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
           }
           __syncwarp();
-          if (kk % kStepsPerSlot == kStepsPerSlot - 1 || kk + 1 == p.nkb) ++gs;
+          if (kk % kStepsPerSlot == kStepsPerSlot - 1 || kk + 1 == nkb) ++gs;
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         }
       }
@@ -436,11 +480,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       bool live = true;
       int g = 0;
       for (int t = unit0; t < total_tiles && live; t += nunits) {
-        int row0, n0;
+        int row0, n0, kb0 = 0, nkb = p.nkb;
         int64_t row_end;
-        tile_coords<BN, kPair>(t, ntn, kGrouped, s_off, s_cum, p.num_groups, rank, p.M, row0, n0, g, row_end);
-        const bool last_tile = t + nunits >= total_tiles;
-        for (int kb = 0; kb < p.nkb; ++kb, ++step) {
+        coords(t, row0, n0, g, row_end, kb0, nkb);
+        for (int kb = 0; kb < nkb; ++kb, ++step) {
           const uint32_t chunk = (step / C::kScaleChunk) % kMxScaleChunks;
           if (step % C::kScaleChunk == 0 &&
               !mbar_wait(&sc_empty[chunk], ((step / C::kScaleSlots) & 1u) ^ 1u, p.timeout_ns)) {
@@ -448,7 +491,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             break;
           }
           float* dst = sScale + (step % C::kScaleSlots) * C::kSlotFloats;
-          const float* sa_kb = p.sa + static_cast<int64_t>(kb) * p.M;
+          const float* sa_kb = p.sa + static_cast<int64_t>(kb0 + kb) * p.M;
 #pragma unroll
           for (int i = 0; i < kBlockM / 32; ++i) {
             const int64_t r = static_cast<int64_t>(row0) + lane + 32 * i;
@@ -459,16 +502,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             for (int i = 0; i < BN / 128; ++i) {
               const int c = 4 * (lane + 32 * i);
               if (n0 + c < p.N)
-                cp_async_16(dst + kBlockM + c, p.sb + static_cast<int64_t>(kb) * p.N + n0 + c);
+                cp_async_16(dst + kBlockM + c, p.sb + static_cast<int64_t>(kb0 + kb) * p.N + n0 + c);
             }
           } else if (lane < BN / 128 && n0 + 128 * lane < p.N) {
             const int64_t nb = static_cast<int64_t>(g) * nnb + n0 / 128 + lane;
             cp_async_4(dst + kBlockM + lane, p.sb + nb * p.nkb + kb);
           }
-          if (step % C::kScaleChunk == C::kScaleChunk - 1 || (last_tile && kb + 1 == p.nkb))
-            cp_async_mbar_arrive(&sc_full[chunk]);
+          if (step % C::kScaleChunk == C::kScaleChunk - 1) cp_async_mbar_arrive(&sc_full[chunk]);
         }
       }
+      if (live && step % C::kScaleChunk != 0)   // the last chunk, not full
+        cp_async_mbar_arrive(&sc_full[(step / C::kScaleChunk) % kMxScaleChunks]);
       if (!live) {
         record_mx_status(kStatusTimeout);
         *abort_flag = 1;
@@ -490,9 +534,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       bool live = true;
       int g = 0;
       for (int t = unit0; t < total_tiles && live; t += nunits) {
-        int row0, n0;
+        int row0, n0, kb0 = 0, nkb = p.nkb;
         int64_t row_end;
-        tile_coords<BN, kPair>(t, ntn, kGrouped, s_off, s_cum, p.num_groups, rank, p.M, row0, n0, g, row_end);
+        coords(t, row0, n0, g, row_end, kb0, nkb);
+        const int nsl = (nkb + kStepsPerSlot - 1) / kStepsPerSlot;  // scale slots of the tile
         // scales outside the rows and columns the tile writes are not read
         // (their bytes are 127, 2^0) and not checked
         uint32_t a_ok = 0, b_ok = 0;
@@ -505,7 +550,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         for (int v = 0; v < kBVals; ++v)
           b_ok |= (n0 + (kRowScale ? 32 * v + lane : 128 * v) < p.N) ? 1u << v : 0u;
         for (int sl = 0; sl < nsl && live; ++sl, ++gs) {
-          const int nsteps = min(kStepsPerSlot, p.nkb - sl * kStepsPerSlot);
+          const int nsteps = min(kStepsPerSlot, nkb - sl * kStepsPerSlot);
           uint32_t wa[4] = {0u, 0u, 0u, 0u};
           uint32_t wb[kBVals];
 #pragma unroll
@@ -599,47 +644,58 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
     // Drains one tile's accumulator: read this thread's row (BN/2 columns)
     // out of TMEM, hand the accumulator back, store through shared memory.
-    auto drain = [&](int row0, int n0, int64_t row_end) {
-      const uint32_t abuf = epi_tiles % C::kAccBufs;
-      const uint32_t aphase = (epi_tiles / C::kAccBufs) & 1u;
-      ++epi_tiles;
-      if (!mbar_wait(&acc_full[abuf], aphase, p.timeout_ns)) {
-        live = false;
-        return;
-      }
-      tc_fence_after_sync();
+    // `rows0` is the first row of the tile's group in D; a tile without
+    // k-blocks (`empty_tile`) is zeros and takes no accumulator.
+    auto drain = [&](int row0, int n0, int64_t row_end, int64_t rows0, bool empty_tile) {
       uint32_t acc[C::kColsPerThread / 32][32];
-      const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * C::kColsPerThread;
+      if (kSegK && empty_tile) {
+        if (p.accumulate) return;
 #pragma unroll
-      for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
+        for (int ch = 0; ch < C::kColsPerThread / 32; ++ch)
 #pragma unroll
-      for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_wait_ld(acc[ch]);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (kPair)
-          mbar_arrive_cluster(mapa_shared(&acc_empty[abuf], 0));
-        else
-          mbar_arrive(&acc_empty[abuf]);
+          for (int i = 0; i < 32; ++i) acc[ch][i] = 0u;
+      } else {
+        const uint32_t abuf = epi_tiles % C::kAccBufs;
+        const uint32_t aphase = (epi_tiles / C::kAccBufs) & 1u;
+        ++epi_tiles;
+        if (!mbar_wait(&acc_full[abuf], aphase, p.timeout_ns)) {
+          live = false;
+          return;
+        }
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem_base + lane_base + abuf * BN + colhalf * C::kColsPerThread;
+#pragma unroll
+        for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_ld32(taddr + ch * 32, acc[ch]);
+#pragma unroll
+        for (int ch = 0; ch < C::kColsPerThread / 32; ++ch) tmem_wait_ld(acc[ch]);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair)
+            mbar_arrive_cluster(mapa_shared(&acc_empty[abuf], 0));
+          else
+            mbar_arrive(&acc_empty[abuf]);
+        }
       }
       const int ncol0 = n0 + colhalf * C::kColsPerThread;
       const int y0 = row0 + quarter * 32;
       if (y0 < row_end && ncol0 < p.N) {
         const float* v = reinterpret_cast<const float*>(&acc[0][0]);
+        const int yd = kSegK ? static_cast<int>(rows0) + y0 : y0;
         if (p.out_bf16)
-          store_segment<C::kColsPerThread, true, kMxOutSlots>(v, s_out, out_seq, lane, &tmD, ncol0, y0, false);
+          store_segment<C::kColsPerThread, true, kMxOutSlots>(v, s_out, out_seq, lane, &tmD, ncol0, yd, false);
         else
-          store_segment<C::kColsPerThread, false, kMxOutSlots>(v, s_out, out_seq, lane, &tmD, ncol0, y0,
+          store_segment<C::kColsPerThread, false, kMxOutSlots>(v, s_out, out_seq, lane, &tmD, ncol0, yd,
                                                                p.accumulate != 0);
       }
     };
 
     int g = 0;
     for (int t = unit0; t < total_tiles && live; t += nunits) {
-      int row0, n0;
+      int row0, n0, kb0 = 0, nkb = p.nkb;
       int64_t row_end;
-      tile_coords<BN, kPair>(t, ntn, kGrouped, s_off, s_cum, p.num_groups, rank, p.M, row0, n0, g, row_end);
-      drain(row0, n0, row_end);
+      coords(t, row0, n0, g, row_end, kb0, nkb);
+      drain(row0, n0, row_end, kSegK ? g * p.M : 0, nkb == 0);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -661,10 +717,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   }
 }
 
-template <int BN, bool kRowScale, bool kGrouped, bool kPair>
+template <int BN, bool kRowScale, bool kGrouped, bool kPair, bool kSegK = false>
 cudaError_t run_mx(const GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed, bool* reg_check_failed) {
   using C = MxCfg<BN, kPair, kRowScale>;
-  auto kern = gemm_mx_kernel<BN, kRowScale, kGrouped, kPair>;
+  auto kern = gemm_mx_kernel<BN, kRowScale, kGrouped, kPair, kSegK>;
   cudaFuncAttributes attr;
   cudaError_t err = cudaFuncGetAttributes(&attr, kern);
   if (err != cudaSuccess) return err;
@@ -691,7 +747,7 @@ cudaError_t run_mx(const GemmArgs& a, int sm_count, cudaStream_t stream, bool* t
     const uint64_t sB[1] = {static_cast<uint64_t>(a.K)};
     if (!encode_operand(&tmB, a.b, 2, dB, sB, b_rows)) { *tmap_failed = true; return cudaErrorInvalidValue; }
   }
-  if (!encode_output(&tmD, a.d, a.M, a.N, a.out_bf16, kOutRows)) { *tmap_failed = true; return cudaErrorInvalidValue; }
+  if (!encode_output(&tmD, a.d, kSegK ? a.M * a.num_groups : a.M, a.N, a.out_bf16, kOutRows)) { *tmap_failed = true; return cudaErrorInvalidValue; }
 
   KParams kp;
   kp.sa = a.sa;
@@ -709,7 +765,7 @@ cudaError_t run_mx(const GemmArgs& a, int sm_count, cudaStream_t stream, bool* t
   const int64_t ntn = (a.N + BN - 1) / BN;
   int64_t mt_bound = kGrouped ? (a.M / kBlockM + a.num_groups) : (a.M + kBlockM - 1) / kBlockM;
   if (kPair) mt_bound = (mt_bound + 1) / 2;
-  const int64_t units = mt_bound * ntn;
+  const int64_t units = mt_bound * ntn * (kSegK ? a.num_groups : 1);
   if (units <= 0) return cudaSuccess;
   static std::atomic<int> cluster_cache[kMaxCachedDevices];  // co-resident clusters, per device
   return launch_persistent<kPair>(kern, units, sm_count, kMxThreads, C::kSmemBytes, stream, cluster_cache, tmA, tmB,
@@ -734,6 +790,16 @@ cudaError_t launch_gemm_pow2(const GemmArgs& a, int sm_count, cudaStream_t strea
                   : run_mx<256, true, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
   return narrow ? run_mx<128, false, false, false>(a, sm_count, stream, tmap_failed, reg_check_failed)
                 : run_mx<256, false, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
+}
+
+cudaError_t launch_wgrad_pow2(const GemmArgs& a, int sm_count, cudaStream_t stream, bool* tmap_failed,
+                              bool* reg_check_failed) {
+  *tmap_failed = false;
+  *reg_check_failed = false;
+  const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256) * a.num_groups;
+  if (a.M <= 128 || a.N <= 128 || 2 * tiles < sm_count)
+    return run_mx<128, true, false, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
+  return run_mx<256, true, false, true, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
 }
 
 cudaError_t gemm_mx_take_status(int* status) {

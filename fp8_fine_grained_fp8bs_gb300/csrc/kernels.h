@@ -72,6 +72,11 @@ cudaError_t gemm_take_status(int* status);
 // in [2^-127, 2^127] records FP8BS_ERR_DEVICE_ARG in its status word.
 cudaError_t launch_gemm_pow2(const GemmArgs& args, int sm_count, cudaStream_t stream, bool* tmap_failed,
                              bool* reg_check_failed);
+// The experts' weight gradients: a [M][K] and b [N][K] hold all experts' rows
+// along K (K / 128 blocks, sa [K/128][M], sb [K/128][N]), offsets the segments;
+// d [num_groups][M][N].
+cudaError_t launch_wgrad_pow2(const GemmArgs& args, int sm_count, cudaStream_t stream, bool* tmap_failed,
+                              bool* reg_check_failed);
 cudaError_t gemm_mx_take_status(int* status);
 
 // ---- fp4.cu (4-bit quantisers and dequantiser; plain loads, no waits)
@@ -163,6 +168,74 @@ cudaError_t launch_gather_bf16_rows(const uint16_t* y, int64_t rows_in, int64_t 
                                     int64_t rows_out, uint16_t* out, int sm_count, cudaStream_t stream);
 cudaError_t launch_moe_combine(const uint16_t* y, int64_t rows_y, int64_t N, const int32_t* idx, const float* w,
                                int64_t T, int k, uint16_t* out, int sm_count, cudaStream_t stream);
+
+// out[t] = add[t] + the rows of token t (idx < 0: none); add may be NULL.
+cudaError_t launch_moe_dispatch_backward(const uint16_t* d, int64_t rows, int64_t N, const int32_t* idx, int64_t T, int k,
+                                         const uint16_t* add, uint16_t* out, int sm_count, cudaStream_t stream);
+
+// ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; no waits)
+struct NormArgs {
+  const uint16_t* x;       // [M][ldx]
+  const uint16_t* res;     // [M][ldr] or NULL
+  const void* gain;        // [K]
+  bool gain_f32;
+  int64_t M, K, ldx, ldr;
+  float eps;
+  bool pow2;
+  uint16_t* r;             // [M][K] or NULL
+  uint16_t* y;             // [M][K] or NULL
+  uint8_t* q;              // [M][K] or NULL
+  float* s;                // [K/128][M]
+  float* rstd;             // [M] or NULL
+};
+cudaError_t launch_rmsnorm(const NormArgs& args, int sm_count, cudaStream_t stream);
+int64_t rmsnorm_max_columns();
+
+struct NormBackwardArgs {
+  const uint16_t* dy;      // [M][lddy]
+  const uint16_t* r;       // [M][ldr]
+  const void* gain;
+  bool gain_f32;
+  const float* rstd;       // [M]
+  const uint16_t* dres;    // [M][lddres] or NULL
+  int64_t M, K, lddy, ldr, lddres;
+  uint16_t* dx;            // [M][K]
+  float* dgain;            // [K] or NULL
+  bool accumulate;
+};
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& args, void* ws, cudaStream_t stream);
+
+struct CombineBackwardArgs {
+  const uint16_t* dout;      // [T][ldo]
+  int64_t T, N, ldo;
+  const uint16_t* y;         // [rows][N] or NULL
+  int64_t rows;
+  const int32_t* row_of;     // [T][k]
+  const int32_t* row_token;  // [rows]
+  const float* w;            // [T][k]
+  int k;
+  bool pow2;
+  uint16_t* dy;              // [rows][N] or NULL
+  uint8_t* q;                // [rows][N] or NULL
+  float* s;                  // [N/128][rows]
+  float* dw;                 // [T][k] or NULL
+};
+cudaError_t launch_combine_backward(const CombineBackwardArgs& args, int sm_count, cudaStream_t stream);
+
+struct SwigluBackwardArgs {
+  const uint16_t* h;       // [M][ldh]
+  const uint16_t* dv;      // [M][lddv]
+  const int32_t* live;     // [M] or NULL
+  int64_t M, I, ldh, lddv;
+  bool pow2;
+  uint16_t* dh;            // [M][2I] or NULL
+  uint8_t* q;              // [M][2I] or NULL
+  float* s;                // [2I/128][M]
+};
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& args, int sm_count, cudaStream_t stream);
+// Reads and clears the status word (a row_token that does not fit row_of).
+cudaError_t train_take_status(int* status);
 
 // Diagnostic: a kernel whose bounded wait runs out (nothing ever arrives on
 // its barrier) and records FP8BS_ERR_TIMEOUT in the GEMM status word.

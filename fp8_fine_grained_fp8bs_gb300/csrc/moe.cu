@@ -19,7 +19,9 @@
 //   * moe_combine: out[t] = BF16(sum_j w[t][j] * y[idx[t][j]]) with the
 //     products and the sum in FP32 (j ascending, one rounding to BF16);
 //     idx[t][j] < 0 contributes nothing.
-// All three are memory-bound copies: one warp per row, 16-byte accesses.
+//   * moe_dispatch_backward: out[t] = BF16(add[t] + sum_j d[idx[t][j]]), the
+//     gradient of the dispatch (each token's row copied to its k rows).
+// All are memory-bound copies: one warp per row, 16-byte accesses.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -145,21 +147,26 @@ __device__ __forceinline__ void axpy8(float (&acc)[8], float w, const uint4& v) 
   }
 }
 
+// kWeighted: the combine.  Without weights it is the gradient of the dispatch
+// (the sum of a token's rows), which starts from `add` (or NULL; it may be
+// `out` itself).
+template <bool kWeighted>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const uint16_t* __restrict__ y, int64_t rows_y,
                                                                    int64_t N, const int32_t* __restrict__ idx,
                                                                    const float* __restrict__ w, int64_t T, int k,
-                                                                   uint16_t* __restrict__ out) {
+                                                                   const uint16_t* add, uint16_t* out) {
   constexpr int kBatch = 8;  // expert rows whose loads are in flight together
   const int lane = threadIdx.x & 31;
   const int64_t vec = N / 8;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kMoeWarps + (threadIdx.x >> 5); t < T;
        t += static_cast<int64_t>(gridDim.x) * kMoeWarps) {
     const int32_t* it = idx + t * k;
-    const float* wt = w + t * k;
+    const float* wt = kWeighted ? w + t * k : nullptr;
     for (int64_t v = lane; v < vec; v += 32) {
       float acc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+      if (!kWeighted && add != nullptr) axpy8(acc, 1.0f, reinterpret_cast<const uint4*>(add + t * N)[v]);
       for (int j0 = 0; j0 < k; j0 += kBatch) {
         // all of the batch's loads first, then the multiply-adds in j order
         uint4 val[kBatch];
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const uint16_t
           const int32_t src = j < k ? it[j] : -1;
           const bool ok = src >= 0 && src < rows_y;
           okj[u] = ok;
-          wj[u] = ok ? wt[j] : 0.0f;
+          wj[u] = kWeighted ? (ok ? wt[j] : 0.0f) : 1.0f;
           val[u] = ok ? __ldg(reinterpret_cast<const uint4*>(y + static_cast<int64_t>(src) * N) + v)
                       : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -232,7 +239,16 @@ cudaError_t launch_gather_bf16_rows(const uint16_t* y, int64_t rows_in, int64_t 
 cudaError_t launch_moe_combine(const uint16_t* y, int64_t rows_y, int64_t N, const int32_t* idx, const float* w,
                                int64_t T, int k, uint16_t* out, int sm_count, cudaStream_t stream) {
   if (T <= 0) return cudaSuccess;
-  moe_combine_kernel<<<grid_for_rows(T, sm_count), kMoeThreads, 0, stream>>>(y, rows_y, N, idx, w, T, k, out);
+  moe_combine_kernel<true>
+      <<<grid_for_rows(T, sm_count), kMoeThreads, 0, stream>>>(y, rows_y, N, idx, w, T, k, nullptr, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_moe_dispatch_backward(const uint16_t* d, int64_t rows, int64_t N, const int32_t* idx, int64_t T, int k,
+                                         const uint16_t* add, uint16_t* out, int sm_count, cudaStream_t stream) {
+  if (T <= 0) return cudaSuccess;
+  moe_combine_kernel<false>
+      <<<grid_for_rows(T, sm_count), kMoeThreads, 0, stream>>>(d, rows, N, idx, nullptr, T, k, add, out);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,656 @@
+// Operators of a training step around the 8-bit products: the root-mean-square
+// norm with the residual's addition and 8-bit output, its gradient, the
+// gradient of the MoE combine (the experts' output gradients in their
+// segments, quantised, and the gate weights' gradient), and the gradient of
+// the SwiGLU with 8-bit output.
+//
+// What is quantised is the BF16 value that the unfused operator would store,
+// so codes and scales are those of fp8bs_quantize_act_ex on it (one rounding
+// to BF16, then the quantiser's).  Statistics and sums are float32.  All are
+// memory-bound streams: every input is read once, into registers.
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "group_quant.cuh"
+#include "kernels.h"
+#include "launch.h"
+#include "tmap.h"
+
+namespace fp8bs {
+namespace {
+
+__device__ int g_train_status;
+
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Eight float32 values rounded to BF16 (nearest, ties to even).
+__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight gains from column c on.
+template <bool kF32>
+__device__ __forceinline__ void load_gain(const void* gain, int c, float (&f)[8]) {
+  if (kF32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gain) + c);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gain) + c)), f);
+  }
+}
+
+template <bool kPow2>
+__device__ __forceinline__ Divisor divisor_of(uint32_t a16) {
+  return kPow2 ? pow2_divisor_bits(a16) : make_divisor(__uint_as_float(a16 << 16));
+}
+
+// Eight values of a group -> eight codes.  A power-of-two divisor's quotient is
+// one exact product, which keeps the sign of a zero.
+template <bool kPow2>
+__device__ __forceinline__ uint2 quant8(const uint4& v, const Divisor& d) {
+  if (!kPow2 || !d.fast) return quant8m(v, d);
+  float f[8];
+  widen8(v, f);
+  const float2 y2 = make_float2(d.y, d.y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 r = __fmul2_rn(make_float2(f[2 * i], f[2 * i + 1]), y2);
+    f[2 * i] = r.x;
+    f[2 * i + 1] = r.y;
+  }
+  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+}
+
+// |x| maximum (BF16 bits) over the 16 lanes of each half-warp; every lane of the warp takes part.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
+#pragma unroll
+  for (int o = 1; o <= 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A row is held by `warps` warps, kVecs 16-byte pieces a thread; short rows
+// share a CTA.  Sums of a row: lanes, then warps, in a fixed order.
+constexpr int kNormMaxThreads = 512;
+constexpr int kMaxNormK = 16384;   // 512 threads x 4 pieces x 8 values
+
+struct RowPlace {
+  int warps;   // warps per row
+  int rows;    // rows per CTA
+  int vecs;    // pieces per thread
+};
+inline RowPlace place_rows(int K) {
+  RowPlace p;
+  const int nv = (K + 7) / 8;
+  p.vecs = nv > 256 ? 4 : nv > 64 ? 2 : 1;
+  p.warps = (nv + 32 * p.vecs - 1) / (32 * p.vecs);
+  p.rows = std::max(1, 8 / p.warps);
+  return p;
+}
+
+// Sum over the row's warps; s_part: one float per warp of the CTA, alternating
+// between two sets so that one barrier per row is enough.
+__device__ __forceinline__ float row_sum(float v, int warps, float (*s_part)[kNormMaxThreads / 32], int& parity) {
+  v = warp_sum(v);
+  if (warps == 1) return v;
+  const int warp = threadIdx.x >> 5, first = warp / warps * warps;
+  if ((threadIdx.x & 31) == 0) s_part[parity][warp] = v;
+  __syncthreads();
+  float sum = s_part[parity][first];
+  for (int i = 1; i < warps; ++i) sum += s_part[parity][first + i];
+  parity ^= 1;
+  return sum;
+}
+
+// ------------------------------------------------------------------- norm
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* res;   // or NULL
+  const void* gain;
+  int64_t M, ldx, ldr;
+  int K, warps;
+  float eps;
+  uint16_t* r;           // or NULL
+  uint16_t* y;           // or NULL
+  uint8_t* q;            // or NULL (with s)
+  float* s;
+  float* rstd;           // or NULL
+};
+
+template <int kVecs, bool kGainF32, bool kPow2>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams p) {
+  __shared__ float s_part[2][kNormMaxThreads / 32];
+  griddep_launch_dependents();
+  const int T = 32 * p.warps;
+  const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
+  const int rows = blockDim.x / T;
+  const int nv = p.K / 8;
+  int parity = 0;
+  griddep_wait();
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows; row0 < p.M; row0 += static_cast<int64_t>(gridDim.x) * rows) {
+    const int64_t row = row0 + sub;
+    const bool live = row < p.M;
+    uint4 v[kVecs];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && c < nv) v[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + 8 * c);
+    }
+    if (p.res != nullptr) {
+      uint4 w[kVecs];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int c = i * T + t;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && c < nv) w[i] = *reinterpret_cast<const uint4*>(p.res + row * p.ldr + 8 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        float a[8], b[8];
+        widen8(v[i], a);
+        widen8(w[i], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+        v[i] = round8(a);
+        const int c = i * T + t;
+        if (live && c < nv) *reinterpret_cast<uint4*>(p.r + row * p.K + 8 * c) = v[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float a[8];
+      widen8(v[i], a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], sum);
+    }
+    sum = row_sum(sum, p.warps, s_part, parity);
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.K) + p.eps);
+    if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      const bool here = live && c < nv;
+      float a[8], g[8];
+      widen8(v[i], a);
+      if (here) {
+        load_gain<kGainF32>(p.gain, 8 * c, g);
+        // r * gain is exact for a BF16 gain, so y is rounded once before BF16
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = a[e] * g[e] * rstd;
+      }
+      const uint4 y = round8(a);
+      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + row * p.K + 8 * c) = y;
+      if (p.q != nullptr) {
+        const Divisor d = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(y)) & 0xFFFFu));
+        if (here) {
+          *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * c) = quant8<kPow2>(y, d);
+          if ((c & 15) == 0) p.s[static_cast<int64_t>(c >> 4) * p.M + row] = d.s;
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------- norm's gradient
+struct NormBackwardParams {
+  const uint16_t* dy;
+  const uint16_t* r;
+  const void* gain;
+  const float* rstd;
+  const uint16_t* dres;  // or NULL
+  int64_t M, lddy, ldr, lddres;
+  int K, warps;
+  uint16_t* dx;
+  float* part;           // [parts][K], or NULL: no gain gradient
+};
+
+constexpr int kNormParts = 304;   // CTAs: two on each of the 152 SMs
+
+// With t = dy gain: dx = rstd t - r rstd^3 mean(t r) + dres.  dy r is exact in
+// float32 and serves the mean and the gain's sum.
+template <int kVecs, bool kGainF32>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const NormBackwardParams p) {
+  __shared__ float s_part[2][kNormMaxThreads / 32];
+  griddep_launch_dependents();
+  const int T = 32 * p.warps;
+  const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
+  const int rows = blockDim.x / T;
+  const int nv = p.K / 8;
+  int parity = 0;
+  float acc[kVecs][8];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+  griddep_wait();
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows; row0 < p.M; row0 += static_cast<int64_t>(gridDim.x) * rows) {
+    const int64_t row = row0 + sub;
+    const bool live = row < p.M;
+    uint4 d[kVecs], r[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      d[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && c < nv) {
+        d[i] = *reinterpret_cast<const uint4*>(p.dy + row * p.lddy + 8 * c);
+        r[i] = *reinterpret_cast<const uint4*>(p.r + row * p.ldr + 8 * c);
+      }
+    }
+    const float rstd = live ? p.rstd[row] : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      if (!(live && c < nv)) continue;
+      float a[8], b[8], g[8];
+      widen8(d[i], a);
+      widen8(r[i], b);
+      load_gain<kGainF32>(p.gain, 8 * c, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float ab = a[e] * b[e];
+        sum = fmaf(ab, g[e], sum);
+        acc[i][e] = fmaf(ab, rstd, acc[i][e]);
+      }
+    }
+    sum = row_sum(sum, p.warps, s_part, parity);
+    const float f = rstd * rstd * (rstd * (sum / static_cast<float>(p.K)));
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      if (!(live && c < nv)) continue;
+      float a[8], b[8], g[8];
+      widen8(d[i], a);
+      widen8(r[i], b);
+      load_gain<kGainF32>(p.gain, 8 * c, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] = fmaf(-b[e], f, a[e] * g[e] * rstd);
+      if (p.dres != nullptr) {
+        widen8(*reinterpret_cast<const uint4*>(p.dres + row * p.lddres + 8 * c), b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+      }
+      *reinterpret_cast<uint4*>(p.dx + row * p.K + 8 * c) = round8(a);
+    }
+  }
+  if (p.part == nullptr) return;
+  float* out = p.part + (static_cast<int64_t>(blockIdx.x) * rows + sub) * p.K;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = i * T + t;
+    if (c >= nv) continue;
+    float4* o = reinterpret_cast<float4*>(out + 8 * c);
+    o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+  }
+}
+
+// The gain's gradient: the CTAs' partial sums added up, 32 columns a CTA, each
+// of its eight warps an eighth of the parts, in a fixed order.
+__global__ void __launch_bounds__(256) norm_gain_kernel(const float* part, int parts, int K, float* dgain, int accumulate) {
+  __shared__ float s_sum[8][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (c < K) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += 8) sum += part[static_cast<int64_t>(i) * K + c];
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || c >= K) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += s_sum[i][lane];
+  dgain[c] = accumulate ? dgain[c] + sum : sum;
+}
+
+// ------------------------------------------------------ combine's gradient
+struct CombineBackwardParams {
+  const uint16_t* dout;
+  int64_t T, ldo, N;
+  const uint16_t* y;         // NULL: no weight gradient
+  int64_t rows;
+  const int32_t* row_of;     // [T][k]
+  const int32_t* row_token;  // [rows]
+  const float* w;            // [T][k]
+  int k, slots;              // slots per CTA
+  int splits;                // CTAs per token
+  uint16_t* dy;              // or NULL
+  uint8_t* q;                // or NULL (with s)
+  float* s;
+  float* dw;                 // or NULL
+};
+
+constexpr int kCbThreads = 256;
+constexpr int kCbSlots = 8;       // most slots per CTA
+constexpr int kCbZeroRows = 16;   // padding rows looked at by one CTA
+
+// One token and up to kCbSlots of its choices per CTA: a piece of dout is read
+// once, multiplied by each choice's weight into the choice's row, and by the
+// choice's row of y into the weight's gradient.  max |BF16(w x)| over a group is
+// BF16(|w| max |x|), since both roundings are monotonic, so one maximum serves
+// all choices.  CTAs behind the tokens' zero the rows without a token.
+template <bool kPow2>
+__global__ void __launch_bounds__(kCbThreads) combine_backward_kernel(const CombineBackwardParams p) {
+  __shared__ int32_t s_row[kCbSlots];     // the slot's row, -1: none
+  __shared__ float s_w[kCbSlots];         // the row's weight
+  __shared__ int s_write[kCbSlots];       // this slot writes the row
+  __shared__ float s_dot[kCbSlots][kCbThreads / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nv = static_cast<int>(p.N / 8);
+  const int64_t nkb = p.N / kGroup;
+  const int64_t work = p.T * p.splits;
+  if (blockIdx.x >= work) {
+    const int64_t r0 = (blockIdx.x - work) * kCbZeroRows;
+    for (int64_t row = r0 + warp; row < r0 + kCbZeroRows && row < p.rows; row += kCbThreads / 32) {
+      if (p.row_token[row] >= 0) continue;
+      if (p.dy != nullptr)
+        for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
+      if (p.q != nullptr) {
+        for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = make_uint2(0u, 0u);
+        for (int64_t kb = lane; kb < nkb; kb += 32) p.s[kb * p.rows + row] = 0.0f;
+      }
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x / p.splits;
+  const int j0 = static_cast<int>(blockIdx.x - t * p.splits) * p.slots;
+  const int n = min(p.slots, p.k - j0);
+  if (threadIdx.x < n) {
+    const int j = j0 + threadIdx.x;
+    const int32_t row = p.row_of[t * p.k + j];
+    bool ok = row >= 0 && row < p.rows;
+    if (ok && p.row_token[row] != t) {
+      atomicCAS(&g_train_status, 0, kStatusDeviceArg);
+      ok = false;
+    }
+    // a row named by several slots takes the sum of their weights, once
+    float w = 0.0f;
+    bool first = ok;
+    for (int i = 0; i < p.k; ++i) {
+      if (p.row_of[t * p.k + i] != row) continue;
+      w += p.w[t * p.k + i];
+      if (i < j) first = false;
+    }
+    s_row[threadIdx.x] = ok ? row : -1;
+    s_w[threadIdx.x] = w;
+    s_write[threadIdx.x] = first;
+  }
+  __syncthreads();
+  float dot[kCbSlots];
+#pragma unroll
+  for (int j = 0; j < kCbSlots; ++j) dot[j] = 0.0f;
+  // whole warps go through the loop together (half-warp maxima)
+  for (int v0 = 32 * warp; v0 < nv; v0 += kCbThreads) {
+    const int v = v0 + lane;
+    const bool here = v < nv;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (here) x = __ldg(reinterpret_cast<const uint4*>(p.dout + t * p.ldo + 8 * v));
+    uint4 y[kCbSlots];
+    if (p.dw != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kCbSlots; ++j) {
+        y[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < n && here && s_row[j] >= 0)
+          y[j] = __ldg(reinterpret_cast<const uint4*>(p.y + static_cast<int64_t>(s_row[j]) * p.N + 8 * v));
+      }
+    }
+    const float amax = __uint_as_float(half_warp_max(umax_halves(absmax8_bits(x)) & 0xFFFFu) << 16);
+    float a[8];
+    widen8(x, a);
+#pragma unroll
+    for (int j = 0; j < kCbSlots; ++j) {
+      if (j >= n || s_row[j] < 0) continue;
+      if (p.dw != nullptr) {
+        float b[8];
+        widen8(y[j], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot[j] = fmaf(a[e], b[e], dot[j]);
+      }
+      if (!s_write[j] || !here) continue;
+      const int64_t row = s_row[j];
+      const float w = s_w[j];
+      float b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = a[e] * w;
+      const uint4 d = round8(b);
+      if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = d;
+      if (p.q != nullptr) {
+        const Divisor dv = divisor_of<kPow2>(static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(amax * fabsf(w)))));
+        *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = quant8<kPow2>(d, dv);
+        if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = dv.s;
+      }
+    }
+  }
+  if (p.dw == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < kCbSlots; ++j) {
+    if (j >= n) break;
+    const float sum = warp_sum(dot[j]);
+    if (lane == 0) s_dot[j][warp] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < n) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCbThreads / 32; ++i) sum += s_dot[threadIdx.x][i];
+    p.dw[t * p.k + j0 + threadIdx.x] = s_row[threadIdx.x] >= 0 ? sum : 0.0f;
+  }
+}
+
+// ------------------------------------------------------- SwiGLU's gradient
+struct SwigluBackwardParams {
+  const uint16_t* h;
+  const uint16_t* dv;
+  const int32_t* live;   // or NULL
+  int64_t M, I, ldh, lddv;
+  uint16_t* dh;          // [M][2I] or NULL
+  uint8_t* q;            // or NULL (with s)
+  float* s;
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// d silu(g) u / d (g, u) times dv.  With e = e^-|g| and c = 1 / (1 + e), sigma(g)
+// and sigma(-g) are c and e c in one order or the other, so neither overflows nor
+// cancels.  Below -64, where e runs out of float32's normal numbers in the end,
+// sigma(g) = e^g to within 2^-92 and e^g is applied as its root twice, once to the
+// larger factor, so that the product does not underflow on the way.
+__device__ __forceinline__ void swiglu_grad(float g, float u, float dv, float& dg, float& du) {
+  if (g < -64.0f) {
+    const float root = expf(0.5f * g);
+    const bool first = fabsf(dv) > fabsf(u);
+    du = dv * root * (g * root);
+    dg = (first ? dv : u) * root * (first ? u : dv) * root * (1.0f + g);
+    return;
+  }
+  const float e = expf(-fabsf(g));
+  const float c = rcp_approx(1.0f + e);
+  const float ec = e * c;
+  const float sig = g >= 0.0f ? c : ec, other = g >= 0.0f ? ec : c;
+  du = dv * (g * sig);
+  dg = dv * u * (sig * fmaf(g, other, 1.0f));
+}
+
+constexpr int kSbThreads = 256;
+
+template <bool kPow2>
+__global__ void __launch_bounds__(kSbThreads) swiglu_backward_kernel(const SwigluBackwardParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t upr = p.I / 8;                        // pieces of 8 columns a row, a multiple of 16
+  const int64_t units = p.M * upr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kSbThreads;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kSbThreads + threadIdx.x - lane; u0 < units; u0 += step) {
+    const int64_t unit = u0 + lane;
+    const bool here = unit < units;
+    const int64_t row = here ? unit / upr : 0;
+    const int64_t c = here ? unit - row * upr : 0;
+    float dg[8], du[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[e] = du[e] = 0.0f;
+    if (here && (p.live == nullptr || p.live[row] >= 0)) {
+      const uint16_t* hr = p.h + row * p.ldh + 8 * c;
+      const uint4 gw = __ldg(reinterpret_cast<const uint4*>(hr)), uw = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
+      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(p.dv + row * p.lddv + 8 * c));
+      float g[8], u[8], v[8];
+      widen8(gw, g);
+      widen8(uw, u);
+      widen8(vw, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e]);
+    }
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const uint4 d = round8(part == 0 ? dg : du);
+      const int64_t col = part * p.I + 8 * c;
+      if (here && p.dh != nullptr) *reinterpret_cast<uint4*>(p.dh + row * 2 * p.I + col) = d;
+      if (p.q != nullptr) {
+        const Divisor dv = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(d)) & 0xFFFFu));
+        if (here) {
+          *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = quant8<kPow2>(d, dv);
+          if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = dv.s;
+        }
+      }
+    }
+  }
+}
+
+// CTAs of `kern` that fit on the device at once.
+template <typename Kern>
+cudaError_t resident_ctas(Kern kern, int threads, int sm_count, std::atomic<int> (&cache)[kMaxCachedDevices], int64_t* n) {
+  int per_sm = 0;
+  const cudaError_t e = cached_per_device(
+      cache, [&](int* v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, threads, 0); }, &per_sm);
+  *n = static_cast<int64_t>(per_sm) * sm_count;
+  return e;
+}
+
+template <int kVecs, bool kGainF32, bool kPow2>
+cudaError_t run_norm(const NormParams& p, const RowPlace& at, int sm_count, cudaStream_t stream) {
+  auto kern = norm_kernel<kVecs, kGainF32, kPow2>;
+  const int threads = 32 * at.warps * at.rows;
+  static std::atomic<int> cache[kNormMaxThreads / 32 + 1][kMaxCachedDevices];
+  int64_t slots = 0;
+  const cudaError_t e = resident_ctas(kern, threads, sm_count, cache[threads / 32], &slots);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (p.M + at.rows - 1) / at.rows;
+  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), threads, stream, p);
+}
+
+template <int kVecs>
+cudaError_t run_norm_kind(const NormParams& p, const RowPlace& at, bool gain_f32, bool pow2, int sm_count, cudaStream_t stream) {
+  if (gain_f32)
+    return pow2 ? run_norm<kVecs, true, true>(p, at, sm_count, stream) : run_norm<kVecs, true, false>(p, at, sm_count, stream);
+  return pow2 ? run_norm<kVecs, false, true>(p, at, sm_count, stream) : run_norm<kVecs, false, false>(p, at, sm_count, stream);
+}
+
+int norm_grid(int64_t M, int rows) { return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, kNormParts)); }
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream) {
+  const RowPlace at = place_rows(static_cast<int>(a.K));
+  NormParams p;
+  p.x = a.x; p.res = a.res; p.gain = a.gain; p.M = a.M; p.ldx = a.ldx; p.ldr = a.ldr; p.K = static_cast<int>(a.K);
+  p.warps = at.warps; p.eps = a.eps; p.r = a.r; p.y = a.y; p.q = a.q; p.s = a.s; p.rstd = a.rstd;
+  return at.vecs == 4   ? run_norm_kind<4>(p, at, a.gain_f32, a.pow2, sm_count, stream)
+         : at.vecs == 2 ? run_norm_kind<2>(p, at, a.gain_f32, a.pow2, sm_count, stream)
+                        : run_norm_kind<1>(p, at, a.gain_f32, a.pow2, sm_count, stream);
+}
+
+int64_t rmsnorm_max_columns() { return kMaxNormK; }
+
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
+  if (M == 0 || K == 0) return 0;
+  const RowPlace at = place_rows(static_cast<int>(K));
+  return 4 * K * norm_grid(M, at.rows) * at.rows;
+}
+
+cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, void* ws, cudaStream_t stream) {
+  const RowPlace at = place_rows(static_cast<int>(a.K));
+  const int grid = norm_grid(a.M, at.rows), threads = 32 * at.warps * at.rows;
+  NormBackwardParams p;
+  p.dy = a.dy; p.r = a.r; p.gain = a.gain; p.rstd = a.rstd; p.dres = a.dres; p.M = a.M; p.lddy = a.lddy; p.ldr = a.ldr;
+  p.lddres = a.lddres; p.K = static_cast<int>(a.K); p.warps = at.warps; p.dx = a.dx;
+  p.part = a.dgain != nullptr ? static_cast<float*>(ws) : nullptr;
+  auto kern = at.vecs == 4   ? (a.gain_f32 ? norm_backward_kernel<4, true> : norm_backward_kernel<4, false>)
+              : at.vecs == 2 ? (a.gain_f32 ? norm_backward_kernel<2, true> : norm_backward_kernel<2, false>)
+                             : (a.gain_f32 ? norm_backward_kernel<1, true> : norm_backward_kernel<1, false>);
+  const cudaError_t e = launch_behind(kern, dim3(grid), threads, stream, p);
+  if (e != cudaSuccess || a.dgain == nullptr) return e;
+  return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), 256, stream,
+                       static_cast<const float*>(p.part), grid * at.rows, p.K, a.dgain, a.accumulate ? 1 : 0);
+}
+
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int sm_count, cudaStream_t stream) {
+  CombineBackwardParams p;
+  p.dout = a.dout; p.T = a.T; p.ldo = a.ldo; p.N = a.N; p.y = a.y; p.rows = a.rows; p.row_of = a.row_of;
+  p.row_token = a.row_token; p.w = a.w; p.k = a.k; p.dy = a.dy; p.q = a.q; p.s = a.s; p.dw = a.dw;
+  // few tokens: one choice per CTA, so that more SMs share them
+  p.slots = a.T * ((a.k + kCbSlots - 1) / kCbSlots) < 2 * sm_count ? 1 : std::min(a.k, kCbSlots);
+  p.splits = (a.k + p.slots - 1) / p.slots;
+  const int64_t grid = a.T * p.splits + (a.rows + kCbZeroRows - 1) / kCbZeroRows;
+  if (grid <= 0) return cudaSuccess;
+  return launch_behind(a.pow2 ? combine_backward_kernel<true> : combine_backward_kernel<false>,
+                       dim3(static_cast<unsigned>(grid)), kCbThreads, stream, p);
+}
+
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cudaStream_t stream) {
+  SwigluBackwardParams p;
+  p.h = a.h; p.dv = a.dv; p.live = a.live; p.M = a.M; p.I = a.I; p.ldh = a.ldh; p.lddv = a.lddv;
+  p.dh = a.dh; p.q = a.q; p.s = a.s;
+  auto kern = a.pow2 ? swiglu_backward_kernel<true> : swiglu_backward_kernel<false>;
+  static std::atomic<int> cache[2][kMaxCachedDevices];
+  int64_t slots = 0;
+  const cudaError_t e = resident_ctas(kern, kSbThreads, sm_count, cache[a.pow2 ? 1 : 0], &slots);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (p.M * (p.I / 8) + kSbThreads - 1) / kSbThreads;
+  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), kSbThreads, stream, p);
+}
+
+cudaError_t train_take_status(int* status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_train_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_train_status, &zero, sizeof(int));
+  }
+  *status = v;
+  return e;
+}
+
+}  // namespace fp8bs

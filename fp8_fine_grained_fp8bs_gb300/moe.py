@@ -38,8 +38,15 @@ moe_layer_fp4() routes the tokens (fp8bs_moe_route), lays the choices out
 (fp8bs_moe_layout, the same segments as RecvPlan's), quantises the tokens'
 rows into them, runs the two grouped 4-bit GEMMs around the SwiGLU and
 combines, without reading anything back, so it can be captured in a CUDA graph.
+
+moe_layer_fp8() is the same layer with 8-bit experts and power-of-two scales, to be
+trained: moe_layer_fp8_backward() gives the gradients of its input, its router's
+logits and its experts' weights, every product of it in 8 bits as in the forward
+pass (the layer's inputs re-tiled from 1x128 to 128x1 groups for the weights').
 """
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import numpy as np
 
@@ -247,3 +254,110 @@ def moe_layer_fp4(x, logits, experts, k: int, fmt: int = 0, score: int = 0, bias
     h = grouped_gemm_fp4(quantize_fp4(x, fmt, rows=row_token), offsets, gate_up, fmt)
     y = grouped_gemm_fp4(swiglu_quantize_fp4(h, fmt, live=row_token), offsets, down, fmt)
     return _kernel_combine(y, row_of, route[1]), route
+
+
+class Fp8Experts(NamedTuple):
+    """Codes and scales of the experts' weights, each as the products read them: gate/up [E, 2I, H] and
+    down [E, H, I] forward, their transposes [E, H, 2I] and [E, I, H] backward (None for serving only)."""
+    gate_up: tuple
+    down: tuple
+    gate_up_t: tuple | None
+    down_t: tuple | None
+
+
+def quantize_experts_fp8(w_gate_up, w_down, train: bool = True) -> Fp8Experts:
+    """The experts' weights in 8 bits, once per update: w_gate_up [E, 2I, H] (gate | up) and w_down
+    [E, H, I] bfloat16 CUDA tensors, power-of-two scales; without ``train`` no transposed copies."""
+    import torch
+    from . import SCALE_POW2, fp8bs_quantize_weight_ex
+
+    def quantise(w):
+        E, N, K = w.shape
+        if w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous():
+            raise ValueError("weights: contiguous bfloat16 CUDA tensors [E, N, K]")
+        if N % 128 != 0 or K % 128 != 0:
+            raise ValueError(f"weights: {N} x {K}, expected multiples of 128")
+        q = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
+        s = torch.empty((E, N // 128, K // 128), dtype=torch.float32, device=w.device)
+        if not train:      # the experts' blocks follow one another
+            fp8bs_quantize_weight_ex(w, E * N, K, K, q, s, scale_mode=SCALE_POW2)
+            return (q, s), None
+        qt = torch.empty((E, K, N), dtype=torch.uint8, device=w.device)
+        st = torch.empty((E, K // 128, N // 128), dtype=torch.float32, device=w.device)
+        for e in range(E):
+            # expert e's scales may start off 16 bytes, which the library takes for weights
+            fp8bs_quantize_weight_ex(w[e], N, K, K, q[e], s[e], qt[e], st[e], SCALE_POW2)
+        return (q, s), (qt, st)
+
+    gate_up, gate_up_t = quantise(w_gate_up)
+    down, down_t = quantise(w_down)
+    return Fp8Experts(gate_up, down, gate_up_t, down_t)
+
+
+class Fp8Saved(NamedTuple):
+    """What moe_layer_fp8_backward needs of the forward pass."""
+    logits: object
+    route: tuple           # moe_route's result
+    routing: dict          # how moe_route was called
+    layout: tuple          # offsets, row_token, row_of
+    x: tuple               # the dispatched rows' codes and scales
+    h: object              # the gate/up projection's output
+    v: tuple               # the SwiGLU's codes and scales
+    y: object              # the experts' outputs
+
+
+def moe_layer_fp8(xq, sx, logits, experts: Fp8Experts, k: int, score: int = 0, bias=None, valid=None, scale: float = 1.0,
+                  seq=None, alpha: float | None = None):
+    """One MoE layer with 8-bit experts on one rank: xq [T, H] E4M3 codes and sx [H/128, T] their
+    power-of-two scales (rmsnorm_quantize or quantize_act with ``pow2``), logits [T, E] (float32 or bfloat16,
+    the router's product), experts from quantize_experts_fp8.  Returns (out [T, H] bfloat16, saved): saved
+    goes to moe_layer_fp8_backward; saved.route is moe_route's result, with ``alpha`` the balance loss in it.
+    Every launch is on the current stream; nothing is read back."""
+    from . import grouped_gemm, moe_layout, moe_route, swiglu_quantize
+    if xq.dim() != 2 or logits.dim() != 2 or xq.shape[0] != logits.shape[0]:
+        raise ValueError(f"xq {tuple(xq.shape)} and logits {tuple(logits.shape)}: one row per token each")
+    if tuple(sx.shape) != (xq.shape[1] // 128, xq.shape[0]):
+        raise ValueError(f"sx: shape {tuple(sx.shape)} for codes {tuple(xq.shape)}")
+    E, two_i, H = experts.gate_up[0].shape
+    if logits.shape[1] != E or xq.shape[1] != H or tuple(experts.down[0].shape) != (E, H, two_i // 2):
+        raise ValueError(f"xq {tuple(xq.shape)}, logits {tuple(logits.shape)} and experts "
+                         f"{tuple(experts.gate_up[0].shape)}, {tuple(experts.down[0].shape)} do not fit")
+    routing = dict(score=score, valid=valid, seq=seq, scale=scale)
+    route = moe_route(logits, k, bias=bias, alpha=alpha, **routing)
+    layout = offsets, row_token, row_of = moe_layout(route[0], E)
+    x = _kernel_gather_q(xq, sx, True, row_token, True)
+    h = grouped_gemm(*x, offsets, *experts.gate_up, pow2=True)
+    v = swiglu_quantize(h, pow2=True)
+    y = grouped_gemm(*v, offsets, *experts.down, pow2=True)
+    routing["alpha"] = 0.0 if alpha is None else alpha
+    return _kernel_combine(y, row_of, route[1]), Fp8Saved(logits, route, routing, layout, x, h, v, y)
+
+
+def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=None, dx_add=None, dw_gate_up=None, dw_down=None):
+    """Gradients of moe_layer_fp8 from dout [T, H] bfloat16 (and dloss, one float32, of the balance loss):
+    (dx [T, H] bfloat16, the gradient of the values that the layer's input codes stand for, ``dx_add`` added;
+    dlogits; dw_gate_up [E, 2I, H] and dw_down [E, H, I] float32).  Weight gradients given are added to and
+    returned.  The experts are those of the forward pass, with their transposed copies."""
+    from . import (grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward, moe_route_backward,
+                   requant_1x128_to_128x1, swiglu_backward_quantize)
+    if experts.gate_up_t is None:
+        raise ValueError("experts: quantised for serving only, without their transposed copies")
+    idx, w, *stats = saved.route
+    if dloss is not None and not stats:
+        raise ValueError("dloss: the forward pass had no balance loss (alpha)")
+    offsets, row_token, row_of = saved.layout
+    dyq, sdy, _, dw = moe_combine_backward(dout, saved.y, row_of, row_token, w, pow2=True)
+    dv = grouped_gemm(dyq, sdy, offsets, *experts.down_t, pow2=True)
+    dhq, sdh, _ = swiglu_backward_quantize(saved.h, dv, row_token, pow2=True)
+    drows = grouped_gemm(dhq, sdh, offsets, *experts.gate_up_t, pow2=True)
+    dx = moe_dispatch_backward(drows, row_of, dx_add)
+
+    def weights(a, b, out):
+        return grouped_wgrad(*requant_1x128_to_128x1(*a), *requant_1x128_to_128x1(*b), offsets, out=out,
+                             accumulate=out is not None)
+
+    dw_down = weights((dyq, sdy), saved.v, dw_down)
+    dw_gate_up = weights((dhq, sdh), saved.x, dw_gate_up)
+    counts, tokens = stats[:2] if stats else (None, None)
+    dlogits = moe_route_backward(saved.logits, idx, dw, counts=counts, tokens=tokens, dloss=dloss, **saved.routing)
+    return dx, dlogits, dw_gate_up, dw_down

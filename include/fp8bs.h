@@ -537,6 +537,136 @@ int fp8bs_moe_layout(const int32_t* idx, int64_t T, int k, int E, int32_t* offse
 int64_t fp8bs_moe_layout_rows(int64_t T, int k, int E);
 int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E);
 
+/* -------------------------------------------------------------- training
+ * The operators of a training step around the 8-bit products.  Where one
+ * quantises, it quantises the BF16 value that it would store: codes and scales
+ * are bit for bit those of fp8bs_quantize_act_ex on that value.  Sums are taken
+ * in float32 in a fixed order: the same inputs give the same bits.
+ */
+
+#define FP8BS_RMSNORM_MIN_EPS 7.8886090522101181e-31f /* 2^-100: squares that underflow do not count beside it */
+
+/*
+ * Root-mean-square norm of the residual stream, quantised for the Linear that
+ * reads it:
+ *
+ *   r    = residual ? BF16_rne(x + residual) : x      (the sum in float32)
+ *   rstd = 1 / sqrt(mean_k r^2 + eps)                 (float32)
+ *   y    = BF16_rne(r * gain * rstd);   (q, s) = the 1x128 quantisation of y
+ *
+ *   x        [M][ldx] BF16.  residual [M][ldr] BF16, or NULL.           (in)
+ *   gain     [K] float32 or BF16 (fp8bs_in_dtype).                      (in)
+ *   r        [M][K] BF16, given exactly with a residual; it may be x or
+ *            residual itself where that has K columns a row.           (out)
+ *   y        [M][K] BF16 or NULL.                                      (out)
+ *   q, s     [M][K] E4M3 and [K/128][M] float32, both or neither.      (out)
+ *   rstd     [M] float32 or NULL (the gradient reads it).              (out)
+ * At least one of y and q.  Rules: K % 8 == 0, with q K % 128 == 0, K <= 16384;
+ * 2^-100 <= eps <= 1e30; the sum of a row's squares has to stay in float32's
+ * range.  x, residual, gain, r, y and q 16-byte aligned, s and rstd 4.
+ */
+int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* gain, int gain_dtype, float eps, void* r, void* y, uint8_t* q, float* s,
+                           int scale_mode, float* rstd, void* stream);
+
+/*
+ * Its gradient, with t = dy * gain (the gradient through the residual's
+ * addition is dx for both summands):
+ *
+ *   dx      = BF16_rne(rstd t - r rstd^3 mean_k(t r) + dres)
+ *   dgain_k = sum_m dy r rstd          (accumulate: added to what dgain holds)
+ *
+ *   dy    [M][lddy] BF16, the gradient of y.  r [M][ldr] BF16 (x where there
+ *         was no residual).  rstd [M].  dres [M][lddres] BF16 or NULL, what
+ *         reaches r along the residual stream.                          (in)
+ *   dx    [M][K] BF16; it may be dy, r or dres itself where that has K
+ *         columns a row.  dgain [K] float32, or NULL.                  (out)
+ *   ws    scratch of fp8bs_rmsnorm_backward_workspace_bytes(M, K) bytes, 16-byte
+ *         aligned, with dgain; two calls at once need one each.
+ * Rules as above, K % 8 == 0.  M == 0 gives a dgain of zeros.
+ */
+int fp8bs_rmsnorm_backward(const void* dy, int64_t M, int64_t K, int64_t lddy, const void* r, int64_t ldr,
+                           const void* gain, int gain_dtype, const float* rstd, const void* dres, int64_t lddres,
+                           void* dx, float* dgain, int accumulate, void* ws, int64_t ws_bytes, void* stream);
+/* -1 for arguments that fp8bs_rmsnorm_backward refuses. */
+int64_t fp8bs_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/*
+ * Gradient of the SwiGLU v = silu(gate) * up with respect to its input, the
+ * operand of the gate/up projection's gradients:
+ *
+ *   dgate = BF16_rne(dv up sigma(gate) (1 + gate sigma(-gate)))
+ *   dup   = BF16_rne(dv gate sigma(gate));   (q, s) = the 1x128 quantisation
+ *
+ *   h     [M][ldh] BF16, gate in columns [0, I), up in [I, 2I).
+ *   dv    [M][lddv] BF16.  live DEVICE int32 [M] or NULL: live[i] < 0 gives a
+ *         row of zeros, and h's and dv's row is not read.               (in)
+ *   dh    [M][2I] BF16 or NULL: dgate, then dup.                       (out)
+ *   q, s  [M][2I] E4M3 and [2I/128][M] float32, both or neither.       (out)
+ * At least one of dh and q.  Rules: I % 128 == 0, ldh >= 2I, lddv >= I; 16-byte
+ * rows and pointers (live and s: 4).
+ */
+int fp8bs_swiglu_backward_quantize(const void* h, int64_t M, int64_t I, int64_t ldh, const void* dv, int64_t lddv,
+                                   const int32_t* live, void* dh, uint8_t* q, float* s, int scale_mode, void* stream);
+
+/*
+ * Gradient of fp8bs_moe_combine: of the experts' outputs, in their segments and
+ * quantised for the products that read them, and of the gate weights.
+ *
+ *   row i = row_of[t][j]:  dy[i] = BF16_rne(w[t][j] dout[t]);  (q, s) = the 1x128
+ *     quantisation of dy;  dw[t][j] = sum_n dout[t][n] y[i][n]
+ *   rows with row_token[i] < 0: zeros (codes, scales and dy).
+ *   row_of[t][j] < 0 (or >= rows): no row; dw[t][j] = 0.
+ *
+ *   dout  [T][ldo] BF16.  y [rows][N] BF16, the experts' outputs (NULL with
+ *         dw NULL).  row_of [T][k], row_token [rows] int32 as
+ *         fp8bs_moe_layout gives them; w [T][k] float32.                (in)
+ *   dy    [rows][N] BF16 or NULL.  q, s [rows][N] E4M3 and [N/128][rows]
+ *         float32, both or neither.  dw [T][k] float32 or NULL.        (out)
+ * At least one of dy and q.  A row that several slots of its token name takes
+ * the sum of their weights.  A row that a token names and row_token gives to
+ * another records FP8BS_ERR_DEVICE_ARG and is passed over (dw 0).  Rows that
+ * row_token gives to a token that does not name them are left as they are.
+ * Rules: N % 8 == 0, with q N % 128 == 0; 1 <= k <= 64, T * k <= 2^24, rows <=
+ * 2^30; dout, y, dy, q 16-byte aligned, ldo * 2 % 16 == 0, the others 4.
+ */
+int fp8bs_moe_combine_backward(const void* dout, int64_t T, int64_t N, int64_t ldo, const void* y, int64_t rows,
+                               const int32_t* row_of, const int32_t* row_token, const float* w, int k, void* dy,
+                               uint8_t* q, float* s, int scale_mode, float* dw, void* stream);
+
+/*
+ * Gradient of the dispatch, which copied each token to the rows of its choices:
+ *   dx[t] = BF16_rne(add[t] + sum_j d[row_of[t][j]]),  the sum in float32, j
+ * ascending; row_of[t][j] < 0 (or >= rows) adds nothing.
+ *   d [rows][N] BF16; add [T][N] BF16 or NULL (it may be dx); dx [T][N] BF16.
+ * Rules as fp8bs_moe_combine.
+ */
+int fp8bs_moe_dispatch_backward(const void* d, int64_t rows, int64_t N, const int32_t* row_of, int64_t T, int k,
+                                const void* add, void* dx, void* stream);
+
+/*
+ * Gradient of the experts' weights (the grouped form of the Wgrad GEMM): with
+ * the rows [offsets[g], offsets[g+1]) of both operands expert g's,
+ *
+ *   D[g][n][k] (+)= sum_r A[r][n] B[r][k],
+ *
+ * A the gradients of the experts' outputs and B their inputs, both in 128x1
+ * groups with power-of-two scales (fp8bs_requant_1x128_to_128x1, or
+ * fp8bs_quantize_act_ex's transposed output), applied by the tensor core as in
+ * fp8bs_gemm_pow2, with the same rule for scales.
+ *
+ *   a_t  [N][R] E4M3, sa_t [R/128][N] float32.
+ *   b_t  [K][R] E4M3, sb_t [R/128][K] float32.                          (in)
+ *   offsets DEVICE int32 [num_groups + 1], as in fp8bs_grouped_gemm, at most R. (in)
+ *   d    [num_groups][N][K] FP32 or BF16.  accumulate: FP32 only; non-zero
+ *        adds to D.  An expert without rows gets zeros (or adds nothing). (out)
+ * Rows outside every segment are not read.  Rules: R, N, K % 128 == 0, R <= 2^30,
+ * 1 <= num_groups <= 512, num_groups * N < 2^31; a_t, b_t, sb_t, d 16-byte aligned.
+ */
+int fp8bs_grouped_wgrad_pow2(const uint8_t* a_t, const float* sa_t, const uint8_t* b_t, const float* sb_t, int64_t R,
+                             const int32_t* offsets, int num_groups, void* d, int d_dtype, int64_t N, int64_t K,
+                             int accumulate, void* stream);
+
 /*
  * Synchronises `stream`, then returns and clears the device status of the
  * current device: FP8BS_OK, FP8BS_ERR_TIMEOUT, FP8BS_ERR_DEVICE_ARG, or
