@@ -35,14 +35,17 @@
 //     warp touches tensor memory while the MMAs run), then per k-block four
 //     mxf8f6f4 MMAs of K = 32 into the tile's accumulator, the scale-factor
 //     id the k-block's byte in the slot;
-//   * warp 2: copies each k-block's float32 scales (128 rows of A, the
-//     tile's B scales) into a shared-memory scale ring with cp.async;
-//   * warp 3: converts the float32 scales of four k-blocks at a time to
-//     UE8M0 bytes in the shared-memory layout tcgen05.cp.32x128b.warpx4
-//     takes (32 rows of 16 bytes, row i landing in lane 32q + i of every
-//     lane quarter q, bytes 4c..4c+3 in column c); a scale that is neither
-//     zero nor a power of two in [2^-127, 2^127] records
-//     FP8BS_ERR_DEVICE_ARG;
+//   * warps 2 and 3: convert the float32 scales of four k-blocks at a time
+//     (every other scale slot each) to UE8M0 bytes in the shared-memory
+//     layout tcgen05.cp.32x128b.warpx4 takes (32 rows of 16 bytes, row i
+//     landing in lane 32q + i of every lane quarter q, bytes 4c..4c+3 in
+//     column c); a scale that is neither zero nor a power of two in
+//     [2^-127, 2^127] records FP8BS_ERR_DEVICE_ARG.  They read the scales
+//     straight into registers, a slot's 24 to 48 loads a lane in flight
+//     together: a ring of float32 scales in shared memory between a loading
+//     and a converting warp cost 24 KB of it and, with one scale per column,
+//     17% of the time (experts' weight gradients of 16 x 2048 rows, [4096][7168]:
+//     863 us, 717 with the conversion left out);
 //   * warps 4-11: the epilogue: after a tile's last MMA, read the
 //     accumulator out of TMEM (each thread one row, half of the columns),
 //     hand it back to the MMA, and store through shared memory with TMA.
@@ -65,7 +68,6 @@ __device__ int g_gemm_mx_status;
 constexpr int kMxThreads = 384;       // 12 warps
 constexpr int kMxEpiWarp0 = 4;        // warps 4..11: epilogue
 constexpr int kMxEpiThreads = 256;
-constexpr int kMxScaleChunks = 2;
 constexpr uint32_t kMxTmemCols = 512;
 constexpr int kSfSlotCols = 32;       // one scale slot: A scales at +0..3, B scales at +16..+16+BN/32
 constexpr int kSfbOffset = 16;
@@ -74,7 +76,7 @@ constexpr int kStepsPerSlot = 4;      // k-blocks per slot: one byte each
 // i, 32+i, 64+i, 96+i of the tile, four k-block bytes each), then B scales,
 // one 512-byte block per 128 columns (row i: columns i, 32+i, 64+i, 96+i).
 constexpr int kSfRowsBytes = 512;
-// Register split: warps 0-3 (producer, MMA, scale loader, converter) at
+// Register split: warps 0-3 (producer, MMA, converters) at
 // MxCfg::kRegsProducer, warps 4-11 at MxCfg::kRegsEpilogue (128
 // accumulators and the store); 4 x 32 x 72 + 8 x 32 x 216 or 4 x 32 x 88 +
 // 8 x 32 x 208 = 384 x 168, the CTA's allocation at launch.  The converter
@@ -105,15 +107,11 @@ struct MxCfg {
   static_assert(kSfSlots >= 4, "scale slots");
   static_assert(kSfbOffset + kSfbCols <= kSfSlotCols, "scale slot width");
   static constexpr int kSfSmemBytes = kSfRowsBytes * (1 + BN / 128);   // one shared-memory scale slot
-  static constexpr int kSlotFloats = kBlockM + (kRowScale ? BN : 4);
-  static constexpr int kScaleChunk = 8;
-  static constexpr int kScaleSlots = kScaleChunk * kMxScaleChunks;
   static constexpr int kColsPerThread = BN / 2;
   static constexpr int kOutBytes = (kMxEpiThreads / 32) * kMxOutSlots * kOutBoxBytes;
   static constexpr int kMaxStages = 6;
-  static constexpr int kNumBarsMax = 2 * kMaxStages + 2 * kMxScaleChunks + 2 * 8 + 2 * 2 + 1;
-  static constexpr int kFixedBytes = kOutBytes + kSfSlots * kSfSmemBytes + kScaleSlots * kSlotFloats * 4 +
-                                     kNumBarsMax * 8 + 16 + 2 * (kMaxGroups + 1) * 4 + 1024;
+  static constexpr int kNumBarsMax = 2 * kMaxStages + 2 * 8 + 2 * 2 + 1;
+  static constexpr int kFixedBytes = kOutBytes + kSfSlots * kSfSmemBytes + kNumBarsMax * 8 + 16 + 2 * (kMaxGroups + 1) * 4 + 1024;
   static constexpr int kFit = (kSmemBudget - kFixedBytes) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 3, "operand ring too shallow");
@@ -121,9 +119,8 @@ struct MxCfg {
   static constexpr int kOffB = kOffA + kStages * kABytes;
   static constexpr int kOffOut = kOffB + kStages * kBBytes;
   static constexpr int kOffSf = kOffOut + kOutBytes;                     // 1024-aligned
-  static constexpr int kOffScale = kOffSf + kSfSlots * kSfSmemBytes;
-  static constexpr int kOffBar = kOffScale + kScaleSlots * kSlotFloats * 4;
-  static constexpr int kNumBars = 2 * kStages + 2 * kMxScaleChunks + 2 * kSfSlots + 2 * kAccBufs + 1;
+  static constexpr int kOffBar = kOffSf + kSfSlots * kSfSmemBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * kSfSlots + 2 * kAccBufs + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffGroups = kOffMisc + 16;
   static constexpr int kSmemBytes = kOffGroups + 2 * (kMaxGroups + 1) * 4 + 1024;
@@ -199,6 +196,23 @@ __device__ __forceinline__ SegTile seg_tile(int t, int ntn, int tiles, const int
   return s;
 }
 
+// The bytes of four scales, the first in the low byte: the top bytes of the
+// doubled bit patterns, once a test of all four finds neither mantissa nor sign
+// bits nor an infinity; else (2^-127, or a scale to refuse) one by one.
+__device__ __forceinline__ uint32_t ue8m0_x4(const float (&s)[4], uint32_t& bad) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(s[i]);
+  uint32_t w = __byte_perm(__byte_perm(b[0] << 1, b[1] << 1, 0x0073), __byte_perm(b[2] << 1, b[3] << 1, 0x0073), 0x5410);
+  const uint32_t inf = ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;   // a byte of 255
+  if (((b[0] | b[1] | b[2] | b[3]) & 0x807FFFFFu) != 0u || inf != 0u) {
+    w = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= ue8m0_of(s[i], bad) << (8 * i);
+  }
+  return w;
+}
+
 // kSegK: the weight gradients of the experts.  A [M][K] and B [N][K] hold all
 // experts' rows along K (p.nkb blocks in all), group g those of its segment, and
 // D is [groups][M][N]; every role takes a tile's k-blocks from seg_tile.
@@ -211,14 +225,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + C::kOffA;
   uint8_t* sB = smem + C::kOffB;
-  float* sScale = reinterpret_cast<float*>(smem + C::kOffScale);
   uint8_t* sSf = smem + C::kOffSf;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* full = bars;                                // [kStages] TMA -> MMA
   uint64_t* empty = full + C::kStages;                  // [kStages] MMA -> TMA
-  uint64_t* sc_full = empty + C::kStages;               // [2] float scales landed in shared memory
-  uint64_t* sc_empty = sc_full + kMxScaleChunks;        // [2] converter done with them
-  uint64_t* sf_full = sc_empty + kMxScaleChunks;        // [kSfSlots] UE8M0 slot written to shared memory
+  uint64_t* sf_full = empty + C::kStages;               // [kSfSlots] UE8M0 slot written to shared memory
   uint64_t* sf_empty = sf_full + C::kSfSlots;           // [kSfSlots] copy and MMAs that read the slot done
   uint64_t* acc_full = sf_empty + C::kSfSlots;          // [kAccBufs] tile accumulated
   uint64_t* acc_empty = acc_full + C::kAccBufs;         // [kAccBufs] accumulator read out
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   int* s_off = reinterpret_cast<int*>(smem + C::kOffGroups);
   int* s_cum = s_off + (kMaxGroups + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform, and known to be
   const int lane = threadIdx.x & 31;
   const int ntn = (p.N + BN - 1) / BN;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
@@ -241,10 +252,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-    }
-    for (int s = 0; s < kMxScaleChunks; ++s) {
-      mbar_init(&sc_full[s], 32);                   // one cp.async arrival per loader lane
-      mbar_init(&sc_empty[s], 1);                   // the converter warp
     }
     for (int s = 0; s < C::kSfSlots; ++s) {
       mbar_init(&sf_full[s], kPair ? 2 : 1);        // the converters of both CTAs, on the leader (producer waits)
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   // set-up above overlaps that kernel's tail; operands, scales and D are
   // touched only after it has completed.
   griddep_wait();
-  const uint32_t tmem_base = misc[0];
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, misc[0], 0);
   const int total_tiles = static_cast<int>(misc[2]);
   volatile uint32_t* abort_flag = &misc[1];
   // tile of unit t, with its k-blocks; g carries the group of the previous unit in
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           } else if (kb % kStepsPerSlot == 0) {
             ++gs;
           }
-          if (lane == 0) {
+          if (elect_one()) {
             if (kPair) {
               if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::kABytes + C::kBBytes));
               const uint32_t leader_full = mapa_shared(&full[stage], 0);
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           // producer waited for them before loading the slot's first stage)
           if (!warp_wait(&full[stage], phase, p.timeout_ns)) { live = false; break; }
           tc_fence_after_sync();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t adesc = sw128_kmajor_desc(smem_u32(sA + stage * C::kABytes));
             const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sB + stage * C::kBBytes));
             const uint32_t sfa = tmem_base + C::kSfBase + ring * kSfSlotCols;
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         *abort_flag = 1;
       }
       // every MMA issued must have completed before TMEM is released
-      if (lane == 0) {
+      if (elect_one()) {
         if (kPair)
           mma_commit_pair(&teardown[0], 0x1);
         else
@@ -474,61 +481,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       }
       __syncwarp();
       (void)mbar_wait(&teardown[0], 0, p.timeout_ns);
-    } else if (warp == 2) {
-      // ----------------------------------------------------- scale loader
-      uint32_t step = 0;
-      bool live = true;
-      int g = 0;
-      for (int t = unit0; t < total_tiles && live; t += nunits) {
-        int row0, n0, kb0 = 0, nkb = p.nkb;
-        int64_t row_end;
-        coords(t, row0, n0, g, row_end, kb0, nkb);
-        for (int kb = 0; kb < nkb; ++kb, ++step) {
-          const uint32_t chunk = (step / C::kScaleChunk) % kMxScaleChunks;
-          if (step % C::kScaleChunk == 0 &&
-              !mbar_wait(&sc_empty[chunk], ((step / C::kScaleSlots) & 1u) ^ 1u, p.timeout_ns)) {
-            live = false;
-            break;
-          }
-          float* dst = sScale + (step % C::kScaleSlots) * C::kSlotFloats;
-          const float* sa_kb = p.sa + static_cast<int64_t>(kb0 + kb) * p.M;
-#pragma unroll
-          for (int i = 0; i < kBlockM / 32; ++i) {
-            const int64_t r = static_cast<int64_t>(row0) + lane + 32 * i;
-            if (r < p.M) cp_async_4(dst + lane + 32 * i, sa_kb + r);
-          }
-          if (kRowScale) {
-#pragma unroll
-            for (int i = 0; i < BN / 128; ++i) {
-              const int c = 4 * (lane + 32 * i);
-              if (n0 + c < p.N)
-                cp_async_16(dst + kBlockM + c, p.sb + static_cast<int64_t>(kb0 + kb) * p.N + n0 + c);
-            }
-          } else if (lane < BN / 128 && n0 + 128 * lane < p.N) {
-            const int64_t nb = static_cast<int64_t>(g) * nnb + n0 / 128 + lane;
-            cp_async_4(dst + kBlockM + lane, p.sb + nb * p.nkb + kb);
-          }
-          if (step % C::kScaleChunk == C::kScaleChunk - 1) cp_async_mbar_arrive(&sc_full[chunk]);
-        }
-      }
-      if (live && step % C::kScaleChunk != 0)   // the last chunk, not full
-        cp_async_mbar_arrive(&sc_full[(step / C::kScaleChunk) % kMxScaleChunks]);
-      if (!live) {
-        record_mx_status(kStatusTimeout);
-        *abort_flag = 1;
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 3) {
-      // -------------------------------------------------------- converter
+    } else if (warp >= 2) {
+      // ------------------------------------------------------- converters
       // Per scale slot (four k-blocks of a tile), lane i builds the rows i of
       // the slot's 512-byte blocks: A rows row0 + 32j + i (j = 0..3) and B
-      // columns n0 + 32c + i, one byte per k-block, reading the float32 scale
-      // ring kBatch k-blocks at a time (loads in flight together), and stores
-      // them with 16-byte writes.  Block-scaled B has one scale per 128
-      // columns, so a lane converts BN/128 B scales per k-block.
+      // columns n0 + 32c + i, one byte per k-block, and stores them with
+      // 16-byte writes.  Block-scaled B has one scale per 128 columns, so a
+      // lane converts BN/128 B scales per k-block.  Scales outside the rows
+      // and columns the tile writes are not read (their bytes are 127, 2^0).
       constexpr int kBVals = kRowScale ? C::kSfbCols : BN / 128;
-      constexpr int kBatch = kRowScale ? 2 : 4;
-      uint32_t step = 0;
+      const uint32_t mine = static_cast<uint32_t>(warp) & 1u;
       uint32_t gs = 0;
       uint32_t bad = 0;
       bool live = true;
@@ -538,72 +500,31 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         int64_t row_end;
         coords(t, row0, n0, g, row_end, kb0, nkb);
         const int nsl = (nkb + kStepsPerSlot - 1) / kStepsPerSlot;  // scale slots of the tile
-        // scales outside the rows and columns the tile writes are not read
-        // (their bytes are 127, 2^0) and not checked
-        uint32_t a_ok = 0, b_ok = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t r = static_cast<int64_t>(row0) + 32 * j + lane;
-          a_ok |= (r < row_end && r < p.M) ? 1u << j : 0u;
-        }
-#pragma unroll
-        for (int v = 0; v < kBVals; ++v)
-          b_ok |= (n0 + (kRowScale ? 32 * v + lane : 128 * v) < p.N) ? 1u << v : 0u;
-        for (int sl = 0; sl < nsl && live; ++sl, ++gs) {
+        const int64_t rows = min(row_end, p.M) - row0 - lane;       // of A, from this lane's first
+        const int cols = p.N - n0 - (kRowScale ? lane : 0);
+        for (int sl = 0; sl < nsl; ++sl, ++gs) {
+          if ((gs & 1u) != mine) continue;
           const int nsteps = min(kStepsPerSlot, nkb - sl * kStepsPerSlot);
-          uint32_t wa[4] = {0u, 0u, 0u, 0u};
-          uint32_t wb[kBVals];
+          float va[4][kStepsPerSlot], vb[kBVals][kStepsPerSlot];
 #pragma unroll
-          for (int v = 0; v < kBVals; ++v) wb[v] = 0u;
+          for (int b = 0; b < kStepsPerSlot; ++b) {
+            const int64_t kb = kb0 + sl * kStepsPerSlot + b;
+            const float* pa = p.sa + kb * p.M + row0 + lane;
 #pragma unroll
-          for (int b0 = 0; b0 < kStepsPerSlot; b0 += kBatch) {
-            float va[kBatch][4];
-            float vb[kBatch][kBVals];
+            for (int j = 0; j < 4; ++j) va[j][b] = b < nsteps && 32 * j < rows ? __ldg(pa + 32 * j) : 1.0f;
+            const float* pb = kRowScale ? p.sb + kb * p.N + n0 + lane
+                                        : p.sb + (static_cast<int64_t>(g) * nnb + n0 / 128) * p.nkb + kb;
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              if (b0 + b < nsteps) {
-                const uint32_t st = step + b0 + b;
-                const uint32_t chunk = (st / C::kScaleChunk) % kMxScaleChunks;
-                if (st % C::kScaleChunk == 0 &&
-                    !mbar_wait(&sc_full[chunk], (st / C::kScaleSlots) & 1u, p.timeout_ns))
-                  live = false;
-                const float* scs = sScale + (st % C::kScaleSlots) * C::kSlotFloats;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) va[b][j] = scs[32 * j + lane];
-#pragma unroll
-                for (int v = 0; v < kBVals; ++v) vb[b][v] = scs[kBlockM + (kRowScale ? 32 * v + lane : v)];
-              }
-            }
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              if (b0 + b < nsteps) {
-                const uint32_t sh = 8u * static_cast<uint32_t>(b0 + b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  uint32_t e_bad = 0;
-                  wa[j] |= ue8m0_of(va[b][j], e_bad) << sh;
-                  bad |= (a_ok >> j) & e_bad;
-                }
-#pragma unroll
-                for (int v = 0; v < kBVals; ++v) {
-                  uint32_t e_bad = 0;
-                  wb[v] |= ue8m0_of(vb[b][v], e_bad) << sh;
-                  bad |= (b_ok >> v) & e_bad;
-                }
-                const uint32_t st = step + b0 + b;
-                if (st % C::kScaleChunk == C::kScaleChunk - 1) {   // the chunk is read: hand it back
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(&sc_empty[(st / C::kScaleChunk) % kMxScaleChunks]);
-                }
-              }
-            }
+            for (int v = 0; v < kBVals; ++v)
+              vb[v][b] = b < nsteps && (kRowScale ? 32 : 128) * v < cols
+                             ? __ldg(pb + (kRowScale ? 32 * v : static_cast<int64_t>(v) * p.nkb))
+                             : 1.0f;
           }
-          if (!live) break;
-          step += nsteps;
+          uint32_t wa[4], wb[kBVals];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) wa[j] = (a_ok >> j) & 1u ? wa[j] : 0x7F7F7F7Fu;
+          for (int j = 0; j < 4; ++j) wa[j] = ue8m0_x4(va[j], bad);
 #pragma unroll
-          for (int v = 0; v < kBVals; ++v) wb[v] = (b_ok >> v) & 1u ? wb[v] : 0x7F7F7F7Fu;
+          for (int v = 0; v < kBVals; ++v) wb[v] = ue8m0_x4(vb[v], bad);
           const uint32_t ring = gs % C::kSfSlots;
           if (!warp_wait(&sf_empty[ring], ((gs / C::kSfSlots) & 1u) ^ 1u, p.timeout_ns)) {
             live = false;
