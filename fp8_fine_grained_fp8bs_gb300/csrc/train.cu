@@ -471,77 +471,127 @@ struct SwigluBackwardParams {
   const uint16_t* dv;
   const int32_t* live;   // or NULL
   int64_t M, I, ldh, lddv;
+  int rows;              // rows per CTA and step
   uint16_t* dh;          // [M][2I] or NULL
   uint8_t* q;            // or NULL (with s)
   float* s;
 };
 
+// Hardware base-2 exponential and reciprocal (one instruction each).
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// d silu(g) u / d (g, u) times dv.  With e = e^-|g| and c = 1 / (1 + e), sigma(g)
-// and sigma(-g) are c and e c in one order or the other, so neither overflows nor
-// cancels.  Below -64, where e runs out of float32's normal numbers in the end,
-// sigma(g) = e^g to within 2^-92 and e^g is applied as its root twice, once to the
-// larger factor, so that the product does not underflow on the way.
-__device__ __forceinline__ void swiglu_grad(float g, float u, float dv, float& dg, float& du) {
-  if (g < -64.0f) {
-    const float root = expf(0.5f * g);
-    const bool first = fabsf(dv) > fabsf(u);
-    du = dv * root * (g * root);
-    dg = (first ? dv : u) * root * (first ? u : dv) * root * (1.0f + g);
-    return;
-  }
-  const float e = expf(-fabsf(g));
-  const float c = rcp_approx(1.0f + e);
-  const float ec = e * c;
-  const float sig = g >= 0.0f ? c : ec, other = g >= 0.0f ? ec : c;
-  du = dv * (g * sig);
-  dg = dv * u * (sig * fmaf(g, other, 1.0f));
+// Gradients dg, du of silu(g) u times dv for two pairs, in packed float32, for
+// gates from -64 up.  With e = e^-g: sigma(g) = 1 / (1 + e), sigma(-g) = e sigma(g);
+// neither cancels.  log2 e is taken in two parts: a BF16 gate times the first
+// (15 bits) is exact, so the exponential's argument has no rounding, and the
+// second enters as a factor 1 - g (log2 e - kHi) ln 2.
+__device__ __forceinline__ void swiglu_grad2(uint32_t gw, uint32_t uw, uint32_t vw, uint32_t& dgw, uint32_t& duw) {
+  constexpr float kHi = 1.44268798828125f;        // 23637 / 16384
+  constexpr float kLo = 4.8884955e-06f;           // (log2 e - kHi) ln 2
+  const float2 one = make_float2(1.0f, 1.0f);
+  const float2 g = make_float2(__uint_as_float(gw << 16), __uint_as_float(gw & 0xFFFF0000u));
+  const float2 u = make_float2(__uint_as_float(uw << 16), __uint_as_float(uw & 0xFFFF0000u));
+  const float2 v = make_float2(__uint_as_float(vw << 16), __uint_as_float(vw & 0xFFFF0000u));
+  const float2 t = __fmul2_rn(g, make_float2(-kHi, -kHi));
+  const float2 e = __fmul2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), __ffma2_rn(g, make_float2(-kLo, -kLo), one));
+  const float2 d = __fadd2_rn(e, one);
+  const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 du = __fmul2_rn(v, __fmul2_rn(g, s));
+  const float2 f = __fmul2_rn(s, __ffma2_rn(g, __fmul2_rn(e, s), one));
+  const float2 dg = __fmul2_rn(__fmul2_rn(v, u), f);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(dg.x, dg.y), b = __floats2bfloat162_rn(du.x, du.y);
+  dgw = *reinterpret_cast<const uint32_t*>(&a);
+  duw = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-constexpr int kSbThreads = 256;
-
-template <bool kPow2>
-__global__ void __launch_bounds__(kSbThreads) swiglu_backward_kernel(const SwigluBackwardParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t upr = p.I / 8;                        // pieces of 8 columns a row, a multiple of 16
-  const int64_t units = p.M * upr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kSbThreads;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * kSbThreads + threadIdx.x - lane; u0 < units; u0 += step) {
-    const int64_t unit = u0 + lane;
-    const bool here = unit < units;
-    const int64_t row = here ? unit / upr : 0;
-    const int64_t c = here ? unit - row * upr : 0;
-    float dg[8], du[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dg[e] = du[e] = 0.0f;
-    if (here && (p.live == nullptr || p.live[row] >= 0)) {
-      const uint16_t* hr = p.h + row * p.ldh + 8 * c;
-      const uint4 gw = __ldg(reinterpret_cast<const uint4*>(hr)), uw = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
-      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(p.dv + row * p.lddv + 8 * c));
-      float g[8], u[8], v[8];
-      widen8(gw, g);
-      widen8(uw, u);
-      widen8(vw, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], v[e], dg[e], du[e]);
+// The gradients of the gates below -64 among eight, where e^-g runs out of
+// float32's range in the end: sigma(g) = e^g to within 2^-92, applied as its root
+// twice, once to the larger factor, so that the product does not underflow on the
+// way.  Runs only for eights that hold such a gate; kept out of line.
+constexpr uint32_t kFarGate = 0xC280u;   // BF16 of -64; patterns above it are below -64
+__device__ __noinline__ void swiglu_grad8_far(const uint4 g, const uint4 u, const uint4 v, uint4* dg, uint4* du) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+  uint32_t* out[2] = {reinterpret_cast<uint32_t*>(dg), reinterpret_cast<uint32_t*>(du)};
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t sh = (i & 1) * 16;
+    const uint32_t gb = (gw[i >> 1] >> sh) & 0xFFFFu;
+    if (gb <= kFarGate) continue;
+    const float gate = __uint_as_float(gb << 16);
+    const float up = __uint_as_float(((uw[i >> 1] >> sh) & 0xFFFFu) << 16);
+    const float dv = __uint_as_float(((vw[i >> 1] >> sh) & 0xFFFFu) << 16);
+    const float root = expf(0.5f * gate);
+    const bool first = fabsf(dv) > fabsf(up);
+    const float r[2] = {(first ? dv : up) * root * (first ? up : dv) * root * (1.0f + gate), dv * root * (gate * root)};
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t rb = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(r[k])));
+      out[k][i >> 1] = (out[k][i >> 1] & ~(0xFFFFu << sh)) | (rb << sh);
     }
+  }
+}
+
+constexpr int kSbThreads = 256;   // or as many as a row has pieces, up to 512
+
+// Thread = eight columns of one half of h: the columns stay, the rows advance by
+// the grid, with the next row's loads in flight.  A group of 128 is a half-warp's
+// 16 threads; whole warps go through the loop together.
+template <bool kPow2>
+__global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwardParams p) {
+  griddep_launch_dependents();
+  const int upr = static_cast<int>(p.I / 8);          // pieces a row, a multiple of 16
+  const bool whole = upr * p.rows <= static_cast<int>(blockDim.x);
+  const int sub = whole ? threadIdx.x / upr : 0;
+  const int step_c = whole ? upr : blockDim.x;        // rows longer than a CTA: in steps
+  const int c0 = threadIdx.x - sub * upr;
+  const int64_t rstep = static_cast<int64_t>(gridDim.x) * p.rows;
+  const bool mine = sub < p.rows;
+  griddep_wait();
+  auto is_live = [&](int64_t row) { return mine && row < p.M && (p.live == nullptr || __ldg(p.live + row) >= 0); };
+  auto load = [&](int64_t row, int c, bool live, uint4 (&w)[3]) {
+    w[0] = w[1] = w[2] = make_uint4(0u, 0u, 0u, 0u);
+    if (!live || c >= upr) return;
+    const uint16_t* hr = p.h + row * p.ldh + 8 * c;
+    w[0] = __ldg(reinterpret_cast<const uint4*>(hr));
+    w[1] = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
+    w[2] = __ldg(reinterpret_cast<const uint4*>(p.dv + row * p.lddv + 8 * c));
+  };
+  for (int cc = 0; cc < upr; cc += step_c) {
+    const int c = c0 + cc;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * p.rows + sub;
+    uint4 next[3];
+    load(row, c, is_live(row), next);
+    bool live_after = is_live(row + rstep);            // a row ahead of the loads that wait for it
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.rows; first < p.M; first += rstep, row += rstep) {
+      const uint4 g = next[0], u = next[1], v = next[2];
+      load(row + rstep, c, live_after, next);
+      live_after = is_live(row + 2 * rstep);
+      const bool here = mine && row < p.M && c < upr;
+      uint4 d[2];
+      swiglu_grad2(g.x, u.x, v.x, d[0].x, d[1].x);
+      swiglu_grad2(g.y, u.y, v.y, d[0].y, d[1].y);
+      swiglu_grad2(g.z, u.z, v.z, d[0].z, d[1].z);
+      swiglu_grad2(g.w, u.w, v.w, d[0].w, d[1].w);
+      const uint32_t far = __vmaxu2(__vmaxu2(g.x, g.y), __vmaxu2(g.z, g.w));
+      if ((far >> 16) > kFarGate || (far & 0xFFFFu) > kFarGate) swiglu_grad8_far(g, u, v, &d[0], &d[1]);
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const uint4 d = round8(part == 0 ? dg : du);
-      const int64_t col = part * p.I + 8 * c;
-      if (here && p.dh != nullptr) *reinterpret_cast<uint4*>(p.dh + row * 2 * p.I + col) = d;
-      if (p.q != nullptr) {
-        const Divisor dv = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(d)) & 0xFFFFu));
-        if (here) {
-          *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = quant8<kPow2>(d, dv);
-          if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = dv.s;
+      for (int part = 0; part < 2; ++part) {
+        const int64_t col = part * p.I + 8 * c;
+        if (here && p.dh != nullptr) *reinterpret_cast<uint4*>(p.dh + row * 2 * p.I + col) = d[part];
+        if (p.q != nullptr) {
+          const Divisor dv = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(d[part])) & 0xFFFFu));
+          if (here) {
+            *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = quant8<kPow2>(d[part], dv);
+            if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = dv.s;
+          }
         }
       }
     }
@@ -632,13 +682,17 @@ cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cu
   SwigluBackwardParams p;
   p.h = a.h; p.dv = a.dv; p.live = a.live; p.M = a.M; p.I = a.I; p.ldh = a.ldh; p.lddv = a.lddv;
   p.dh = a.dh; p.q = a.q; p.s = a.s;
+  const int upr = static_cast<int>(a.I / 8);
+  // short rows share a CTA; longer ones take one of their own size, above 512 pieces 256 threads in steps
+  p.rows = std::max(1, kSbThreads / upr);
+  const int threads = upr > 512 ? kSbThreads : (p.rows * upr + 31) / 32 * 32;
   auto kern = a.pow2 ? swiglu_backward_kernel<true> : swiglu_backward_kernel<false>;
-  static std::atomic<int> cache[2][kMaxCachedDevices];
+  static std::atomic<int> cache[2][17][kMaxCachedDevices];
   int64_t slots = 0;
-  const cudaError_t e = resident_ctas(kern, kSbThreads, sm_count, cache[a.pow2 ? 1 : 0], &slots);
+  const cudaError_t e = resident_ctas(kern, threads, sm_count, cache[a.pow2 ? 1 : 0][threads / 32], &slots);
   if (e != cudaSuccess) return e;
-  const int64_t need = (p.M * (p.I / 8) + kSbThreads - 1) / kSbThreads;
-  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), kSbThreads, stream, p);
+  const int64_t need = (p.M + p.rows - 1) / p.rows;
+  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), threads, stream, p);
 }
 
 cudaError_t train_take_status(int* status) {
