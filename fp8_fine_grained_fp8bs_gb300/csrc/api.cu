@@ -612,7 +612,7 @@ int fp8bs_rmsnorm_backward(const void* dy, int64_t M, int64_t K, int64_t lddy, c
   a.dy = static_cast<const uint16_t*>(dy); a.r = static_cast<const uint16_t*>(r); a.gain = gain;
   a.gain_f32 = gain_dtype == FP8BS_IN_F32; a.rstd = rstd; a.dres = static_cast<const uint16_t*>(dres);
   a.M = M; a.K = K; a.lddy = lddy; a.ldr = ldr; a.lddres = lddres; a.dx = static_cast<uint16_t*>(dx);
-  a.dgain = dgain; a.accumulate = accumulate != 0;
+  a.dgain = dgain; a.accumulate = accumulate != 0; a.timeout_ns = g_timeout_ns.load();
   return from_cuda(fp8bs::launch_rmsnorm_backward(a, ws, static_cast<cudaStream_t>(stream)));
 }
 

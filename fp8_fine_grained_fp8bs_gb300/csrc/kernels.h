@@ -173,7 +173,8 @@ cudaError_t launch_moe_combine(const uint16_t* y, int64_t rows_y, int64_t N, con
 cudaError_t launch_moe_dispatch_backward(const uint16_t* d, int64_t rows, int64_t N, const int32_t* idx, int64_t T, int k,
                                          const uint16_t* add, uint16_t* out, int sm_count, cudaStream_t stream);
 
-// ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; no waits)
+// ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; the
+// norm's gradient waits for its own copies, bounded by timeout_ns)
 struct NormArgs {
   const uint16_t* x;       // [M][ldx]
   const uint16_t* res;     // [M][ldr] or NULL
@@ -202,6 +203,7 @@ struct NormBackwardArgs {
   uint16_t* dx;            // [M][K]
   float* dgain;            // [K] or NULL
   bool accumulate;
+  uint64_t timeout_ns;
 };
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
 cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& args, void* ws, cudaStream_t stream);
@@ -234,7 +236,8 @@ struct SwigluBackwardArgs {
   float* s;                // [2I/128][M]
 };
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& args, int sm_count, cudaStream_t stream);
-// Reads and clears the status word (a row_token that does not fit row_of).
+// Reads and clears the status word (a wait that ran out, a row_token that does not
+// fit row_of).
 cudaError_t train_take_status(int* status);
 
 // Diagnostic: a kernel whose bounded wait runs out (nothing ever arrives on

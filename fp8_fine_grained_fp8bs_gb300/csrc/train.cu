@@ -222,89 +222,181 @@ struct NormBackwardParams {
   const float* rstd;
   const uint16_t* dres;  // or NULL
   int64_t M, lddy, ldr, lddres;
-  int K, warps;
+  int K, warps, stages;
   uint16_t* dx;
-  float* part;           // [parts][K], or NULL: no gain gradient
+  float* part;           // [CTAs][K], or NULL: no gain gradient
+  uint64_t timeout_ns;
 };
 
-constexpr int kNormParts = 304;   // CTAs: two on each of the 152 SMs
+constexpr int kRingMaxStages = 4;
+constexpr int kRingBytes = 112 * 1024;       // of a CTA, two to an SM
+constexpr int kRingMaxBytes = 224 * 1024;    // of a CTA that has an SM for itself
+
+// Eight values in packed pairs.
+__device__ __forceinline__ void widen8x2(const uint4& v, float2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 round8x2(const float2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool kF32>
+__device__ __forceinline__ void load_gain2(const void* gain, int c, float2 (&f)[4]) {
+  float v[8];
+  load_gain<kF32>(gain, c, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
 
 // With t = dy gain: dx = rstd t - r rstd^3 mean(t r) + dres.  dy r is exact in
-// float32 and serves the mean and the gain's sum.
+// float32 and serves the mean and the gain's sum, which stays in the thread's
+// registers over the CTA's rows.  The rows (dy, r and dres) come by bulk copies
+// into a ring of stages that the next rows fill while one is worked on; both
+// passes over a row read it from there.
 template <int kVecs, bool kGainF32>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const NormBackwardParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float s_part[2][kNormMaxThreads / 32];
-  griddep_launch_dependents();
+  __shared__ uint64_t full[kRingMaxStages];
   const int T = 32 * p.warps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
   const int rows = blockDim.x / T;
   const int nv = p.K / 8;
-  int parity = 0;
-  float acc[kVecs][8];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+  const int arrays = p.dres != nullptr ? 3 : 2;
+  const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.K);
+  const uint32_t stage_bytes = arrays * rows * row_bytes;
+  const int64_t rstep = static_cast<int64_t>(gridDim.x) * rows;
+  const int64_t row_first = static_cast<int64_t>(blockIdx.x) * rows;
+  const int steps = static_cast<int>((p.M - row_first + rstep - 1) / rstep);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
   griddep_wait();
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows; row0 < p.M; row0 += static_cast<int64_t>(gridDim.x) * rows) {
-    const int64_t row = row0 + sub;
+  // one lane per row and array copies it
+  auto issue = [&](int step) {
+    if (warp != 0 || step >= steps) return;
+    const int s = step % p.stages;
+    const int64_t row0 = row_first + step * rstep;
+    const int n = static_cast<int>(min(static_cast<int64_t>(rows), p.M - row0));
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], arrays * n * row_bytes);
+    __syncwarp();
+    if (lane < arrays * n) {
+      const int which = lane / n, i = lane - which * n;
+      const uint16_t* src = which == 0   ? p.dy + (row0 + i) * p.lddy
+                            : which == 1 ? p.r + (row0 + i) * p.ldr
+                                         : p.dres + (row0 + i) * p.lddres;
+      bulk_load(ring + s * stage_bytes + (which * rows + i) * row_bytes, src, row_bytes, &full[s]);
+    }
+    __syncwarp();
+  };
+  for (int s = 0; s < p.stages; ++s) issue(s);
+  float2 acc[kVecs][4], gain[kVecs][4];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = i * T + t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = gain[i][e] = make_float2(0.0f, 0.0f);
+    if (c < nv) load_gain2<kGainF32>(p.gain, 8 * c, gain[i]);
+  }
+  auto rstd_of = [&](int step) {
+    const int64_t row = row_first + step * rstep + sub;
+    return step < steps && row < p.M ? __ldg(p.rstd + row) : 0.0f;
+  };
+  float rstd_next = rstd_of(0);
+  int waited = 0;
+  for (int step = 0; step < steps; ++step) {
+    const int s = step % p.stages;
+    const int64_t row = row_first + step * rstep + sub;
     const bool live = row < p.M;
-    uint4 d[kVecs], r[kVecs];
+    const float rstd = rstd_next;
+    rstd_next = rstd_of(step + 1);
+    const bool ok = mbar_wait(&full[s], (step / p.stages) & 1, p.timeout_ns);
+    const uint8_t* stage = ring + s * stage_bytes + sub * row_bytes;
+    float2 sum = make_float2(0.0f, 0.0f);
+    const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int c = i * T + t;
-      d[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && c < nv) {
-        d[i] = *reinterpret_cast<const uint4*>(p.dy + row * p.lddy + 8 * c);
-        r[i] = *reinterpret_cast<const uint4*>(p.r + row * p.ldr + 8 * c);
+      if (!(ok && live && c < nv)) continue;
+      float2 a[4], b[4];
+      widen8x2(*reinterpret_cast<const uint4*>(stage + 16 * c), a);
+      widen8x2(*reinterpret_cast<const uint4*>(stage + rows * row_bytes + 16 * c), b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 ab = __fmul2_rn(a[e], b[e]);
+        sum = __ffma2_rn(ab, gain[i][e], sum);
+        acc[i][e] = __ffma2_rn(ab, rstd2, acc[i][e]);
       }
     }
-    const float rstd = live ? p.rstd[row] : 0.0f;
-    float sum = 0.0f;
+    const float lanes = warp_sum(sum.x + sum.y);
+    const int parity = step & 1;
+    if (lane == 0) s_part[parity][warp] = lanes;
+    if (!__syncthreads_and(ok)) {
+      if (threadIdx.x == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
+      break;
+    }
+    ++waited;
+    if (step > 0) issue(step - 1 + p.stages);   // every thread is done with the stage before
+    float total = s_part[parity][sub * p.warps];
+    for (int i = 1; i < p.warps; ++i) total += s_part[parity][sub * p.warps + i];
+    const float f = -(rstd * rstd * (rstd * (total / static_cast<float>(p.K))));
+    const float2 f2 = make_float2(f, f);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int c = i * T + t;
       if (!(live && c < nv)) continue;
-      float a[8], b[8], g[8];
-      widen8(d[i], a);
-      widen8(r[i], b);
-      load_gain<kGainF32>(p.gain, 8 * c, g);
+      float2 a[4], b[4];
+      widen8x2(*reinterpret_cast<const uint4*>(stage + 16 * c), a);
+      widen8x2(*reinterpret_cast<const uint4*>(stage + rows * row_bytes + 16 * c), b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ab = a[e] * b[e];
-        sum = fmaf(ab, g[e], sum);
-        acc[i][e] = fmaf(ab, rstd, acc[i][e]);
+      for (int e = 0; e < 4; ++e) a[e] = __ffma2_rn(b[e], f2, __fmul2_rn(__fmul2_rn(a[e], gain[i][e]), rstd2));
+      if (arrays == 3) {
+        widen8x2(*reinterpret_cast<const uint4*>(stage + 2 * rows * row_bytes + 16 * c), b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
       }
-    }
-    sum = row_sum(sum, p.warps, s_part, parity);
-    const float f = rstd * rstd * (rstd * (sum / static_cast<float>(p.K)));
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = i * T + t;
-      if (!(live && c < nv)) continue;
-      float a[8], b[8], g[8];
-      widen8(d[i], a);
-      widen8(r[i], b);
-      load_gain<kGainF32>(p.gain, 8 * c, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = fmaf(-b[e], f, a[e] * g[e] * rstd);
-      if (p.dres != nullptr) {
-        widen8(*reinterpret_cast<const uint4*>(p.dres + row * p.lddres + 8 * c), b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += b[e];
-      }
-      *reinterpret_cast<uint4*>(p.dx + row * p.K + 8 * c) = round8(a);
+      *reinterpret_cast<uint4*>(p.dx + row * p.K + 8 * c) = round8x2(a);
     }
   }
+  if (waited < steps) {   // a wait ran out: what was issued lands before the CTA may leave
+    if (warp == 0)
+      for (int step = waited; step < min(steps, max(waited - 1, 0) + p.stages); ++step)
+        (void)mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
+    return;
+  }
   if (p.part == nullptr) return;
-  float* out = p.part + (static_cast<int64_t>(blockIdx.x) * rows + sub) * p.K;
+  // the CTA's sum over its rows' threads, through the ring where rows share the CTA
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.K;
+  float* scratch = reinterpret_cast<float*>(ring);
+  if (rows > 1) {
+    __syncthreads();
+    out = scratch + sub * p.K;
+  }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = i * T + t;
     if (c >= nv) continue;
     float4* o = reinterpret_cast<float4*>(out + 8 * c);
-    o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    o[0] = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+    o[1] = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+  }
+  if (rows == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
+    float sum = scratch[c];
+    for (int i = 1; i < rows; ++i) sum += scratch[i * p.K + c];
+    p.part[static_cast<int64_t>(blockIdx.x) * p.K + c] = sum;
   }
 }
 
@@ -627,7 +719,32 @@ cudaError_t run_norm_kind(const NormParams& p, const RowPlace& at, bool gain_f32
   return pow2 ? run_norm<kVecs, false, true>(p, at, sm_count, stream) : run_norm<kVecs, false, false>(p, at, sm_count, stream);
 }
 
-int norm_grid(int64_t M, int rows) { return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, kNormParts)); }
+// Ring and grid of the gradient: two CTAs an SM where two stages of half an SM's
+// shared memory hold the rows, else one.  The grid goes by the sizes alone (152
+// SMs), so that the parts, and the bits of their sum, do too.
+struct NormBackwardPlan {
+  RowPlace at;
+  int stages, stage_bytes, grid;
+};
+NormBackwardPlan plan_norm_backward(int64_t M, int64_t K, bool dres) {
+  NormBackwardPlan n;
+  n.at = place_rows(static_cast<int>(K));
+  n.stage_bytes = static_cast<int>((dres ? 3 : 2) * n.at.rows * K * 2);
+  const bool two = 12 * n.at.rows * K <= kRingBytes;   // two stages of three arrays, with or without dres
+  n.stages = std::min(kRingMaxStages, (two ? kRingBytes : kRingMaxBytes) / n.stage_bytes);
+  n.grid = static_cast<int>(std::min<int64_t>((M + n.at.rows - 1) / n.at.rows, two ? 304 : 152));
+  return n;
+}
+
+template <int kVecs, bool kGainF32>
+cudaError_t run_norm_backward(const NormBackwardParams& p, const NormBackwardPlan& n, cudaStream_t stream) {
+  auto kern = norm_backward_kernel<kVecs, kGainF32>;
+  const int smem = n.stages * n.stage_bytes;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
+  if (e != cudaSuccess) return e;
+  return launch_behind_smem(kern, dim3(static_cast<unsigned>(n.grid)), static_cast<unsigned>(32 * n.at.warps * n.at.rows),
+                            static_cast<size_t>(smem), stream, p);
+}
 
 }  // namespace
 
@@ -644,25 +761,22 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream)
 int64_t rmsnorm_max_columns() { return kMaxNormK; }
 
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
-  if (M == 0 || K == 0) return 0;
-  const RowPlace at = place_rows(static_cast<int>(K));
-  return 4 * K * norm_grid(M, at.rows) * at.rows;
+  return M == 0 || K == 0 ? 0 : 4 * K * plan_norm_backward(M, K, true).grid;
 }
 
 cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, void* ws, cudaStream_t stream) {
-  const RowPlace at = place_rows(static_cast<int>(a.K));
-  const int grid = norm_grid(a.M, at.rows), threads = 32 * at.warps * at.rows;
+  const NormBackwardPlan n = plan_norm_backward(a.M, a.K, a.dres != nullptr);
   NormBackwardParams p;
   p.dy = a.dy; p.r = a.r; p.gain = a.gain; p.rstd = a.rstd; p.dres = a.dres; p.M = a.M; p.lddy = a.lddy; p.ldr = a.ldr;
-  p.lddres = a.lddres; p.K = static_cast<int>(a.K); p.warps = at.warps; p.dx = a.dx;
+  p.lddres = a.lddres; p.K = static_cast<int>(a.K); p.warps = n.at.warps; p.stages = n.stages; p.dx = a.dx;
   p.part = a.dgain != nullptr ? static_cast<float*>(ws) : nullptr;
-  auto kern = at.vecs == 4   ? (a.gain_f32 ? norm_backward_kernel<4, true> : norm_backward_kernel<4, false>)
-              : at.vecs == 2 ? (a.gain_f32 ? norm_backward_kernel<2, true> : norm_backward_kernel<2, false>)
-                             : (a.gain_f32 ? norm_backward_kernel<1, true> : norm_backward_kernel<1, false>);
-  const cudaError_t e = launch_behind(kern, dim3(grid), threads, stream, p);
+  p.timeout_ns = a.timeout_ns;
+  const cudaError_t e = n.at.vecs == 4   ? (a.gain_f32 ? run_norm_backward<4, true>(p, n, stream) : run_norm_backward<4, false>(p, n, stream))
+                        : n.at.vecs == 2 ? (a.gain_f32 ? run_norm_backward<2, true>(p, n, stream) : run_norm_backward<2, false>(p, n, stream))
+                                         : (a.gain_f32 ? run_norm_backward<1, true>(p, n, stream) : run_norm_backward<1, false>(p, n, stream));
   if (e != cudaSuccess || a.dgain == nullptr) return e;
   return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), 256, stream,
-                       static_cast<const float*>(p.part), grid * at.rows, p.K, a.dgain, a.accumulate ? 1 : 0);
+                       static_cast<const float*>(p.part), n.grid, p.K, a.dgain, a.accumulate ? 1 : 0);
 }
 
 cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int sm_count, cudaStream_t stream) {
