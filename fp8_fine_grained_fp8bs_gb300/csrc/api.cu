@@ -577,7 +577,7 @@ int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, con
   a.x = static_cast<const uint16_t*>(x); a.res = static_cast<const uint16_t*>(residual); a.gain = gain;
   a.gain_f32 = gain_dtype == FP8BS_IN_F32; a.M = M; a.K = K; a.ldx = ldx; a.ldr = ldr; a.eps = eps;
   a.pow2 = scale_mode == FP8BS_SCALE_POW2; a.r = static_cast<uint16_t*>(r); a.y = static_cast<uint16_t*>(y);
-  a.q = q; a.s = s; a.rstd = rstd;
+  a.q = q; a.s = s; a.rstd = rstd; a.timeout_ns = g_timeout_ns.load();
   return from_cuda(fp8bs::launch_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -174,7 +174,7 @@ cudaError_t launch_moe_dispatch_backward(const uint16_t* d, int64_t rows, int64_
                                          const uint16_t* add, uint16_t* out, int sm_count, cudaStream_t stream);
 
 // ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; the
-// norm's gradient waits for its own copies, bounded by timeout_ns)
+// norm and its gradient wait for their own copies, bounded by timeout_ns)
 struct NormArgs {
   const uint16_t* x;       // [M][ldx]
   const uint16_t* res;     // [M][ldr] or NULL
@@ -188,6 +188,7 @@ struct NormArgs {
   uint8_t* q;              // [M][K] or NULL
   float* s;                // [K/128][M]
   float* rstd;             // [M] or NULL
+  uint64_t timeout_ns;
 };
 cudaError_t launch_rmsnorm(const NormArgs& args, int sm_count, cudaStream_t stream);
 int64_t rmsnorm_max_columns();

@@ -42,39 +42,44 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight gains from column c on.
-template <bool kF32>
-__device__ __forceinline__ void load_gain(const void* gain, int c, float (&f)[8]) {
-  if (kF32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gain) + c);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gain) + c)), f);
-  }
-}
-
+// Table of absmax divisors, for kernels whose CTAs quantise many groups.
 template <bool kPow2>
-__device__ __forceinline__ Divisor divisor_of(uint32_t a16) {
-  return kPow2 ? pow2_divisor_bits(a16) : make_divisor(__uint_as_float(a16 << 16));
-}
+struct Divisors {
+  DivTable table;
+  __device__ __forceinline__ void init() { div_table_init(table); }   // a barrier follows before use
+  __device__ __forceinline__ Divisor of(uint32_t a16) const { return table_divisor(table, a16); }
+};
+template <>
+struct Divisors<true> {
+  __device__ __forceinline__ void init() {}
+  __device__ __forceinline__ Divisor of(uint32_t a16) const { return pow2_divisor_bits(a16); }
+};
 
-// Eight values of a group -> eight codes.  A power-of-two divisor's quotient is
-// one exact product, which keeps the sign of a zero.
+// Eight BF16 values of a group with maximum a16 (BF16 bits) -> eight codes; the
+// scale.  A power of two: with e the biased exponent of the smallest power of two
+// times 1.75 that is at least the maximum (31 carries where the 7 bits of its
+// fraction exceed 96, those of 1.75), s = 2^(e - 135).  The quotient is then one
+// exact product, which keeps the sign of a zero.  Groups whose scale or its
+// reciprocal is not a normal number, zeros among them, take the general way.
 template <bool kPow2>
-__device__ __forceinline__ uint2 quant8(const uint4& v, const Divisor& d) {
-  if (!kPow2 || !d.fast) return quant8m(v, d);
-  float f[8];
-  widen8(v, f);
-  const float2 y2 = make_float2(d.y, d.y);
+__device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
+  if (kPow2) {
+    const uint32_t e = (a16 + 31u) >> 7;
+    if (e >= 9u) {
+      const float y = __uint_as_float((262u - e) << 23);
+      const float2 y2 = make_float2(y, y);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float2 f[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 r = __fmul2_rn(make_float2(f[2 * i], f[2 * i + 1]), y2);
-    f[2 * i] = r.x;
-    f[2 * i + 1] = r.y;
+      for (int i = 0; i < 4; ++i)
+        f[i] = __fmul2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), y2);
+      codes = make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
+      return __uint_as_float((e - 8u) << 23);
+    }
   }
-  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+  const Divisor d = divisors.of(a16);
+  codes = quant8m(v, d);
+  return d.s;
 }
 
 // |x| maximum (BF16 bits) over the 16 lanes of each half-warp; every lane of the warp takes part.
@@ -90,6 +95,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Sum of up to 16 warps' values, by every thread, in a fixed order.
+__device__ __forceinline__ float sum_of_warps(const float* part, int warps) {
+  const int lane = threadIdx.x & 31;
+  float v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // A row is held by `warps` warps, kVecs 16-byte pieces a thread; short rows
 // share a CTA.  Sums of a row: lanes, then warps, in a fixed order.
 constexpr int kNormMaxThreads = 512;
@@ -100,134 +114,17 @@ struct RowPlace {
   int rows;    // rows per CTA
   int vecs;    // pieces per thread
 };
-inline RowPlace place_rows(int K) {
+inline RowPlace place_rows(int K, int four_from) {   // four pieces a thread from that many pieces a row on
   RowPlace p;
   const int nv = (K + 7) / 8;
-  p.vecs = nv > 256 ? 4 : nv > 64 ? 2 : 1;
+  p.vecs = nv > four_from ? 4 : nv > 64 ? 2 : 1;
   p.warps = (nv + 32 * p.vecs - 1) / (32 * p.vecs);
   p.rows = std::max(1, 8 / p.warps);
   return p;
 }
 
-// Sum over the row's warps; s_part: one float per warp of the CTA, alternating
-// between two sets so that one barrier per row is enough.
-__device__ __forceinline__ float row_sum(float v, int warps, float (*s_part)[kNormMaxThreads / 32], int& parity) {
-  v = warp_sum(v);
-  if (warps == 1) return v;
-  const int warp = threadIdx.x >> 5, first = warp / warps * warps;
-  if ((threadIdx.x & 31) == 0) s_part[parity][warp] = v;
-  __syncthreads();
-  float sum = s_part[parity][first];
-  for (int i = 1; i < warps; ++i) sum += s_part[parity][first + i];
-  parity ^= 1;
-  return sum;
-}
-
-// ------------------------------------------------------------------- norm
-struct NormParams {
-  const uint16_t* x;
-  const uint16_t* res;   // or NULL
-  const void* gain;
-  int64_t M, ldx, ldr;
-  int K, warps;
-  float eps;
-  uint16_t* r;           // or NULL
-  uint16_t* y;           // or NULL
-  uint8_t* q;            // or NULL (with s)
-  float* s;
-  float* rstd;           // or NULL
-};
-
-template <int kVecs, bool kGainF32, bool kPow2>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams p) {
-  __shared__ float s_part[2][kNormMaxThreads / 32];
-  griddep_launch_dependents();
-  const int T = 32 * p.warps;
-  const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
-  const int rows = blockDim.x / T;
-  const int nv = p.K / 8;
-  int parity = 0;
-  griddep_wait();
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows; row0 < p.M; row0 += static_cast<int64_t>(gridDim.x) * rows) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.M;
-    uint4 v[kVecs];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = i * T + t;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && c < nv) v[i] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + 8 * c);
-    }
-    if (p.res != nullptr) {
-      uint4 w[kVecs];
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int c = i * T + t;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && c < nv) w[i] = *reinterpret_cast<const uint4*>(p.res + row * p.ldr + 8 * c);
-      }
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        float a[8], b[8];
-        widen8(v[i], a);
-        widen8(w[i], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += b[e];
-        v[i] = round8(a);
-        const int c = i * T + t;
-        if (live && c < nv) *reinterpret_cast<uint4*>(p.r + row * p.K + 8 * c) = v[i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float a[8];
-      widen8(v[i], a);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], sum);
-    }
-    sum = row_sum(sum, p.warps, s_part, parity);
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.K) + p.eps);
-    if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = i * T + t;
-      const bool here = live && c < nv;
-      float a[8], g[8];
-      widen8(v[i], a);
-      if (here) {
-        load_gain<kGainF32>(p.gain, 8 * c, g);
-        // r * gain is exact for a BF16 gain, so y is rounded once before BF16
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = a[e] * g[e] * rstd;
-      }
-      const uint4 y = round8(a);
-      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + row * p.K + 8 * c) = y;
-      if (p.q != nullptr) {
-        const Divisor d = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(y)) & 0xFFFFu));
-        if (here) {
-          *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * c) = quant8<kPow2>(y, d);
-          if ((c & 15) == 0) p.s[static_cast<int64_t>(c >> 4) * p.M + row] = d.s;
-        }
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------- norm's gradient
-struct NormBackwardParams {
-  const uint16_t* dy;
-  const uint16_t* r;
-  const void* gain;
-  const float* rstd;
-  const uint16_t* dres;  // or NULL
-  int64_t M, lddy, ldr, lddres;
-  int K, warps, stages;
-  uint16_t* dx;
-  float* part;           // [CTAs][K], or NULL: no gain gradient
-  uint64_t timeout_ns;
-};
-
+constexpr int kNormFour = 1024;   // pieces a row from which a thread of the norm takes four
+constexpr int kNormWarps = 32;    // of the norm, per SM
 constexpr int kRingMaxStages = 4;
 constexpr int kRingBytes = 112 * 1024;       // of a CTA, two to an SM
 constexpr int kRingMaxBytes = 224 * 1024;    // of a CTA that has an SM for itself
@@ -247,13 +144,211 @@ __device__ __forceinline__ uint4 round8x2(const float2 (&f)[4]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Eight gains of a thread's columns, kept as they are stored.
 template <bool kF32>
-__device__ __forceinline__ void load_gain2(const void* gain, int c, float2 (&f)[4]) {
-  float v[8];
-  load_gain<kF32>(gain, c, v);
+struct Gain;
+template <>
+struct Gain<false> {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* gain, int c, bool here) {
+    w = make_uint4(0u, 0u, 0u, 0u);
+    if (here) w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gain) + c));
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const { widen8x2(w, f); }
+};
+template <>
+struct Gain<true> {
+  float2 v[4];
+  __device__ __forceinline__ void load(const void* gain, int c, bool here) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gain) + c);
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 a = here ? __ldg(p) : zero, b = here ? __ldg(p + 1) : zero;
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) f[i] = v[i];
+  }
+};
+
+// The ring of a CTA: step i is the CTA's rows row(i) .. row(i) + rows - 1 of up to
+// three matrices, copied row by row into stage i % stages, one lane of warp 0 per
+// row and matrix.
+struct RowRing {
+  uint8_t* base;
+  uint64_t* full;
+  int64_t M;
+  int rows, arrays, stages, steps;
+  uint32_t row_bytes, array_bytes;
+  __device__ __forceinline__ RowRing(uint8_t* ring, uint64_t* bars, int K, int rows_, int arrays_, int stages_, int64_t M_)
+      : base(ring), full(bars), M(M_), rows(rows_), arrays(arrays_), stages(stages_) {
+    row_bytes = 2u * static_cast<uint32_t>(K);
+    array_bytes = rows * row_bytes;
+    const int64_t step_rows = static_cast<int64_t>(gridDim.x) * rows;
+    steps = static_cast<int>((M - row(0) + step_rows - 1) / step_rows);
+  }
+  __device__ __forceinline__ int64_t row(int step) const {
+    return (static_cast<int64_t>(step) * gridDim.x + blockIdx.x) * rows;
+  }
+  __device__ __forceinline__ uint8_t* stage(int step) const { return base + (step % stages) * (arrays * array_bytes); }
+  __device__ __forceinline__ void init() const {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void issue(int step, const uint16_t* const (&src)[3], const int64_t (&ld)[3]) const {
+    if (threadIdx.x >= 32 || step >= steps) return;
+    uint64_t* bar = &full[step % stages];
+    const int64_t row0 = row(step);
+    const int n = static_cast<int>(min(static_cast<int64_t>(rows), M - row0));
+    const int lane = threadIdx.x;
+    if (lane == 0) mbar_arrive_expect_tx(bar, arrays * n * row_bytes);
+    __syncwarp();
+    if (lane < arrays * n) {
+      const int which = lane / n, i = lane - which * n;
+      const uint16_t* from = which == 0 ? src[0] + (row0 + i) * ld[0] : which == 1 ? src[1] + (row0 + i) * ld[1] : src[2] + (row0 + i) * ld[2];
+      bulk_load(stage(step) + which * array_bytes + i * row_bytes, from, row_bytes, bar);
+    }
+    __syncwarp();
+  }
+  // After a wait that ran out: the copies of steps [from, to) land before the CTA may leave.
+  __device__ __forceinline__ void drain(int from, int to, uint64_t timeout_ns) const {
+    if (threadIdx.x >= 32) return;
+    for (int step = from; step < min(steps, to); ++step) (void)mbar_wait(&full[step % stages], (step / stages) & 1, timeout_ns);
+  }
+};
+
+// ------------------------------------------------------------------- norm
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* res;   // or NULL
+  const void* gain;
+  int64_t M, ldx, ldr;
+  int K, warps, stages;
+  float eps, inv_k;
+  uint16_t* r;           // or NULL
+  uint16_t* y;           // or NULL
+  uint8_t* q;            // or NULL (with s)
+  float* s;
+  float* rstd;           // or NULL
+  uint64_t timeout_ns;
+};
+
+// A CTA's rows come by bulk copies into a ring of stages that the next rows fill
+// while one is worked on; the sum of x and the residual then stays in registers,
+// as the gain does over all rows.
+template <int kVecs, bool kGainF32, bool kPow2>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float s_part[2][kNormMaxThreads / 32];
+  __shared__ uint64_t full[kRingMaxStages];
+  const int T = 32 * p.warps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
+  const int nv = p.K / 8;
+  const int arrays = p.res != nullptr ? 2 : 1;
+  RowRing rr(ring, full, p.K, blockDim.x / T, arrays, p.stages, p.M);
+  const uint16_t* const src[3] = {p.x, p.res, nullptr};
+  const int64_t ld[3] = {p.ldx, p.ldr, 0};
+  __shared__ Divisors<kPow2> divisors;
+  divisors.init();
+  rr.init();
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int s = 0; s < p.stages; ++s) rr.issue(s, src, ld);
+  Gain<kGainF32> gain[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = i * T + t;
+    gain[i].load(p.gain, 8 * c, c < nv);
+  }
+  int waited = 0;
+  for (int step = 0; step < rr.steps; ++step) {
+    const int64_t row = rr.row(step) + sub;
+    const bool live = row < p.M;
+    const bool ok = mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
+    const uint8_t* stage = rr.stage(step) + sub * rr.row_bytes;
+    uint4 v[kVecs];
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!(ok && live && c < nv)) continue;
+      v[i] = *reinterpret_cast<const uint4*>(stage + 16 * c);
+      float2 a[4];
+      widen8x2(v[i], a);
+      if (arrays == 2) {
+        float2 b[4];
+        widen8x2(*reinterpret_cast<const uint4*>(stage + rr.array_bytes + 16 * c), b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
+        v[i] = round8x2(a);
+        *reinterpret_cast<uint4*>(p.r + row * p.K + 8 * c) = v[i];
+        widen8x2(v[i], a);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = __ffma2_rn(a[e], a[e], sum);
+    }
+    const float lanes = warp_sum(sum.x + sum.y);
+    const int parity = step & 1;
+    if (lane == 0) s_part[parity][warp] = lanes;
+    if (!__syncthreads_and(ok)) {
+      if (threadIdx.x == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
+      break;
+    }
+    ++waited;
+    rr.issue(step + p.stages, src, ld);   // the stage just read: every thread holds its values
+    // the hardware's reciprocal root (2^-22.9) and one Newton step
+    const float m = fmaf(sum_of_warps(&s_part[parity][sub * p.warps], p.warps), p.inv_k, p.eps);
+    const float root = rsqrtf(m);
+    const float rstd = root * fmaf(-0.5f * m * root, root, 1.5f);
+    const float2 rstd2 = make_float2(rstd, rstd);
+    if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = i * T + t;
+      const bool here = live && c < nv;
+      float2 a[4], g[4];
+      widen8x2(v[i], a);
+      gain[i].get(g);
+      // r * gain is exact for a BF16 gain, so y is rounded once before BF16
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], g[e]), rstd2);
+      const uint4 y = round8x2(a);
+      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + row * p.K + 8 * c) = y;
+      if (p.q != nullptr) {
+        uint2 codes;
+        const float s = quantise8<kPow2>(y, half_warp_max(umax_halves(absmax8_bits(y)) & 0xFFFFu), divisors, codes);
+        if (here) {
+          *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * c) = codes;
+          if ((c & 15) == 0) p.s[static_cast<int64_t>(c >> 4) * p.M + row] = s;
+        }
+      }
+    }
+  }
+  if (waited < rr.steps) rr.drain(waited, waited + p.stages, p.timeout_ns);
 }
+
+// ---------------------------------------------------------- norm's gradient
+struct NormBackwardParams {
+  const uint16_t* dy;
+  const uint16_t* r;
+  const void* gain;
+  const float* rstd;
+  const uint16_t* dres;  // or NULL
+  int64_t M, lddy, ldr, lddres;
+  int K, warps, stages;
+  float inv_k;           // 1 / K
+  uint16_t* dx;
+  float* part;           // [CTAs][K], or NULL: no gain gradient
+  uint64_t timeout_ns;
+};
 
 // With t = dy gain: dx = rstd t - r rstd^3 mean(t r) + dres.  dy r is exact in
 // float32 and serves the mean and the gain's sum, which stays in the thread's
@@ -271,71 +366,49 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
   const int rows = blockDim.x / T;
   const int nv = p.K / 8;
   const int arrays = p.dres != nullptr ? 3 : 2;
-  const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.K);
-  const uint32_t stage_bytes = arrays * rows * row_bytes;
-  const int64_t rstep = static_cast<int64_t>(gridDim.x) * rows;
-  const int64_t row_first = static_cast<int64_t>(blockIdx.x) * rows;
-  const int steps = static_cast<int>((p.M - row_first + rstep - 1) / rstep);
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
+  RowRing rr(ring, full, p.K, rows, arrays, p.stages, p.M);
+  const uint16_t* const src[3] = {p.dy, p.r, p.dres};
+  const int64_t ld[3] = {p.lddy, p.ldr, p.lddres};
+  rr.init();
   griddep_launch_dependents();
   griddep_wait();
-  // one lane per row and array copies it
-  auto issue = [&](int step) {
-    if (warp != 0 || step >= steps) return;
-    const int s = step % p.stages;
-    const int64_t row0 = row_first + step * rstep;
-    const int n = static_cast<int>(min(static_cast<int64_t>(rows), p.M - row0));
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], arrays * n * row_bytes);
-    __syncwarp();
-    if (lane < arrays * n) {
-      const int which = lane / n, i = lane - which * n;
-      const uint16_t* src = which == 0   ? p.dy + (row0 + i) * p.lddy
-                            : which == 1 ? p.r + (row0 + i) * p.ldr
-                                         : p.dres + (row0 + i) * p.lddres;
-      bulk_load(ring + s * stage_bytes + (which * rows + i) * row_bytes, src, row_bytes, &full[s]);
-    }
-    __syncwarp();
-  };
-  for (int s = 0; s < p.stages; ++s) issue(s);
-  float2 acc[kVecs][4], gain[kVecs][4];
+  for (int s = 0; s < p.stages; ++s) rr.issue(s, src, ld);
+  float2 acc[kVecs][4];
+  Gain<kGainF32> gain[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = i * T + t;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = gain[i][e] = make_float2(0.0f, 0.0f);
-    if (c < nv) load_gain2<kGainF32>(p.gain, 8 * c, gain[i]);
+    for (int e = 0; e < 4; ++e) acc[i][e] = make_float2(0.0f, 0.0f);
+    gain[i].load(p.gain, 8 * c, c < nv);
   }
   auto rstd_of = [&](int step) {
-    const int64_t row = row_first + step * rstep + sub;
-    return step < steps && row < p.M ? __ldg(p.rstd + row) : 0.0f;
+    const int64_t row = rr.row(step) + sub;
+    return step < rr.steps && row < p.M ? __ldg(p.rstd + row) : 0.0f;
   };
   float rstd_next = rstd_of(0);
   int waited = 0;
-  for (int step = 0; step < steps; ++step) {
-    const int s = step % p.stages;
-    const int64_t row = row_first + step * rstep + sub;
+  for (int step = 0; step < rr.steps; ++step) {
+    const int64_t row = rr.row(step) + sub;
     const bool live = row < p.M;
     const float rstd = rstd_next;
     rstd_next = rstd_of(step + 1);
-    const bool ok = mbar_wait(&full[s], (step / p.stages) & 1, p.timeout_ns);
-    const uint8_t* stage = ring + s * stage_bytes + sub * row_bytes;
+    const bool ok = mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
+    const uint8_t* stage = rr.stage(step) + sub * rr.row_bytes;
     float2 sum = make_float2(0.0f, 0.0f);
     const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int c = i * T + t;
       if (!(ok && live && c < nv)) continue;
-      float2 a[4], b[4];
+      float2 a[4], b[4], g[4];
+      gain[i].get(g);
       widen8x2(*reinterpret_cast<const uint4*>(stage + 16 * c), a);
-      widen8x2(*reinterpret_cast<const uint4*>(stage + rows * row_bytes + 16 * c), b);
+      widen8x2(*reinterpret_cast<const uint4*>(stage + rr.array_bytes + 16 * c), b);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 ab = __fmul2_rn(a[e], b[e]);
-        sum = __ffma2_rn(ab, gain[i][e], sum);
+        sum = __ffma2_rn(ab, g[e], sum);
         acc[i][e] = __ffma2_rn(ab, rstd2, acc[i][e]);
       }
     }
@@ -347,32 +420,30 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
       break;
     }
     ++waited;
-    if (step > 0) issue(step - 1 + p.stages);   // every thread is done with the stage before
-    float total = s_part[parity][sub * p.warps];
-    for (int i = 1; i < p.warps; ++i) total += s_part[parity][sub * p.warps + i];
-    const float f = -(rstd * rstd * (rstd * (total / static_cast<float>(p.K))));
+    if (step > 0) rr.issue(step - 1 + p.stages, src, ld);   // every thread is done with the stage before
+    const float total = sum_of_warps(&s_part[parity][sub * p.warps], p.warps);
+    const float f = -(rstd * rstd * (rstd * (total * p.inv_k)));
     const float2 f2 = make_float2(f, f);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int c = i * T + t;
       if (!(live && c < nv)) continue;
-      float2 a[4], b[4];
+      float2 a[4], b[4], g[4];
+      gain[i].get(g);
       widen8x2(*reinterpret_cast<const uint4*>(stage + 16 * c), a);
-      widen8x2(*reinterpret_cast<const uint4*>(stage + rows * row_bytes + 16 * c), b);
+      widen8x2(*reinterpret_cast<const uint4*>(stage + rr.array_bytes + 16 * c), b);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] = __ffma2_rn(b[e], f2, __fmul2_rn(__fmul2_rn(a[e], gain[i][e]), rstd2));
+      for (int e = 0; e < 4; ++e) a[e] = __ffma2_rn(b[e], f2, __fmul2_rn(__fmul2_rn(a[e], g[e]), rstd2));
       if (arrays == 3) {
-        widen8x2(*reinterpret_cast<const uint4*>(stage + 2 * rows * row_bytes + 16 * c), b);
+        widen8x2(*reinterpret_cast<const uint4*>(stage + 2 * rr.array_bytes + 16 * c), b);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
       }
       *reinterpret_cast<uint4*>(p.dx + row * p.K + 8 * c) = round8x2(a);
     }
   }
-  if (waited < steps) {   // a wait ran out: what was issued lands before the CTA may leave
-    if (warp == 0)
-      for (int step = waited; step < min(steps, max(waited - 1, 0) + p.stages); ++step)
-        (void)mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
+  if (waited < rr.steps) {
+    rr.drain(waited, max(waited - 1, 0) + p.stages, p.timeout_ns);
     return;
   }
   if (p.part == nullptr) return;
@@ -453,6 +524,8 @@ __global__ void __launch_bounds__(kCbThreads) combine_backward_kernel(const Comb
   __shared__ float s_w[kCbSlots];         // the row's weight
   __shared__ int s_write[kCbSlots];       // this slot writes the row
   __shared__ float s_dot[kCbSlots][kCbThreads / 32];
+  __shared__ Divisors<kPow2> divisors;
+  divisors.init();
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -535,9 +608,11 @@ __global__ void __launch_bounds__(kCbThreads) combine_backward_kernel(const Comb
       const uint4 d = round8(b);
       if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = d;
       if (p.q != nullptr) {
-        const Divisor dv = divisor_of<kPow2>(static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(amax * fabsf(w)))));
-        *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = quant8<kPow2>(d, dv);
-        if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = dv.s;
+        uint2 codes;
+        const uint32_t top = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(amax * fabsf(w))));
+        const float s = quantise8<kPow2>(d, top, divisors, codes);
+        *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = codes;
+        if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = s;
       }
     }
   }
@@ -638,6 +713,9 @@ constexpr int kSbThreads = 256;   // or as many as a row has pieces, up to 512
 // 16 threads; whole warps go through the loop together.
 template <bool kPow2>
 __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwardParams p) {
+  __shared__ Divisors<kPow2> divisors;
+  divisors.init();
+  __syncthreads();
   griddep_launch_dependents();
   const int upr = static_cast<int>(p.I / 8);          // pieces a row, a multiple of 16
   const bool whole = upr * p.rows <= static_cast<int>(blockDim.x);
@@ -679,10 +757,11 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwa
         const int64_t col = part * p.I + 8 * c;
         if (here && p.dh != nullptr) *reinterpret_cast<uint4*>(p.dh + row * 2 * p.I + col) = d[part];
         if (p.q != nullptr) {
-          const Divisor dv = divisor_of<kPow2>(half_warp_max(umax_halves(absmax8_bits(d[part])) & 0xFFFFu));
+          uint2 codes;
+          const float s = quantise8<kPow2>(d[part], half_warp_max(umax_halves(absmax8_bits(d[part])) & 0xFFFFu), divisors, codes);
           if (here) {
-            *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = quant8<kPow2>(d[part], dv);
-            if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = dv.s;
+            *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = codes;
+            if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = s;
           }
         }
       }
@@ -701,22 +780,21 @@ cudaError_t resident_ctas(Kern kern, int threads, int sm_count, std::atomic<int>
 }
 
 template <int kVecs, bool kGainF32, bool kPow2>
-cudaError_t run_norm(const NormParams& p, const RowPlace& at, int sm_count, cudaStream_t stream) {
+cudaError_t run_norm(const NormParams& p, int grid, int threads, int smem, cudaStream_t stream) {
   auto kern = norm_kernel<kVecs, kGainF32, kPow2>;
-  const int threads = 32 * at.warps * at.rows;
-  static std::atomic<int> cache[kNormMaxThreads / 32 + 1][kMaxCachedDevices];
-  int64_t slots = 0;
-  const cudaError_t e = resident_ctas(kern, threads, sm_count, cache[threads / 32], &slots);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
   if (e != cudaSuccess) return e;
-  const int64_t need = (p.M + at.rows - 1) / at.rows;
-  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), threads, stream, p);
+  return launch_behind_smem(kern, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(threads), static_cast<size_t>(smem),
+                            stream, p);
 }
 
 template <int kVecs>
-cudaError_t run_norm_kind(const NormParams& p, const RowPlace& at, bool gain_f32, bool pow2, int sm_count, cudaStream_t stream) {
+cudaError_t run_norm_kind(const NormParams& p, bool gain_f32, bool pow2, int grid, int threads, int smem, cudaStream_t stream) {
   if (gain_f32)
-    return pow2 ? run_norm<kVecs, true, true>(p, at, sm_count, stream) : run_norm<kVecs, true, false>(p, at, sm_count, stream);
-  return pow2 ? run_norm<kVecs, false, true>(p, at, sm_count, stream) : run_norm<kVecs, false, false>(p, at, sm_count, stream);
+    return pow2 ? run_norm<kVecs, true, true>(p, grid, threads, smem, stream)
+                : run_norm<kVecs, true, false>(p, grid, threads, smem, stream);
+  return pow2 ? run_norm<kVecs, false, true>(p, grid, threads, smem, stream)
+              : run_norm<kVecs, false, false>(p, grid, threads, smem, stream);
 }
 
 // Ring and grid of the gradient: two CTAs an SM where two stages of half an SM's
@@ -728,7 +806,7 @@ struct NormBackwardPlan {
 };
 NormBackwardPlan plan_norm_backward(int64_t M, int64_t K, bool dres) {
   NormBackwardPlan n;
-  n.at = place_rows(static_cast<int>(K));
+  n.at = place_rows(static_cast<int>(K), 256);
   n.stage_bytes = static_cast<int>((dres ? 3 : 2) * n.at.rows * K * 2);
   const bool two = 12 * n.at.rows * K <= kRingBytes;   // two stages of three arrays, with or without dres
   n.stages = std::min(kRingMaxStages, (two ? kRingBytes : kRingMaxBytes) / n.stage_bytes);
@@ -749,13 +827,20 @@ cudaError_t run_norm_backward(const NormBackwardParams& p, const NormBackwardPla
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream) {
-  const RowPlace at = place_rows(static_cast<int>(a.K));
+  const RowPlace at = place_rows(static_cast<int>(a.K), kNormFour);
+  const int threads = 32 * at.warps * at.rows;
+  const int stage_bytes = static_cast<int>((a.res != nullptr ? 2 : 1) * at.rows * a.K * 2);
+  int ctas = std::max(1, kNormWarps / (at.warps * at.rows));   // per SM
+  while (ctas > 1 && 2 * stage_bytes > kRingMaxBytes / ctas - 1024) --ctas;
   NormParams p;
   p.x = a.x; p.res = a.res; p.gain = a.gain; p.M = a.M; p.ldx = a.ldx; p.ldr = a.ldr; p.K = static_cast<int>(a.K);
-  p.warps = at.warps; p.eps = a.eps; p.r = a.r; p.y = a.y; p.q = a.q; p.s = a.s; p.rstd = a.rstd;
-  return at.vecs == 4   ? run_norm_kind<4>(p, at, a.gain_f32, a.pow2, sm_count, stream)
-         : at.vecs == 2 ? run_norm_kind<2>(p, at, a.gain_f32, a.pow2, sm_count, stream)
-                        : run_norm_kind<1>(p, at, a.gain_f32, a.pow2, sm_count, stream);
+  p.warps = at.warps; p.eps = a.eps; p.inv_k = 1.0f / static_cast<float>(a.K); p.r = a.r; p.y = a.y; p.q = a.q; p.s = a.s; p.rstd = a.rstd; p.timeout_ns = a.timeout_ns;
+  p.stages = std::min(kRingMaxStages, (kRingMaxBytes / ctas - 1024 * (ctas > 1)) / stage_bytes);
+  const int smem = p.stages * stage_bytes;
+  const int grid = static_cast<int>(std::min<int64_t>((a.M + at.rows - 1) / at.rows, static_cast<int64_t>(ctas) * sm_count));
+  return at.vecs == 4   ? run_norm_kind<4>(p, a.gain_f32, a.pow2, grid, threads, smem, stream)
+         : at.vecs == 2 ? run_norm_kind<2>(p, a.gain_f32, a.pow2, grid, threads, smem, stream)
+                        : run_norm_kind<1>(p, a.gain_f32, a.pow2, grid, threads, smem, stream);
 }
 
 int64_t rmsnorm_max_columns() { return kMaxNormK; }
@@ -770,7 +855,7 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, void* ws, cudaStr
   p.dy = a.dy; p.r = a.r; p.gain = a.gain; p.rstd = a.rstd; p.dres = a.dres; p.M = a.M; p.lddy = a.lddy; p.ldr = a.ldr;
   p.lddres = a.lddres; p.K = static_cast<int>(a.K); p.warps = n.at.warps; p.stages = n.stages; p.dx = a.dx;
   p.part = a.dgain != nullptr ? static_cast<float*>(ws) : nullptr;
-  p.timeout_ns = a.timeout_ns;
+  p.timeout_ns = a.timeout_ns; p.inv_k = 1.0f / static_cast<float>(a.K);
   const cudaError_t e = n.at.vecs == 4   ? (a.gain_f32 ? run_norm_backward<4, true>(p, n, stream) : run_norm_backward<4, false>(p, n, stream))
                         : n.at.vecs == 2 ? (a.gain_f32 ? run_norm_backward<2, true>(p, n, stream) : run_norm_backward<2, false>(p, n, stream))
                                          : (a.gain_f32 ? run_norm_backward<1, true>(p, n, stream) : run_norm_backward<1, false>(p, n, stream));
