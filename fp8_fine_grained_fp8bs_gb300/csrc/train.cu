@@ -501,135 +501,245 @@ struct CombineBackwardParams {
   const int32_t* row_of;     // [T][k]
   const int32_t* row_token;  // [rows]
   const float* w;            // [T][k]
-  int k, slots;              // slots per CTA
-  int splits;                // CTAs per token
+  int k, slots, parts;       // slots of a part, parts of a token
+  int warps;                 // that compute; one more copies
+  int chunk, chunks;         // pieces of 8 columns per stage, stages a row is cut into
+  int stages;
   uint16_t* dy;              // or NULL
   uint8_t* q;                // or NULL (with s)
   float* s;
   float* dw;                 // or NULL
+  uint64_t timeout_ns;
 };
 
-constexpr int kCbThreads = 256;
-constexpr int kCbSlots = 8;       // most slots per CTA
-constexpr int kCbZeroRows = 16;   // padding rows looked at by one CTA
+constexpr int kCbVecs = 4;           // pieces of a stage per thread
+constexpr int kCbMaxWarps = 8;
+constexpr int kCbMaxK = 64;
+constexpr int kCbMaxStages = 8;
+constexpr int kCbRingBytes = 64 * 1024;   // of a CTA, three to an SM
 
-// One token and up to kCbSlots of its choices per CTA: a piece of dout is read
-// once, multiplied by each choice's weight into the choice's row, and by the
-// choice's row of y into the weight's gradient.  max |BF16(w x)| over a group is
-// BF16(|w| max |x|), since both roundings are monotonic, so one maximum serves
-// all choices.  CTAs behind the tokens' zero the rows without a token.
+// A CTA walks over parts of tokens (a token's slots, or with few tokens a share of
+// them).  Its last warp streams what the others read through a ring of stages, by
+// bulk copies: a piece of dout's row, then the same piece of y's row for each slot;
+// with a stage go the slot's row and weight.  The other warps keep dout's piece in
+// registers, multiply it by each slot's weight into the slot's row, and by y into the
+// weight's gradient.  max |BF16(w x)| over a group is BF16(|w| max |x|), since both
+// roundings are monotonic, so one maximum serves all slots.  The copying warp also
+// zeroes the CTA's share of the rows without a token, some after each part.
+// (One CTA per token with plain loads, eight slots at once, took 348 us for 8192
+// tokens of 8 x 7168: waiting for its four rounds of loads.)
 template <bool kPow2>
-__global__ void __launch_bounds__(kCbThreads) combine_backward_kernel(const CombineBackwardParams p) {
-  __shared__ int32_t s_row[kCbSlots];     // the slot's row, -1: none
-  __shared__ float s_w[kCbSlots];         // the row's weight
-  __shared__ int s_write[kCbSlots];       // this slot writes the row
-  __shared__ float s_dot[kCbSlots][kCbThreads / 32];
+__global__ void __launch_bounds__(32 * (kCbMaxWarps + 1), 3) combine_backward_kernel(const CombineBackwardParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kCbMaxStages], empty[kCbMaxStages];
+  __shared__ int32_t s_row[kCbMaxStages];     // the stage's row, -1: none
+  __shared__ float s_w[kCbMaxStages];         // its weight
+  __shared__ int s_write[kCbMaxStages];       // this slot writes the row
+  __shared__ float s_dot[2][kCbMaxK][kCbMaxWarps];
   __shared__ Divisors<kPow2> divisors;
-  divisors.init();
-  griddep_launch_dependents();
-  griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nv = static_cast<int>(p.N / 8);
-  const int64_t nkb = p.N / kGroup;
-  const int64_t work = p.T * p.splits;
-  if (blockIdx.x >= work) {
-    const int64_t r0 = (blockIdx.x - work) * kCbZeroRows;
-    for (int64_t row = r0 + warp; row < r0 + kCbZeroRows && row < p.rows; row += kCbThreads / 32) {
-      if (p.row_token[row] >= 0) continue;
-      if (p.dy != nullptr)
-        for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
-      if (p.q != nullptr) {
-        for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = make_uint2(0u, 0u);
-        for (int64_t kb = lane; kb < nkb; kb += 32) p.s[kb * p.rows + row] = 0.0f;
+  const int64_t units = p.T * p.parts;
+  const int stage_bytes = 16 * p.chunk;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], p.warps);
+    }
+    fence_barrier_init();
+  }
+  divisors.init();
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == p.warps) {
+    // ------------------------------------------------------------- copying
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool live = true;
+    // the CTA's share of the rows, looked at 32 at a time
+    const int64_t z1 = p.rows * (blockIdx.x + 1) / gridDim.x;
+    int64_t z = p.rows * blockIdx.x / gridDim.x;
+    auto zero_rows = [&]() {
+      uint32_t mask = __ballot_sync(0xffffffffu, z + lane < z1 && p.row_token[z + lane] < 0);
+      for (; mask != 0u; mask &= mask - 1u) {
+        const int64_t row = z + __ffs(mask) - 1;
+        if (p.dy != nullptr)
+          for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
+        if (p.q != nullptr) {
+          for (int v = lane; v < nv / 2; v += 32) *reinterpret_cast<uint4*>(p.q + row * p.N + 16 * v) = make_uint4(0u, 0u, 0u, 0u);
+          for (int kb = lane; kb < nv / 16; kb += 32) p.s[static_cast<int64_t>(kb) * p.rows + row] = 0.0f;
+        }
+      }
+      z += 32;
+    };
+    // waits for the next stage, names its row and weight, and copies `bytes` into it
+    auto put = [&](const uint16_t* from, uint32_t bytes, int32_t row, float w, int write) {
+      if (!live) return;
+      if (!__shfl_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns), 0)) {
+        live = false;
+        return;
+      }
+      if (lane == 0) {
+        s_row[stage] = row;
+        s_w[stage] = w;
+        s_write[stage] = write;
+        if (bytes != 0u) {
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          bulk_load(ring + stage * stage_bytes, from, bytes, &full[stage]);
+        } else {
+          mbar_arrive(&full[stage]);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+    };
+    for (int64_t u = blockIdx.x; u < units && live; u += gridDim.x) {
+      const int64_t t = u / p.parts;
+      const int j0 = static_cast<int>(u - t * p.parts) * p.slots;
+      const int n = min(p.slots, p.k - j0);
+      // slots lane and lane + 32 of the token
+      int32_t row[2];
+      float w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        row[h] = j < p.k ? p.row_of[t * p.k + j] : -1;
+        w[h] = j < p.k ? p.w[t * p.k + j] : 0.0f;
+        if (row[h] < 0 || row[h] >= p.rows) row[h] = -1;
+        if (row[h] >= 0 && p.row_token[row[h]] != t) {
+          atomicCAS(&g_train_status, 0, kStatusDeviceArg);
+          row[h] = -1;
+        }
+      }
+      // a row named by several slots takes the sum of their weights, once
+      float total[2] = {0.0f, 0.0f};
+      bool first[2] = {true, true};
+      for (int i = 0; i < p.k; ++i) {
+        const int32_t r = __shfl_sync(0xffffffffu, i < 32 ? row[0] : row[1], i & 31);
+        const float wi = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r == row[h]) {
+            total[h] += wi;
+            if (i < lane + 32 * h) first[h] = false;
+          }
+      }
+      for (int c = 0; c < p.chunks; ++c) {
+        const int v0 = c * p.chunk;
+        const uint32_t bytes = 16u * static_cast<uint32_t>(min(p.chunk, nv - v0));
+        put(p.dout + t * p.ldo + 8 * v0, bytes, 0, 0.0f, 0);
+        for (int j = j0; j < j0 + n; ++j) {
+          const int32_t r = __shfl_sync(0xffffffffu, j < 32 ? row[0] : row[1], j & 31);
+          const float wj = __shfl_sync(0xffffffffu, j < 32 ? total[0] : total[1], j & 31);
+          const int write = __shfl_sync(0xffffffffu, static_cast<int>(j < 32 ? first[0] : first[1]), j & 31);
+          put(p.y + static_cast<int64_t>(r) * p.N + 8 * v0, r >= 0 && p.dw != nullptr ? bytes : 0u, r, wj, write && r >= 0);
+        }
+      }
+      if (z < z1) zero_rows();
+    }
+    while (z < z1) zero_rows();
+    if (!live) {   // what was issued lands before the CTA may leave
+      if (lane == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
+      for (int i = 0; i < p.stages && i < issued; ++i) {
+        int st = stage - 1 - i;
+        uint32_t ph = phase;
+        if (st < 0) { st += p.stages; ph ^= 1u; }
+        (void)mbar_wait(&full[st], ph, p.timeout_ns);
       }
     }
     return;
   }
-  const int64_t t = blockIdx.x / p.splits;
-  const int j0 = static_cast<int>(blockIdx.x - t * p.splits) * p.slots;
-  const int n = min(p.slots, p.k - j0);
-  if (threadIdx.x < n) {
-    const int j = j0 + threadIdx.x;
-    const int32_t row = p.row_of[t * p.k + j];
-    bool ok = row >= 0 && row < p.rows;
-    if (ok && p.row_token[row] != t) {
-      atomicCAS(&g_train_status, 0, kStatusDeviceArg);
-      ok = false;
-    }
-    // a row named by several slots takes the sum of their weights, once
-    float w = 0.0f;
-    bool first = ok;
-    for (int i = 0; i < p.k; ++i) {
-      if (p.row_of[t * p.k + i] != row) continue;
-      w += p.w[t * p.k + i];
-      if (i < j) first = false;
-    }
-    s_row[threadIdx.x] = ok ? row : -1;
-    s_w[threadIdx.x] = w;
-    s_write[threadIdx.x] = first;
-  }
-  __syncthreads();
-  float dot[kCbSlots];
+
+  // --------------------------------------------------------------- computing
+  int stage = 0;
+  uint32_t phase = 0, parity = 0;
+  bool live = true;   // a warp whose wait ran out goes on without data, for the barriers' sake
+  auto take = [&]() {
+    live = live && mbar_wait(&full[stage], phase, p.timeout_ns);
+    live = __all_sync(0xffffffffu, live);
+  };
+  auto give = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+  };
+  const int t0 = 32 * kCbVecs * warp + lane;   // this thread's first piece of a stage; its others follow 32 apart
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t t = u / p.parts;
+    const int j0 = static_cast<int>(u - t * p.parts) * p.slots;
+    const int n = min(p.slots, p.k - j0);
+    for (int c = 0; c < p.chunks; ++c) {
+      const int v0 = c * p.chunk;
+      const int len = min(p.chunk, nv - v0);
+      take();
+      uint4 x[kCbVecs];
+      uint32_t top[kCbVecs];
 #pragma unroll
-  for (int j = 0; j < kCbSlots; ++j) dot[j] = 0.0f;
-  // whole warps go through the loop together (half-warp maxima)
-  for (int v0 = 32 * warp; v0 < nv; v0 += kCbThreads) {
-    const int v = v0 + lane;
-    const bool here = v < nv;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (here) x = __ldg(reinterpret_cast<const uint4*>(p.dout + t * p.ldo + 8 * v));
-    uint4 y[kCbSlots];
-    if (p.dw != nullptr) {
+      for (int i = 0; i < kCbVecs; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && t0 + 32 * i < len) x[i] = *reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 16 * (t0 + 32 * i));
+        top[i] = half_warp_max(umax_halves(absmax8_bits(x[i])) & 0xFFFFu);
+      }
+      give();
+      for (int j = 0; j < n; ++j) {
+        take();
+        const int64_t row = live ? s_row[stage] : -1;
+        const float w = s_w[stage];
+        const bool write = live && s_write[stage] != 0;
+        if (p.dw != nullptr) {
+          float2 dot = make_float2(0.0f, 0.0f);
+          if (row >= 0) {
 #pragma unroll
-      for (int j = 0; j < kCbSlots; ++j) {
-        y[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (j < n && here && s_row[j] >= 0)
-          y[j] = __ldg(reinterpret_cast<const uint4*>(p.y + static_cast<int64_t>(s_row[j]) * p.N + 8 * v));
+            for (int i = 0; i < kCbVecs; ++i) {
+              if (t0 + 32 * i >= len) continue;
+              float2 a[4], b[4];
+              widen8x2(x[i], a);
+              widen8x2(*reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 16 * (t0 + 32 * i)), b);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dot = __ffma2_rn(a[e], b[e], dot);
+            }
+          }
+          give();
+          const float sum = warp_sum(dot.x + dot.y);
+          if (lane == 0) s_dot[parity][j][warp] = c == 0 ? sum : s_dot[parity][j][warp] + sum;
+        } else {
+          give();
+        }
+        if (!write) continue;
+        const float2 w2 = make_float2(w, w);
+#pragma unroll
+        for (int i = 0; i < kCbVecs; ++i) {
+          if (t0 + 32 * i >= len) continue;
+          const int v = v0 + t0 + 32 * i;
+          float2 a[4];
+          widen8x2(x[i], a);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(a[e], w2);
+          const uint4 d = round8x2(a);
+          if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = d;
+          if (p.q != nullptr) {
+            uint2 codes;
+            const uint32_t a16 = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(top[i] << 16) * fabsf(w)));
+            const float s = quantise8<kPow2>(d, a16, divisors, codes);
+            *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = codes;
+            if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = s;
+          }
+        }
       }
     }
-    const float amax = __uint_as_float(half_warp_max(umax_halves(absmax8_bits(x)) & 0xFFFFu) << 16);
-    float a[8];
-    widen8(x, a);
-#pragma unroll
-    for (int j = 0; j < kCbSlots; ++j) {
-      if (j >= n || s_row[j] < 0) continue;
-      if (p.dw != nullptr) {
-        float b[8];
-        widen8(y[j], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dot[j] = fmaf(a[e], b[e], dot[j]);
-      }
-      if (!s_write[j] || !here) continue;
-      const int64_t row = s_row[j];
-      const float w = s_w[j];
-      float b[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = a[e] * w;
-      const uint4 d = round8(b);
-      if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = d;
-      if (p.q != nullptr) {
-        uint2 codes;
-        const uint32_t top = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(amax * fabsf(w))));
-        const float s = quantise8<kPow2>(d, top, divisors, codes);
-        *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = codes;
-        if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = s;
-      }
+    if (p.dw == nullptr) continue;
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * p.warps) : "memory");   // the computing warps
+    for (int j = threadIdx.x; j < n; j += 32 * p.warps) {
+      float sum = 0.0f;
+      for (int i = 0; i < p.warps; ++i) sum += s_dot[parity][j][i];
+      p.dw[t * p.k + j0 + j] = sum;
     }
+    parity ^= 1u;
   }
-  if (p.dw == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < kCbSlots; ++j) {
-    if (j >= n) break;
-    const float sum = warp_sum(dot[j]);
-    if (lane == 0) s_dot[j][warp] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x < n) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kCbThreads / 32; ++i) sum += s_dot[threadIdx.x][i];
-    p.dw[t * p.k + j0 + threadIdx.x] = s_row[threadIdx.x] >= 0 ? sum : 0.0f;
-  }
+  if (!live && lane == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
 }
 
 // ------------------------------------------------------- SwiGLU's gradient
@@ -725,26 +835,36 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwa
   const int64_t rstep = static_cast<int64_t>(gridDim.x) * p.rows;
   const bool mine = sub < p.rows;
   griddep_wait();
-  auto is_live = [&](int64_t row) { return mine && row < p.M && (p.live == nullptr || __ldg(p.live + row) >= 0); };
-  auto load = [&](int64_t row, int c, bool live, uint4 (&w)[3]) {
-    w[0] = w[1] = w[2] = make_uint4(0u, 0u, 0u, 0u);
-    if (!live || c >= upr) return;
-    const uint16_t* hr = p.h + row * p.ldh + 8 * c;
-    w[0] = __ldg(reinterpret_cast<const uint4*>(hr));
-    w[1] = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
-    w[2] = __ldg(reinterpret_cast<const uint4*>(p.dv + row * p.lddv + 8 * c));
-  };
   for (int cc = 0; cc < upr; cc += step_c) {
     const int c = c0 + cc;
+    const bool inside = mine && c < upr;
+    // what the thread reads and writes, moved on by the grid's rows
     int64_t row = static_cast<int64_t>(blockIdx.x) * p.rows + sub;
+    const uint16_t* ph = p.h + row * p.ldh + 8 * c;
+    const uint16_t* pv = p.dv + row * p.lddv + 8 * c;
+    const int32_t* pl = p.live == nullptr ? nullptr : p.live + row;
+    int64_t out = row * 2 * p.I + 8 * c;
+    float* ps = p.s == nullptr ? nullptr : p.s + static_cast<int64_t>(c >> 4) * p.M + row;
+    const int64_t half_s = (p.I >> 7) * p.M;
+    auto row_live = [&](int64_t ahead) {
+      return inside && row + ahead < p.M && (pl == nullptr || __ldg(pl + ahead) >= 0);
+    };
     uint4 next[3];
-    load(row, c, is_live(row), next);
-    bool live_after = is_live(row + rstep);            // a row ahead of the loads that wait for it
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.rows; first < p.M; first += rstep, row += rstep) {
+    auto load = [&](bool live, int64_t ahead) {
+      next[0] = next[1] = next[2] = make_uint4(0u, 0u, 0u, 0u);
+      if (!live) return;
+      const uint16_t* hr = ph + ahead * p.ldh;
+      next[0] = __ldg(reinterpret_cast<const uint4*>(hr));
+      next[1] = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
+      next[2] = __ldg(reinterpret_cast<const uint4*>(pv + ahead * p.lddv));
+    };
+    load(row_live(0), 0);
+    bool live_after = row_live(rstep);            // a row ahead of the loads that wait for it
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.rows; first < p.M; first += rstep) {
       const uint4 g = next[0], u = next[1], v = next[2];
-      load(row + rstep, c, live_after, next);
-      live_after = is_live(row + 2 * rstep);
-      const bool here = mine && row < p.M && c < upr;
+      load(live_after, rstep);
+      live_after = row_live(2 * rstep);
+      const bool here = inside && row < p.M;
       uint4 d[2];
       swiglu_grad2(g.x, u.x, v.x, d[0].x, d[1].x);
       swiglu_grad2(g.y, u.y, v.y, d[0].y, d[1].y);
@@ -752,19 +872,33 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwa
       swiglu_grad2(g.w, u.w, v.w, d[0].w, d[1].w);
       const uint32_t far = __vmaxu2(__vmaxu2(g.x, g.y), __vmaxu2(g.z, g.w));
       if ((far >> 16) > kFarGate || (far & 0xFFFFu) > kFarGate) swiglu_grad8_far(g, u, v, &d[0], &d[1]);
+      if (here && p.dh != nullptr) {
+        *reinterpret_cast<uint4*>(p.dh + out) = d[0];
+        *reinterpret_cast<uint4*>(p.dh + out + p.I) = d[1];
+      }
+      if (p.q != nullptr) {
+        // both halves' maxima in one word
+        uint32_t top = __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const int64_t col = part * p.I + 8 * c;
-        if (here && p.dh != nullptr) *reinterpret_cast<uint4*>(p.dh + row * 2 * p.I + col) = d[part];
-        if (p.q != nullptr) {
-          uint2 codes;
-          const float s = quantise8<kPow2>(d[part], half_warp_max(umax_halves(absmax8_bits(d[part])) & 0xFFFFu), divisors, codes);
-          if (here) {
-            *reinterpret_cast<uint2*>(p.q + row * 2 * p.I + col) = codes;
-            if ((c & 15) == 0) p.s[(col >> 7) * p.M + row] = s;
+        for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        uint2 cg, cu;
+        const float sg = quantise8<kPow2>(d[0], top & 0xFFFFu, divisors, cg);
+        const float su = quantise8<kPow2>(d[1], top >> 16, divisors, cu);
+        if (here) {
+          *reinterpret_cast<uint2*>(p.q + out) = cg;
+          *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
+          if ((c & 15) == 0) {
+            ps[0] = sg;
+            ps[half_s] = su;
           }
         }
       }
+      row += rstep;
+      ph += rstep * p.ldh;
+      pv += rstep * p.lddv;
+      if (pl != nullptr) pl += rstep;
+      out += rstep * 2 * p.I;
+      ps += rstep;
     }
   }
 }
@@ -868,13 +1002,28 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int sm_count, 
   CombineBackwardParams p;
   p.dout = a.dout; p.T = a.T; p.ldo = a.ldo; p.N = a.N; p.y = a.y; p.rows = a.rows; p.row_of = a.row_of;
   p.row_token = a.row_token; p.w = a.w; p.k = a.k; p.dy = a.dy; p.q = a.q; p.s = a.s; p.dw = a.dw;
-  // few tokens: one choice per CTA, so that more SMs share them
-  p.slots = a.T * ((a.k + kCbSlots - 1) / kCbSlots) < 2 * sm_count ? 1 : std::min(a.k, kCbSlots);
-  p.splits = (a.k + p.slots - 1) / p.slots;
-  const int64_t grid = a.T * p.splits + (a.rows + kCbZeroRows - 1) / kCbZeroRows;
+  p.timeout_ns = a.timeout_ns;
+  // a stage holds a whole row of up to 8192 columns, else an equal share of it in whole groups
+  const int nv = static_cast<int>(a.N / 8), most = 32 * kCbVecs * kCbMaxWarps;
+  p.chunks = (nv + most - 1) / most;
+  p.chunk = ((nv + p.chunks - 1) / p.chunks + 15) / 16 * 16;
+  p.chunks = (nv + p.chunk - 1) / p.chunk;
+  p.warps = (p.chunk + 32 * kCbVecs - 1) / (32 * kCbVecs);
+  p.stages = std::min(kCbMaxStages, kCbRingBytes / (16 * p.chunk));
+  const int64_t slots = 3 * static_cast<int64_t>(sm_count);
+  // few tokens: their slots go to several CTAs
+  p.parts = static_cast<int>(a.T == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(a.k, slots / a.T)));
+  p.slots = (a.k + p.parts - 1) / p.parts;
+  p.parts = (a.k + p.slots - 1) / p.slots;
+  // and CTAs without a token share the rows to zero, 16 each at least
+  const int64_t grid = std::min(slots, std::max(a.T * p.parts, (a.rows + 15) / 16));
   if (grid <= 0) return cudaSuccess;
-  return launch_behind(a.pow2 ? combine_backward_kernel<true> : combine_backward_kernel<false>,
-                       dim3(static_cast<unsigned>(grid)), kCbThreads, stream, p);
+  auto kern = a.pow2 ? combine_backward_kernel<true> : combine_backward_kernel<false>;
+  const int smem = p.stages * 16 * p.chunk;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCbRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_behind_smem(kern, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(32 * (p.warps + 1)),
+                            static_cast<size_t>(smem), stream, p);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cudaStream_t stream) {

@@ -1,7 +1,7 @@
 """Gradients of the MoE combine and dispatch, against the float64 forms.
 
-dy is the float32 product w dout rounded to BF16, bit for bit.  dw: a thread adds N / 2048 pieces of 8 products (one
-rounding each, fused), 5 steps over lanes, 8 over warps.  dx: a rounding per addend of a float32 sum, then BF16's."""
+dy is the float32 product w dout rounded to BF16, bit for bit.  dw: of up to 8192 columns a thread adds two times 16
+products (one rounding each, fused), their sum, 5 steps over lanes, one over such parts of the row, 8 over warps.  dx: a rounding per addend of a float32 sum, then BF16's."""
 import numpy as np
 import pytest
 
@@ -31,11 +31,12 @@ def _expected_dy(dout, row_of, w, rows):
 
 
 def _dot_steps(N):
-    return 8 * -(-N // 2048) + 5 + 8
+    return 16 + 1 + 5 + -(-N // 8192) + 8
 
 
 @pytest.mark.parametrize("T,E,k,N", [(1, 8, 2, 128), (1, 8, 8, 7168), (3, 5, 1, 256), (37, 16, 4, 640), (200, 63, 6, 2048),
-                                     (700, 32, 8, 384), (129, 64, 13, 128), (5, 64, 64, 256)])
+                                     (700, 32, 8, 384), (129, 64, 13, 128), (5, 64, 64, 256),
+                                     (350, 8, 3, 128), (6, 8, 2, 8320), (3, 4, 2, 20480)])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_combine_gradient(T, E, k, N, pow2):
     torch, fp8bs = require_gpu()
