@@ -655,7 +655,7 @@ int fp8bs_moe_combine_backward(const void* dout, int64_t T, int64_t N, int64_t l
   fp8bs::CombineBackwardArgs a{};
   a.dout = static_cast<const uint16_t*>(dout); a.T = T; a.N = N; a.ldo = ldo; a.y = static_cast<const uint16_t*>(y);
   a.rows = rows; a.row_of = row_of; a.row_token = row_token; a.w = w; a.k = k; a.pow2 = scale_mode == FP8BS_SCALE_POW2;
-  a.dy = static_cast<uint16_t*>(dy); a.q = q; a.s = s; a.dw = dw; a.timeout_ns = g_timeout_ns.load();
+  a.dy = static_cast<uint16_t*>(dy); a.q = q; a.s = s; a.dw = dw;
   return from_cuda(fp8bs::launch_combine_backward(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -173,8 +173,8 @@ cudaError_t launch_moe_combine(const uint16_t* y, int64_t rows_y, int64_t N, con
 cudaError_t launch_moe_dispatch_backward(const uint16_t* d, int64_t rows, int64_t N, const int32_t* idx, int64_t T, int k,
                                          const uint16_t* add, uint16_t* out, int sm_count, cudaStream_t stream);
 
-// ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; all but
-// the last wait for their own copies, bounded by timeout_ns)
+// ---- train.cu (norm, its gradient, gradients of the combine and the SwiGLU; the
+// norm and its gradient wait for their own copies, bounded by timeout_ns)
 struct NormArgs {
   const uint16_t* x;       // [M][ldx]
   const uint16_t* res;     // [M][ldr] or NULL
@@ -223,7 +223,6 @@ struct CombineBackwardArgs {
   uint8_t* q;                // [rows][N] or NULL
   float* s;                  // [N/128][rows]
   float* dw;                 // [T][k] or NULL
-  uint64_t timeout_ns;
 };
 cudaError_t launch_combine_backward(const CombineBackwardArgs& args, int sm_count, cudaStream_t stream);
 

@@ -42,6 +42,21 @@ __device__ __forceinline__ uint4 round8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight values in packed pairs.
+__device__ __forceinline__ void widen8x2(const uint4& v, float2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 round8x2(const float2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // Table of absmax divisors, for kernels whose CTAs quantise many groups.
 template <bool kPow2>
 struct Divisors {
@@ -54,6 +69,13 @@ struct Divisors<true> {
   __device__ __forceinline__ void init() {}
   __device__ __forceinline__ Divisor of(uint32_t a16) const { return pow2_divisor_bits(a16); }
 };
+
+// Out of line: the kernels inline the common way several times over.
+__device__ __noinline__ uint2 quant8_slow(const uint4 v, const Divisor d) { return quant8m(v, d); }
+__device__ __forceinline__ float quantise8_any(const uint4& v, const Divisor& d, uint2& codes) {
+  codes = quant8_slow(v, d);
+  return d.s;
+}
 
 // Eight BF16 values of a group with maximum a16 (BF16 bits) -> eight codes; the
 // scale.  A power of two: with e the biased exponent of the smallest power of two
@@ -77,9 +99,34 @@ __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const D
       return __uint_as_float((e - 8u) << 23);
     }
   }
-  const Divisor d = divisors.of(a16);
-  codes = quant8m(v, d);
-  return d.s;
+  return quantise8_any(v, divisors.of(a16), codes);
+}
+
+// Eight float32 values times w, rounded to BF16.
+__device__ __forceinline__ uint4 times8(const float2 (&a)[4], float w) {
+  const float2 w2 = make_float2(w, w);
+  float2 f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(a[i], w2);
+  return round8x2(f);
+}
+
+// quantise8 of the BF16 values of a * w.  Scaling by a power of two commutes with
+// rounding: the quotients are the BF16 values of a * (w / s), as long as those that
+// reach a code (|v / s| > 2^-10) are normal numbers, which s >= 2^-103 leaves them.
+template <bool kPow2>
+__device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, uint32_t a16, const Divisors<kPow2>& divisors,
+                                                 uint2& codes) {
+  if (kPow2) {
+    const uint32_t e = (a16 + 31u) >> 7;
+    if (e >= 32u) {
+      float2 f[4];
+      widen8x2(times8(a, w * __uint_as_float((262u - e) << 23)), f);
+      codes = make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
+      return __uint_as_float((e - 8u) << 23);
+    }
+  }
+  return quantise8<kPow2>(times8(a, w), a16, divisors, codes);
 }
 
 // |x| maximum (BF16 bits) over the 16 lanes of each half-warp; every lane of the warp takes part.
@@ -129,21 +176,6 @@ constexpr int kRingMaxStages = 4;
 constexpr int kRingBytes = 112 * 1024;       // of a CTA, two to an SM
 constexpr int kRingMaxBytes = 224 * 1024;    // of a CTA that has an SM for itself
 
-// Eight values in packed pairs.
-__device__ __forceinline__ void widen8x2(const uint4& v, float2 (&f)[4]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint4 round8x2(const float2 (&f)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // Eight gains of a thread's columns, kept as they are stored.
 template <bool kF32>
 struct Gain;
@@ -501,245 +533,149 @@ struct CombineBackwardParams {
   const int32_t* row_of;     // [T][k]
   const int32_t* row_token;  // [rows]
   const float* w;            // [T][k]
-  int k, slots, parts;       // slots of a part, parts of a token
-  int warps;                 // that compute; one more copies
-  int chunk, chunks;         // pieces of 8 columns per stage, stages a row is cut into
-  int stages;
+  int k;
   uint16_t* dy;              // or NULL
   uint8_t* q;                // or NULL (with s)
   float* s;
   float* dw;                 // or NULL
-  uint64_t timeout_ns;
 };
 
-constexpr int kCbVecs = 4;           // pieces of a stage per thread
-constexpr int kCbMaxWarps = 8;
-constexpr int kCbMaxK = 64;
-constexpr int kCbMaxStages = 8;
-constexpr int kCbRingBytes = 64 * 1024;   // of a CTA, three to an SM
+constexpr int kCbWarps = 8;       // of a CTA
+constexpr int kCbUnroll = 4;      // pieces a lane works on at once
+constexpr int kCbZeroRows = 8;    // rows without a token that a warp looks for at a time
 
-// A CTA walks over parts of tokens (a token's slots, or with few tokens a share of
-// them).  Its last warp streams what the others read through a ring of stages, by
-// bulk copies: a piece of dout's row, then the same piece of y's row for each slot;
-// with a stage go the slot's row and weight.  The other warps keep dout's piece in
-// registers, multiply it by each slot's weight into the slot's row, and by y into the
-// weight's gradient.  max |BF16(w x)| over a group is BF16(|w| max |x|), since both
-// roundings are monotonic, so one maximum serves all slots.  The copying warp also
-// zeroes the CTA's share of the rows without a token, some after each part.
-// (One CTA per token with plain loads, eight slots at once, took 348 us for 8192
-// tokens of 8 x 7168: waiting for its four rounds of loads.)
-template <bool kPow2>
-__global__ void __launch_bounds__(32 * (kCbMaxWarps + 1), 3) combine_backward_kernel(const CombineBackwardParams p) {
-  extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t full[kCbMaxStages], empty[kCbMaxStages];
-  __shared__ int32_t s_row[kCbMaxStages];     // the stage's row, -1: none
-  __shared__ float s_w[kCbMaxStages];         // its weight
-  __shared__ int s_write[kCbMaxStages];       // this slot writes the row
-  __shared__ float s_dot[2][kCbMaxK][kCbMaxWarps];
+// A warp takes one slot of a token (with few of them, a CTA's warps share one): it
+// multiplies dout's row by the slot's weight into the slot's row, and by the slot's
+// row of y into the weight's gradient.  Consecutive slots are a CTA's, so dout's row
+// comes from L1 but once.  max |BF16(w x)| over a group is BF16(|w| max |x|), since
+// both roundings are monotonic, so the maximum is taken of dout, for two groups in
+// one word.  Behind the slots, warps zero the rows without a token.
+template <bool kPow2, bool kShared>
+__global__ void __launch_bounds__(32 * kCbWarps, 3) combine_backward_kernel(const CombineBackwardParams p) {
+  __shared__ float s_dot[kCbWarps];
   __shared__ Divisors<kPow2> divisors;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nv = static_cast<int>(p.N / 8);
-  const int64_t units = p.T * p.parts;
-  const int stage_bytes = 16 * p.chunk;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], p.warps);
-    }
-    fence_barrier_init();
-  }
+  constexpr int kApart = 32 * (kShared ? kCbWarps : 1);   // between a lane's pieces
+  const int64_t slots = p.T * p.k;
   divisors.init();
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
-
-  if (warp == p.warps) {
-    // ------------------------------------------------------------- copying
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    bool live = true;
-    // the CTA's share of the rows, looked at 32 at a time
-    const int64_t z1 = p.rows * (blockIdx.x + 1) / gridDim.x;
-    int64_t z = p.rows * blockIdx.x / gridDim.x;
-    auto zero_rows = [&]() {
-      uint32_t mask = __ballot_sync(0xffffffffu, z + lane < z1 && p.row_token[z + lane] < 0);
-      for (; mask != 0u; mask &= mask - 1u) {
-        const int64_t row = z + __ffs(mask) - 1;
-        if (p.dy != nullptr)
-          for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t first_item = kShared ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kCbWarps + warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kShared ? 1 : kCbWarps);
+  for (int64_t item = first_item; item < slots; item += step) {
+    const int64_t t = item / p.k;
+    const int j = static_cast<int>(item - t * p.k);
+    // the token's slots, to find those that name the same row
+    const int32_t* of = p.row_of + t * p.k;
+    const int32_t r0 = lane < p.k ? __ldg(of + lane) : -1;
+    const int32_t r1 = p.k > 32 && lane + 32 < p.k ? __ldg(of + lane + 32) : -1;
+    float w = __ldg(p.w + item);
+    int32_t r = __shfl_sync(0xffffffffu, j < 32 ? r0 : r1, j & 31);
+    if (r >= p.rows) r = -1;
+    const int64_t token = r >= 0 ? __ldg(p.row_token + r) : t;
+    const uint64_t same = static_cast<uint64_t>(__ballot_sync(0xffffffffu, r0 == r)) |
+                          (static_cast<uint64_t>(__ballot_sync(0xffffffffu, r1 == r)) << 32);
+    const bool other = token != t;   // row_token gives the row to another token
+    if (other && lane == 0) atomicCAS(&g_train_status, 0, kStatusDeviceArg);
+    const bool dots = r >= 0 && !other && p.dw != nullptr;
+    // a row named by several slots takes the sum of their weights, from the first of them
+    const bool write = r >= 0 && !other && (same & ((uint64_t{1} << j) - 1)) == 0;
+    if (write && (same >> j) != 1) {
+      w = 0.0f;
+      for (uint64_t m = same; m != 0; m &= m - 1) w += __ldg(p.w + t * p.k + __ffsll(static_cast<long long>(m)) - 1);
+    }
+    float2 dot[kCbUnroll];
+#pragma unroll
+    for (int i = 0; i < kCbUnroll; ++i) dot[i] = make_float2(0.0f, 0.0f);
+    if (dots || write) {
+      const int v_first = (kShared ? 32 * warp : 0) + lane;
+      const uint4* px = reinterpret_cast<const uint4*>(p.dout + t * p.ldo) + v_first;
+      const uint4* py = reinterpret_cast<const uint4*>(p.y + r * p.N) + v_first;
+      uint8_t* qo = p.q + r * p.N + 8 * v_first;
+      uint16_t* yo = p.dy + r * p.N + 8 * v_first;
+      float* so = p.s + static_cast<int64_t>(v_first >> 4) * p.rows + r;
+      const int64_t s_step = kApart / 16 * p.rows;
+      // whole warps go through the loop together (half-warp maxima)
+      for (int v0 = v_first - lane; v0 < nv; v0 += kCbUnroll * kApart) {
+        const int v = v0 + lane;
+        uint4 x[kCbUnroll], y[kCbUnroll];
+#pragma unroll
+        for (int i = 0; i < kCbUnroll; ++i) {
+          x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (v + i * kApart >= nv) continue;
+          x[i] = __ldg(px + i * kApart);
+          if (dots) y[i] = __ldg(py + i * kApart);
+        }
+        uint32_t top[kCbUnroll / 2];
         if (p.q != nullptr) {
-          for (int v = lane; v < nv / 2; v += 32) *reinterpret_cast<uint4*>(p.q + row * p.N + 16 * v) = make_uint4(0u, 0u, 0u, 0u);
-          for (int kb = lane; kb < nv / 16; kb += 32) p.s[static_cast<int64_t>(kb) * p.rows + row] = 0.0f;
-        }
-      }
-      z += 32;
-    };
-    // waits for the next stage, names its row and weight, and copies `bytes` into it
-    auto put = [&](const uint16_t* from, uint32_t bytes, int32_t row, float w, int write) {
-      if (!live) return;
-      if (!__shfl_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns), 0)) {
-        live = false;
-        return;
-      }
-      if (lane == 0) {
-        s_row[stage] = row;
-        s_w[stage] = w;
-        s_write[stage] = write;
-        if (bytes != 0u) {
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          bulk_load(ring + stage * stage_bytes, from, bytes, &full[stage]);
-        } else {
-          mbar_arrive(&full[stage]);
-        }
-      }
-      __syncwarp();
-      ++issued;
-      if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-    };
-    for (int64_t u = blockIdx.x; u < units && live; u += gridDim.x) {
-      const int64_t t = u / p.parts;
-      const int j0 = static_cast<int>(u - t * p.parts) * p.slots;
-      const int n = min(p.slots, p.k - j0);
-      // slots lane and lane + 32 of the token
-      int32_t row[2];
-      float w[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        row[h] = j < p.k ? p.row_of[t * p.k + j] : -1;
-        w[h] = j < p.k ? p.w[t * p.k + j] : 0.0f;
-        if (row[h] < 0 || row[h] >= p.rows) row[h] = -1;
-        if (row[h] >= 0 && p.row_token[row[h]] != t) {
-          atomicCAS(&g_train_status, 0, kStatusDeviceArg);
-          row[h] = -1;
-        }
-      }
-      // a row named by several slots takes the sum of their weights, once
-      float total[2] = {0.0f, 0.0f};
-      bool first[2] = {true, true};
-      for (int i = 0; i < p.k; ++i) {
-        const int32_t r = __shfl_sync(0xffffffffu, i < 32 ? row[0] : row[1], i & 31);
-        const float wi = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
+          for (int i = 0; i < kCbUnroll / 2; ++i) {
+            top[i] = __byte_perm(umax_halves(absmax8_bits(x[2 * i])), umax_halves(absmax8_bits(x[2 * i + 1])), 0x5410);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (r == row[h]) {
-            total[h] += wi;
-            if (i < lane + 32 * h) first[h] = false;
+            for (int o = 1; o <= 8; o <<= 1) top[i] = umax16x2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
           }
-      }
-      for (int c = 0; c < p.chunks; ++c) {
-        const int v0 = c * p.chunk;
-        const uint32_t bytes = 16u * static_cast<uint32_t>(min(p.chunk, nv - v0));
-        put(p.dout + t * p.ldo + 8 * v0, bytes, 0, 0.0f, 0);
-        for (int j = j0; j < j0 + n; ++j) {
-          const int32_t r = __shfl_sync(0xffffffffu, j < 32 ? row[0] : row[1], j & 31);
-          const float wj = __shfl_sync(0xffffffffu, j < 32 ? total[0] : total[1], j & 31);
-          const int write = __shfl_sync(0xffffffffu, static_cast<int>(j < 32 ? first[0] : first[1]), j & 31);
-          put(p.y + static_cast<int64_t>(r) * p.N + 8 * v0, r >= 0 && p.dw != nullptr ? bytes : 0u, r, wj, write && r >= 0);
         }
-      }
-      if (z < z1) zero_rows();
-    }
-    while (z < z1) zero_rows();
-    if (!live) {   // what was issued lands before the CTA may leave
-      if (lane == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
-      for (int i = 0; i < p.stages && i < issued; ++i) {
-        int st = stage - 1 - i;
-        uint32_t ph = phase;
-        if (st < 0) { st += p.stages; ph ^= 1u; }
-        (void)mbar_wait(&full[st], ph, p.timeout_ns);
-      }
-    }
-    return;
-  }
-
-  // --------------------------------------------------------------- computing
-  int stage = 0;
-  uint32_t phase = 0, parity = 0;
-  bool live = true;   // a warp whose wait ran out goes on without data, for the barriers' sake
-  auto take = [&]() {
-    live = live && mbar_wait(&full[stage], phase, p.timeout_ns);
-    live = __all_sync(0xffffffffu, live);
-  };
-  auto give = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
-    if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-  };
-  const int t0 = 32 * kCbVecs * warp + lane;   // this thread's first piece of a stage; its others follow 32 apart
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t t = u / p.parts;
-    const int j0 = static_cast<int>(u - t * p.parts) * p.slots;
-    const int n = min(p.slots, p.k - j0);
-    for (int c = 0; c < p.chunks; ++c) {
-      const int v0 = c * p.chunk;
-      const int len = min(p.chunk, nv - v0);
-      take();
-      uint4 x[kCbVecs];
-      uint32_t top[kCbVecs];
 #pragma unroll
-      for (int i = 0; i < kCbVecs; ++i) {
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && t0 + 32 * i < len) x[i] = *reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 16 * (t0 + 32 * i));
-        top[i] = half_warp_max(umax_halves(absmax8_bits(x[i])) & 0xFFFFu);
-      }
-      give();
-      for (int j = 0; j < n; ++j) {
-        take();
-        const int64_t row = live ? s_row[stage] : -1;
-        const float w = s_w[stage];
-        const bool write = live && s_write[stage] != 0;
-        if (p.dw != nullptr) {
-          float2 dot = make_float2(0.0f, 0.0f);
-          if (row >= 0) {
-#pragma unroll
-            for (int i = 0; i < kCbVecs; ++i) {
-              if (t0 + 32 * i >= len) continue;
-              float2 a[4], b[4];
-              widen8x2(x[i], a);
-              widen8x2(*reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 16 * (t0 + 32 * i)), b);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dot = __ffma2_rn(a[e], b[e], dot);
-            }
-          }
-          give();
-          const float sum = warp_sum(dot.x + dot.y);
-          if (lane == 0) s_dot[parity][j][warp] = c == 0 ? sum : s_dot[parity][j][warp] + sum;
-        } else {
-          give();
-        }
-        if (!write) continue;
-        const float2 w2 = make_float2(w, w);
-#pragma unroll
-        for (int i = 0; i < kCbVecs; ++i) {
-          if (t0 + 32 * i >= len) continue;
-          const int v = v0 + t0 + 32 * i;
+        for (int i = 0; i < kCbUnroll; ++i) {
+          if (v + i * kApart >= nv) continue;
           float2 a[4];
           widen8x2(x[i], a);
+          if (dots) {
+            float2 b[4];
+            widen8x2(y[i], b);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(a[e], w2);
-          const uint4 d = round8x2(a);
-          if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = d;
+            for (int e = 0; e < 4; ++e) dot[i] = __ffma2_rn(a[e], b[e], dot[i]);
+          }
+          if (!write) continue;
+          if (p.dy != nullptr) *reinterpret_cast<uint4*>(yo + 8 * i * kApart) = times8(a, w);
           if (p.q != nullptr) {
+            const uint32_t top16 = i & 1 ? top[i / 2] & 0xFFFF0000u : top[i / 2] << 16;
+            const uint32_t a16 = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(top16) * fabsf(w)));
             uint2 codes;
-            const uint32_t a16 = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(top[i] << 16) * fabsf(w)));
-            const float s = quantise8<kPow2>(d, a16, divisors, codes);
-            *reinterpret_cast<uint2*>(p.q + row * p.N + 8 * v) = codes;
-            if ((v & 15) == 0) p.s[static_cast<int64_t>(v >> 4) * p.rows + row] = s;
+            const float s = quantise8_times<kPow2>(a, w, a16, divisors, codes);
+            *reinterpret_cast<uint2*>(qo + 8 * i * kApart) = codes;
+            if ((lane & 15) == 0) so[i * s_step] = s;
           }
         }
+        px += kCbUnroll * kApart;
+        py += kCbUnroll * kApart;
+        qo += 8 * kCbUnroll * kApart;
+        yo += 8 * kCbUnroll * kApart;
+        so += kCbUnroll * s_step;
       }
     }
     if (p.dw == nullptr) continue;
-    asm volatile("bar.sync 1, %0;" ::"r"(32 * p.warps) : "memory");   // the computing warps
-    for (int j = threadIdx.x; j < n; j += 32 * p.warps) {
-      float sum = 0.0f;
-      for (int i = 0; i < p.warps; ++i) sum += s_dot[parity][j][i];
-      p.dw[t * p.k + j0 + j] = sum;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCbUnroll; ++i) sum += dot[i].x + dot[i].y;
+    sum = warp_sum(sum);
+    if (kShared) {
+      if (lane == 0) s_dot[warp] = sum;
+      __syncthreads();
+      sum = s_dot[0];
+#pragma unroll
+      for (int i = 1; i < kCbWarps; ++i) sum += s_dot[i];
+      __syncthreads();
+      if (warp != 0) continue;
     }
-    parity ^= 1u;
+    if (lane == 0) p.dw[item] = sum;
   }
-  if (!live && lane == 0) atomicCAS(&g_train_status, 0, kStatusTimeout);
+  // rows without a token
+  const int64_t z_step = static_cast<int64_t>(gridDim.x) * kCbWarps * kCbZeroRows;
+  for (int64_t z = (static_cast<int64_t>(blockIdx.x) * kCbWarps + warp) * kCbZeroRows; z < p.rows; z += z_step) {
+    const bool none = lane < kCbZeroRows && z + lane < p.rows && __ldg(p.row_token + z + lane) < 0;
+    for (uint32_t mask = __ballot_sync(0xffffffffu, none); mask != 0u; mask &= mask - 1u) {
+      const int64_t row = z + __ffs(mask) - 1;
+      if (p.dy != nullptr)
+        for (int v = lane; v < nv; v += 32) *reinterpret_cast<uint4*>(p.dy + row * p.N + 8 * v) = make_uint4(0u, 0u, 0u, 0u);
+      if (p.q != nullptr) {
+        for (int v = lane; v < nv / 2; v += 32) *reinterpret_cast<uint4*>(p.q + row * p.N + 16 * v) = make_uint4(0u, 0u, 0u, 0u);
+        for (int kb = lane; kb < nv / 16; kb += 32) p.s[static_cast<int64_t>(kb) * p.rows + row] = 0.0f;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------- SwiGLU's gradient
@@ -1002,28 +938,19 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int sm_count, 
   CombineBackwardParams p;
   p.dout = a.dout; p.T = a.T; p.ldo = a.ldo; p.N = a.N; p.y = a.y; p.rows = a.rows; p.row_of = a.row_of;
   p.row_token = a.row_token; p.w = a.w; p.k = a.k; p.dy = a.dy; p.q = a.q; p.s = a.s; p.dw = a.dw;
-  p.timeout_ns = a.timeout_ns;
-  // a stage holds a whole row of up to 8192 columns, else an equal share of it in whole groups
-  const int nv = static_cast<int>(a.N / 8), most = 32 * kCbVecs * kCbMaxWarps;
-  p.chunks = (nv + most - 1) / most;
-  p.chunk = ((nv + p.chunks - 1) / p.chunks + 15) / 16 * 16;
-  p.chunks = (nv + p.chunk - 1) / p.chunk;
-  p.warps = (p.chunk + 32 * kCbVecs - 1) / (32 * kCbVecs);
-  p.stages = std::min(kCbMaxStages, kCbRingBytes / (16 * p.chunk));
-  const int64_t slots = 3 * static_cast<int64_t>(sm_count);
-  // few tokens: their slots go to several CTAs
-  p.parts = static_cast<int>(a.T == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>(a.k, slots / a.T)));
-  p.slots = (a.k + p.parts - 1) / p.parts;
-  p.parts = (a.k + p.slots - 1) / p.slots;
-  // and CTAs without a token share the rows to zero, 16 each at least
-  const int64_t grid = std::min(slots, std::max(a.T * p.parts, (a.rows + 15) / 16));
-  if (grid <= 0) return cudaSuccess;
-  auto kern = a.pow2 ? combine_backward_kernel<true> : combine_backward_kernel<false>;
-  const int smem = p.stages * 16 * p.chunk;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCbRingBytes);
+  // with fewer slots than two a warp of every SM, a CTA's warps share one
+  const int64_t n = a.T * a.k;
+  const bool shared = n < 2 * static_cast<int64_t>(sm_count);
+  auto kern = a.pow2 ? (shared ? combine_backward_kernel<true, true> : combine_backward_kernel<true, false>)
+                     : (shared ? combine_backward_kernel<false, true> : combine_backward_kernel<false, false>);
+  static std::atomic<int> cache[4][kMaxCachedDevices];
+  int64_t resident = 0;
+  const cudaError_t e = resident_ctas(kern, 32 * kCbWarps, sm_count, cache[(a.pow2 ? 2 : 0) + (shared ? 1 : 0)], &resident);
   if (e != cudaSuccess) return e;
-  return launch_behind_smem(kern, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(32 * (p.warps + 1)),
-                            static_cast<size_t>(smem), stream, p);
+  const int64_t zero = kCbZeroRows * kCbWarps;
+  const int64_t grid = std::min(resident, std::max(shared ? n : (n + kCbWarps - 1) / kCbWarps, (a.rows + zero - 1) / zero));
+  if (grid <= 0) return cudaSuccess;
+  return launch_behind(kern, dim3(static_cast<unsigned>(grid)), 32 * kCbWarps, stream, p);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cudaStream_t stream) {

@@ -75,7 +75,7 @@ def test_step_stage_by_stage(T, E, H, I, k):
     # backward, stage by stage
     dyq, sdy, dy, dw = fp8bs.moe_combine_backward(add, saved.y, saved.layout[2], saved.layout[1], w, True, bf16=True)
     _, dw_ref, dw_mag = train.combine_backward(f32(dout), y, row, to_host(w), len(tok))
-    check_near(to_host(dw), dw_ref, dw_mag, 31, 0.0, "dw")
+    check_near(to_host(dw), dw_ref, dw_mag, 25, 0.0, "dw")
     check_codes(dyq, sdy, bits_of(dy), True, "dy")
     dv = fp8bs.grouped_gemm(dyq, sdy, saved.layout[0], *experts.down_t, pow2=True)
     dhq, sdh, _ = fp8bs.swiglu_backward_quantize(saved.h, dv, saved.layout[1], True)

@@ -1,7 +1,8 @@
 """Gradients of the MoE combine and dispatch, against the float64 forms.
 
-dy is the float32 product w dout rounded to BF16, bit for bit.  dw: of up to 8192 columns a thread adds two times 16
-products (one rounding each, fused), their sum, 5 steps over lanes, one over such parts of the row, 8 over warps.  dx: a rounding per addend of a float32 sum, then BF16's."""
+dy is the float32 product w dout rounded to BF16, bit for bit.  dw: a lane
+adds each piece's 4 pairs of products (one rounding each, fused) to one of four pairs of sums, N / 1024 pieces a sum, then
+8 sums, 5 steps over lanes and, where warps share a slot, 8 more.  dx: a rounding per addend of a float32 sum, then BF16's."""
 import numpy as np
 import pytest
 
@@ -31,7 +32,7 @@ def _expected_dy(dout, row_of, w, rows):
 
 
 def _dot_steps(N):
-    return 16 + 1 + 5 + -(-N // 8192) + 8
+    return 4 * -(-N // 1024) + 8 + 5 + 8
 
 
 @pytest.mark.parametrize("T,E,k,N", [(1, 8, 2, 128), (1, 8, 8, 7168), (3, 5, 1, 256), (37, 16, 4, 640), (200, 63, 6, 2048),
