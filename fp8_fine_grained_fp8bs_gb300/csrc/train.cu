@@ -534,6 +534,7 @@ struct CombineBackwardParams {
   const int32_t* row_token;  // [rows]
   const float* w;            // [T][k]
   int k;
+  int zero;                  // rows that a warp looks over at a time
   uint16_t* dy;              // or NULL
   uint8_t* q;                // or NULL (with s)
   float* s;
@@ -542,7 +543,7 @@ struct CombineBackwardParams {
 
 constexpr int kCbWarps = 8;       // of a CTA
 constexpr int kCbUnroll = 4;      // pieces a lane works on at once
-constexpr int kCbZeroRows = 8;    // rows without a token that a warp looks for at a time
+constexpr int kCbZeroRows = 8;    // rows that a warp looks over at a time for those without a token, at most
 
 // A warp takes one slot of a token (with few of them, a CTA's warps share one): it
 // multiplies dout's row by the slot's weight into the slot's row, and by the slot's
@@ -551,7 +552,7 @@ constexpr int kCbZeroRows = 8;    // rows without a token that a warp looks for 
 // both roundings are monotonic, so the maximum is taken of dout, for two groups in
 // one word.  Behind the slots, warps zero the rows without a token.
 template <bool kPow2, bool kShared>
-__global__ void __launch_bounds__(32 * kCbWarps, 3) combine_backward_kernel(const CombineBackwardParams p) {
+__global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(const CombineBackwardParams p) {
   __shared__ float s_dot[kCbWarps];
   __shared__ Divisors<kPow2> divisors;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -663,9 +664,9 @@ __global__ void __launch_bounds__(32 * kCbWarps, 3) combine_backward_kernel(cons
     if (lane == 0) p.dw[item] = sum;
   }
   // rows without a token
-  const int64_t z_step = static_cast<int64_t>(gridDim.x) * kCbWarps * kCbZeroRows;
-  for (int64_t z = (static_cast<int64_t>(blockIdx.x) * kCbWarps + warp) * kCbZeroRows; z < p.rows; z += z_step) {
-    const bool none = lane < kCbZeroRows && z + lane < p.rows && __ldg(p.row_token + z + lane) < 0;
+  const int64_t z_step = static_cast<int64_t>(gridDim.x) * kCbWarps * p.zero;
+  for (int64_t z = (static_cast<int64_t>(blockIdx.x) * kCbWarps + warp) * p.zero; z < p.rows; z += z_step) {
+    const bool none = lane < p.zero && z + lane < p.rows && __ldg(p.row_token + z + lane) < 0;
     for (uint32_t mask = __ballot_sync(0xffffffffu, none); mask != 0u; mask &= mask - 1u) {
       const int64_t row = z + __ffs(mask) - 1;
       if (p.dy != nullptr)
@@ -947,7 +948,8 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int sm_count, 
   int64_t resident = 0;
   const cudaError_t e = resident_ctas(kern, 32 * kCbWarps, sm_count, cache[(a.pow2 ? 2 : 0) + (shared ? 1 : 0)], &resident);
   if (e != cudaSuccess) return e;
-  const int64_t zero = kCbZeroRows * kCbWarps;
+  p.zero = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCbZeroRows, a.rows / (resident * kCbWarps))));
+  const int64_t zero = static_cast<int64_t>(p.zero) * kCbWarps;
   const int64_t grid = std::min(resident, std::max(shared ? n : (n + kCbWarps - 1) / kCbWarps, (a.rows + zero - 1) / zero));
   if (grid <= 0) return cudaSuccess;
   return launch_behind(kern, dim3(static_cast<unsigned>(grid)), 32 * kCbWarps, stream, p);
