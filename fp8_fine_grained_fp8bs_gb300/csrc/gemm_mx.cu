@@ -717,8 +717,14 @@ cudaError_t launch_wgrad_pow2(const GemmArgs& a, int sm_count, cudaStream_t stre
                               bool* reg_check_failed) {
   *tmap_failed = false;
   *reg_check_failed = false;
+  // One CTA's 128x128 tiles, whose two accumulators hide the stores, where pairs would
+  // leave SMs idle and where few rows per expert leave the float32 stores to count (16
+  // experts [4096][7168] of 256 rows 298 us against 348 with pairs, of 1024 rows 575
+  // against 435).  The rows of a segment are known on the device only: K is their
+  // number with the padding.
   const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256) * a.num_groups;
-  if (a.M <= 128 || a.N <= 128 || 2 * tiles < sm_count)
+  const bool few_rows = !a.out_bf16 && a.K <= int64_t{320} * a.num_groups;
+  if (a.M <= 128 || a.N <= 128 || 2 * tiles < sm_count || few_rows)
     return run_mx<128, true, false, false, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
   return run_mx<256, true, false, true, true>(a, sm_count, stream, tmap_failed, reg_check_failed);
 }

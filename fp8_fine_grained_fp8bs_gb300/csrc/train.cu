@@ -503,24 +503,26 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
   }
 }
 
-// The gain's gradient: the CTAs' partial sums added up, 32 columns a CTA, each
-// of its eight warps an eighth of the parts, in a fixed order.
-__global__ void __launch_bounds__(256) norm_gain_kernel(const float* part, int parts, int K, float* dgain, int accumulate) {
-  __shared__ float s_sum[8][32];
+// The gain's gradient: the CTAs' partial sums added up, 32 columns a CTA, each of its
+// warps every 32nd part, in a fixed order.
+constexpr int kGainWarps = 32;
+__global__ void __launch_bounds__(32 * kGainWarps) norm_gain_kernel(const float* part, int parts, int K, float* dgain,
+                                                                    int accumulate) {
+  __shared__ float s_sum[kGainWarps][32];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.0f;
   if (c < K) {
-#pragma unroll 8
-    for (int i = warp; i < parts; i += 8) sum += part[static_cast<int64_t>(i) * K + c];
+#pragma unroll 10
+    for (int i = warp; i < parts; i += kGainWarps) sum += part[static_cast<int64_t>(i) * K + c];
   }
   s_sum[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || c >= K) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) sum += s_sum[i][lane];
+  for (int i = 1; i < kGainWarps; ++i) sum += s_sum[i][lane];
   dgain[c] = accumulate ? dgain[c] + sum : sum;
 }
 
@@ -931,7 +933,7 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, void* ws, cudaStr
                         : n.at.vecs == 2 ? (a.gain_f32 ? run_norm_backward<2, true>(p, n, stream) : run_norm_backward<2, false>(p, n, stream))
                                          : (a.gain_f32 ? run_norm_backward<1, true>(p, n, stream) : run_norm_backward<1, false>(p, n, stream));
   if (e != cudaSuccess || a.dgain == nullptr) return e;
-  return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), 256, stream,
+  return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), 32 * kGainWarps, stream,
                        static_cast<const float*>(p.part), n.grid, p.K, a.dgain, a.accumulate ? 1 : 0);
 }
 

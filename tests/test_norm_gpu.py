@@ -4,8 +4,8 @@ Tolerances count roundings.  A row's sum of squares: a thread adds up to 32 term
 to 16 over warps, so below 64 float32 roundings of a positive sum, half as many on its root, then quotient,
 addition, root and reciprocal: 40 in all.  y takes two products more: 44, and its rounding to BF16.  In the gradient
 the mean of t r takes 64 roundings of its magnitude, rstd^3 and the products 12 more.  The gain's gradient adds a
-CTA's rows one after the other (M / 304 and one, fewer where rows share a CTA), then 304 * 8 / 8 / 8 parts a warp
-and 8 warps.
+thread's rows one after the other (M / 304 and one; fewer where up to 8 rows share a CTA and are added then), 304 / 32
+parts a warp and 32 warps: below M / 304 + 1 + 8 + 10 + 32.
 """
 import numpy as np
 import pytest
@@ -104,7 +104,7 @@ def test_strides_and_in_place():
 
 
 def _gradient_steps(M):
-    return M / 304 + 1 + 304 / 8 + 8 + 4
+    return M / 304 + 1 + 8 + 10 + 32
 
 
 @pytest.mark.parametrize("M,K", SIZES + [(4099, 264), (2500, 7168), (9, 8), (65, 1000), (11, 16376)])
