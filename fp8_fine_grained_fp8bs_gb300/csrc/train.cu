@@ -70,12 +70,8 @@ struct Divisors<true> {
   __device__ __forceinline__ Divisor of(uint32_t a16) const { return pow2_divisor_bits(a16); }
 };
 
-// Out of line: the kernels inline the common way several times over.
-__device__ __noinline__ uint2 quant8_slow(const uint4 v, const Divisor d) { return quant8m(v, d); }
-__device__ __forceinline__ float quantise8_any(const uint4& v, const Divisor& d, uint2& codes) {
-  codes = quant8_slow(v, d);
-  return d.s;
-}
+// The general way out of line, for a kernel that quantises at many places.
+__device__ __noinline__ uint2 quant8m_call(const uint4 v, const Divisor d) { return quant8m(v, d); }
 
 // Eight BF16 values of a group with maximum a16 (BF16 bits) -> eight codes; the
 // scale.  A power of two: with e the biased exponent of the smallest power of two
@@ -83,7 +79,7 @@ __device__ __forceinline__ float quantise8_any(const uint4& v, const Divisor& d,
 // fraction exceed 96, those of 1.75), s = 2^(e - 135).  The quotient is then one
 // exact product, which keeps the sign of a zero.  Groups whose scale or its
 // reciprocal is not a normal number, zeros among them, take the general way.
-template <bool kPow2>
+template <bool kPow2, bool kCall = false>
 __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
@@ -99,7 +95,9 @@ __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const D
       return __uint_as_float((e - 8u) << 23);
     }
   }
-  return quantise8_any(v, divisors.of(a16), codes);
+  const Divisor d = divisors.of(a16);
+  codes = kCall ? quant8m_call(v, d) : quant8m(v, d);
+  return d.s;
 }
 
 // Eight float32 values times w, rounded to BF16.
@@ -126,7 +124,7 @@ __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, 
       return __uint_as_float((e - 8u) << 23);
     }
   }
-  return quantise8<kPow2>(times8(a, w), a16, divisors, codes);
+  return quantise8<kPow2, true>(times8(a, w), a16, divisors, codes);
 }
 
 // |x| maximum (BF16 bits) over the 16 lanes of each half-warp; every lane of the warp takes part.
