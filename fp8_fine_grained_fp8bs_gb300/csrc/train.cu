@@ -57,6 +57,7 @@ __device__ __forceinline__ uint4 round8x2(const float2 (&f)[4]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
 // Table of absmax divisors, for kernels whose CTAs quantise many groups.
 template <bool kPow2>
 struct Divisors {
@@ -170,6 +171,7 @@ inline RowPlace place_rows(int K, int four_from) {   // four pieces a thread fro
 
 constexpr int kNormFour = 1024;   // pieces a row from which a thread of the norm takes four
 constexpr int kNormWarps = 32;    // of the norm, per SM
+constexpr int kNormStages = 2;    // of the norm's ring, see norm_kernel
 constexpr int kRingMaxStages = 4;
 constexpr int kRingBytes = 112 * 1024;       // of a CTA, two to an SM
 constexpr int kRingMaxBytes = 224 * 1024;    // of a CTA that has an SM for itself
@@ -204,26 +206,32 @@ struct Gain<true> {
   }
 };
 
-// The ring of a CTA: step i is the CTA's rows row(i) .. row(i) + rows - 1 of up to
-// three matrices, copied row by row into stage i % stages, one lane of warp 0 per
-// row and matrix.
+// The ring of a CTA: step i is the CTA's rows (i * CTAs + CTA) * rows and on, of up to
+// three matrices, copied row by row into stage i % stages, one lane of warp 0 per row
+// and matrix.  Steps are issued in order and taken in order.
 struct RowRing {
   uint8_t* base;
   uint64_t* full;
-  int64_t M;
+  int64_t M, step_rows;
   int rows, arrays, stages, steps;
-  uint32_t row_bytes, array_bytes;
+  uint32_t row_bytes, array_bytes, stage_bytes;
+  // the step to issue next (warp 0) and the one taken last
+  int issued, in;
+  int64_t in_row;
+  int out;
+  uint32_t out_phase;
   __device__ __forceinline__ RowRing(uint8_t* ring, uint64_t* bars, int K, int rows_, int arrays_, int stages_, int64_t M_)
       : base(ring), full(bars), M(M_), rows(rows_), arrays(arrays_), stages(stages_) {
     row_bytes = 2u * static_cast<uint32_t>(K);
     array_bytes = rows * row_bytes;
-    const int64_t step_rows = static_cast<int64_t>(gridDim.x) * rows;
-    steps = static_cast<int>((M - row(0) + step_rows - 1) / step_rows);
+    stage_bytes = arrays * array_bytes;
+    step_rows = static_cast<int64_t>(gridDim.x) * rows;
+    issued = in = 0;
+    in_row = static_cast<int64_t>(blockIdx.x) * rows;
+    steps = static_cast<int>((M - in_row + step_rows - 1) / step_rows);
+    out = stages - 1;
+    out_phase = 1;
   }
-  __device__ __forceinline__ int64_t row(int step) const {
-    return (static_cast<int64_t>(step) * gridDim.x + blockIdx.x) * rows;
-  }
-  __device__ __forceinline__ uint8_t* stage(int step) const { return base + (step % stages) * (arrays * array_bytes); }
   __device__ __forceinline__ void init() const {
     if (threadIdx.x == 0) {
       for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -231,25 +239,35 @@ struct RowRing {
     }
     __syncthreads();
   }
-  __device__ __forceinline__ void issue(int step, const uint16_t* const (&src)[3], const int64_t (&ld)[3]) const {
-    if (threadIdx.x >= 32 || step >= steps) return;
-    uint64_t* bar = &full[step % stages];
-    const int64_t row0 = row(step);
-    const int n = static_cast<int>(min(static_cast<int64_t>(rows), M - row0));
+  __device__ __forceinline__ void issue(const uint16_t* const (&src)[3], const int64_t (&ld)[3]) {
+    if (threadIdx.x >= 32 || issued == steps) return;
+    const int n = static_cast<int>(min(static_cast<int64_t>(rows), M - in_row));
     const int lane = threadIdx.x;
-    if (lane == 0) mbar_arrive_expect_tx(bar, arrays * n * row_bytes);
+    if (lane == 0) mbar_arrive_expect_tx(&full[in], arrays * n * row_bytes);
     __syncwarp();
     if (lane < arrays * n) {
-      const int which = lane / n, i = lane - which * n;
-      const uint16_t* from = which == 0 ? src[0] + (row0 + i) * ld[0] : which == 1 ? src[1] + (row0 + i) * ld[1] : src[2] + (row0 + i) * ld[2];
-      bulk_load(stage(step) + which * array_bytes + i * row_bytes, from, row_bytes, bar);
+      const int which = lane >= 2 * n ? 2 : lane >= n ? 1 : 0, i = lane - which * n;
+      const uint16_t* from = which == 0 ? src[0] + (in_row + i) * ld[0] : which == 1 ? src[1] + (in_row + i) * ld[1] : src[2] + (in_row + i) * ld[2];
+      bulk_load(base + in * stage_bytes + which * array_bytes + i * row_bytes, from, row_bytes, &full[in]);
     }
     __syncwarp();
+    ++issued;
+    in_row += step_rows;
+    if (++in == stages) in = 0;
   }
-  // After a wait that ran out: the copies of steps [from, to) land before the CTA may leave.
-  __device__ __forceinline__ void drain(int from, int to, uint64_t timeout_ns) const {
+  // Waits for the next step; its stage is stage().
+  __device__ __forceinline__ bool take(uint64_t timeout_ns) {
+    if (++out == stages) {
+      out = 0;
+      out_phase ^= 1u;
+    }
+    return mbar_wait(&full[out], out_phase, timeout_ns);
+  }
+  __device__ __forceinline__ const uint8_t* stage() const { return base + out * stage_bytes; }
+  // After the wait for step `from` ran out: what is issued lands before the CTA may leave.
+  __device__ __forceinline__ void drain(int from, uint64_t timeout_ns) const {
     if (threadIdx.x >= 32) return;
-    for (int step = from; step < min(steps, to); ++step) (void)mbar_wait(&full[step % stages], (step / stages) & 1, timeout_ns);
+    for (int step = from; step < issued; ++step) (void)mbar_wait(&full[step % stages], (step / stages) & 1, timeout_ns);
   }
 };
 
@@ -271,7 +289,11 @@ struct NormParams {
 
 // A CTA's rows come by bulk copies into a ring of stages that the next rows fill
 // while one is worked on; the sum of x and the residual then stays in registers,
-// as the gain does over all rows.
+// as the gain does over all rows.  Two stages, and the next copy issued after a
+// row's stores, keep the reads in flight few: [16384][7168] with a residual takes
+// 124 us (826 MB, 0.98 of the copy bandwidth), with three or four stages 145, with
+// two filled at the barrier 139.  Without a residual it is bound by instructions
+// (about 170 per eight values; 97 us for 355 MB).
 template <int kVecs, bool kGainF32, bool kPow2>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
@@ -282,7 +304,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
   const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
   const int nv = p.K / 8;
   const int arrays = p.res != nullptr ? 2 : 1;
-  RowRing rr(ring, full, p.K, blockDim.x / T, arrays, p.stages, p.M);
+  const int rows = blockDim.x / T;
+  RowRing rr(ring, full, p.K, rows, arrays, p.stages, p.M);
   const uint16_t* const src[3] = {p.x, p.res, nullptr};
   const int64_t ld[3] = {p.ldx, p.ldr, 0};
   __shared__ Divisors<kPow2> divisors;
@@ -290,19 +313,23 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
   rr.init();
   griddep_launch_dependents();
   griddep_wait();
-  for (int s = 0; s < p.stages; ++s) rr.issue(s, src, ld);
+  for (int s = 0; s < p.stages; ++s) rr.issue(src, ld);
   Gain<kGainF32> gain[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = i * T + t;
     gain[i].load(p.gain, 8 * c, c < nv);
   }
+  // this thread's place in the row-major outputs, moved on with the rows
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows + sub;
+  int64_t at = row * p.K + 8 * t;
+  float* ps = p.s + static_cast<int64_t>(t >> 4) * p.M + row;
+  const int64_t at_step = rr.step_rows * p.K, s_step = static_cast<int64_t>(T >> 4) * p.M;
   int waited = 0;
-  for (int step = 0; step < rr.steps; ++step) {
-    const int64_t row = rr.row(step) + sub;
+  for (int step = 0; step < rr.steps; ++step, row += rr.step_rows, at += at_step, ps += rr.step_rows) {
     const bool live = row < p.M;
-    const bool ok = mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
-    const uint8_t* stage = rr.stage(step) + sub * rr.row_bytes;
+    const bool ok = rr.take(p.timeout_ns);
+    const uint8_t* stage = rr.stage() + sub * rr.row_bytes;
     uint4 v[kVecs];
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -319,7 +346,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
         v[i] = round8x2(a);
-        *reinterpret_cast<uint4*>(p.r + row * p.K + 8 * c) = v[i];
+        *reinterpret_cast<uint4*>(p.r + at + 8 * i * T) = v[i];
         widen8x2(v[i], a);
       }
 #pragma unroll
@@ -333,7 +360,6 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
       break;
     }
     ++waited;
-    rr.issue(step + p.stages, src, ld);   // the stage just read: every thread holds its values
     // the hardware's reciprocal root (2^-22.9) and one Newton step
     const float m = fmaf(sum_of_warps(&s_part[parity][sub * p.warps], p.warps), p.inv_k, p.eps);
     const float root = rsqrtf(m);
@@ -351,18 +377,19 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
 #pragma unroll
       for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], g[e]), rstd2);
       const uint4 y = round8x2(a);
-      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + row * p.K + 8 * c) = y;
+      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + at + 8 * i * T) = y;
       if (p.q != nullptr) {
         uint2 codes;
         const float s = quantise8<kPow2>(y, half_warp_max(umax_halves(absmax8_bits(y)) & 0xFFFFu), divisors, codes);
         if (here) {
-          *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * c) = codes;
-          if ((c & 15) == 0) p.s[static_cast<int64_t>(c >> 4) * p.M + row] = s;
+          *reinterpret_cast<uint2*>(p.q + at + 8 * i * T) = codes;
+          if ((lane & 15) == 0) ps[i * s_step] = s;
         }
       }
     }
+    rr.issue(src, ld);   // into the stage that was read before the barrier
   }
-  if (waited < rr.steps) rr.drain(waited, waited + p.stages, p.timeout_ns);
+  if (waited < rr.steps) rr.drain(waited, p.timeout_ns);
 }
 
 // ---------------------------------------------------------- norm's gradient
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
   rr.init();
   griddep_launch_dependents();
   griddep_wait();
-  for (int s = 0; s < p.stages; ++s) rr.issue(s, src, ld);
+  for (int s = 0; s < p.stages; ++s) rr.issue(src, ld);
   float2 acc[kVecs][4];
   Gain<kGainF32> gain[kVecs];
 #pragma unroll
@@ -412,19 +439,17 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
     for (int e = 0; e < 4; ++e) acc[i][e] = make_float2(0.0f, 0.0f);
     gain[i].load(p.gain, 8 * c, c < nv);
   }
-  auto rstd_of = [&](int step) {
-    const int64_t row = rr.row(step) + sub;
-    return step < rr.steps && row < p.M ? __ldg(p.rstd + row) : 0.0f;
-  };
-  float rstd_next = rstd_of(0);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows + sub;
+  uint16_t* out_row = p.dx + row * p.K + 8 * t;
+  const int64_t out_step = rr.step_rows * p.K;
+  float rstd_next = row < p.M ? __ldg(p.rstd + row) : 0.0f;
   int waited = 0;
-  for (int step = 0; step < rr.steps; ++step) {
-    const int64_t row = rr.row(step) + sub;
+  for (int step = 0; step < rr.steps; ++step, row += rr.step_rows, out_row += out_step) {
     const bool live = row < p.M;
     const float rstd = rstd_next;
-    rstd_next = rstd_of(step + 1);
-    const bool ok = mbar_wait(&full[step % p.stages], (step / p.stages) & 1, p.timeout_ns);
-    const uint8_t* stage = rr.stage(step) + sub * rr.row_bytes;
+    rstd_next = row + rr.step_rows < p.M ? __ldg(p.rstd + row + rr.step_rows) : 0.0f;
+    const bool ok = rr.take(p.timeout_ns);
+    const uint8_t* stage = rr.stage() + sub * rr.row_bytes;
     float2 sum = make_float2(0.0f, 0.0f);
     const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
@@ -450,7 +475,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
       break;
     }
     ++waited;
-    if (step > 0) rr.issue(step - 1 + p.stages, src, ld);   // every thread is done with the stage before
+    if (step > 0) rr.issue(src, ld);   // every thread is done with the stage before
     const float total = sum_of_warps(&s_part[parity][sub * p.warps], p.warps);
     const float f = -(rstd * rstd * (rstd * (total * p.inv_k)));
     const float2 f2 = make_float2(f, f);
@@ -469,11 +494,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
       }
-      *reinterpret_cast<uint4*>(p.dx + row * p.K + 8 * c) = round8x2(a);
+      *reinterpret_cast<uint4*>(out_row + 8 * i * T) = round8x2(a);
     }
   }
   if (waited < rr.steps) {
-    rr.drain(waited, max(waited - 1, 0) + p.stages, p.timeout_ns);
+    rr.drain(waited, p.timeout_ns);
     return;
   }
   if (p.part == nullptr) return;
@@ -906,7 +931,7 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int sm_count, cudaStream_t stream)
   NormParams p;
   p.x = a.x; p.res = a.res; p.gain = a.gain; p.M = a.M; p.ldx = a.ldx; p.ldr = a.ldr; p.K = static_cast<int>(a.K);
   p.warps = at.warps; p.eps = a.eps; p.inv_k = 1.0f / static_cast<float>(a.K); p.r = a.r; p.y = a.y; p.q = a.q; p.s = a.s; p.rstd = a.rstd; p.timeout_ns = a.timeout_ns;
-  p.stages = std::min(kRingMaxStages, (kRingMaxBytes / ctas - 1024 * (ctas > 1)) / stage_bytes);
+  p.stages = std::min(kNormStages, (kRingMaxBytes / ctas - 1024 * (ctas > 1)) / stage_bytes);
   const int smem = p.stages * stage_bytes;
   const int grid = static_cast<int>(std::min<int64_t>((a.M + at.rows - 1) / at.rows, static_cast<int64_t>(ctas) * sm_count));
   return at.vecs == 4   ? run_norm_kind<4>(p, a.gain_f32, a.pow2, grid, threads, smem, stream)
