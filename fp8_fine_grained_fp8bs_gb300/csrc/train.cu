@@ -112,13 +112,15 @@ __device__ __forceinline__ uint4 times8(const float2 (&a)[4], float w) {
 
 // quantise8 of the BF16 values of a * w.  Scaling by a power of two commutes with
 // rounding: the quotients are the BF16 values of a * (w / s), as long as those that
-// reach a code (|v / s| > 2^-10) are normal numbers, which s >= 2^-103 leaves them.
+// reach a code (|v / s| > 2^-10) are normal numbers, which s >= 2^-103 leaves them,
+// and w / s stays in range, which |w| < 2^24 does then.
+constexpr float kPlainWeight = 16777216.0f;
 template <bool kPow2>
 __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, uint32_t a16, const Divisors<kPow2>& divisors,
                                                  uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
-    if (e >= 32u) {
+    if (e >= 32u && fabsf(w) < kPlainWeight) {
       float2 f[4];
       widen8x2(times8(a, w * __uint_as_float((262u - e) << 23)), f);
       codes = make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));

@@ -337,7 +337,10 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     """Gradients of moe_layer_fp8 from dout [T, H] bfloat16 (and dloss, one float32, of the balance loss):
     (dx [T, H] bfloat16, the gradient of the values that the layer's input codes stand for, ``dx_add`` added;
     dlogits; dw_gate_up [E, 2I, H] and dw_down [E, H, I] float32).  Weight gradients given are added to and
-    returned.  The experts are those of the forward pass, with their transposed copies."""
+    returned.  The experts are those of the forward pass, with their transposed copies.  Gradients of a 1x128
+    group that are not zeros but all below 448 * 2^-127 have no scale that the products take (the device status
+    reports it): scale the loss."""
+    import torch
     from . import (grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward, moe_route_backward,
                    requant_1x128_to_128x1, swiglu_backward_quantize)
     if experts.gate_up_t is None:
@@ -345,6 +348,10 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     idx, w, *stats = saved.route
     if dloss is not None and not stats:
         raise ValueError("dloss: the forward pass had no balance loss (alpha)")
+    E, two_i, H = experts.gate_up[0].shape
+    for name, out, shape in (("dw_gate_up", dw_gate_up, (E, two_i, H)), ("dw_down", dw_down, (E, H, two_i // 2))):
+        if out is not None and (tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous float32 tensor {shape}")     # before either is added to
     offsets, row_token, row_of = saved.layout
     dyq, sdy, _, dw = moe_combine_backward(dout, saved.y, row_of, row_token, w, pow2=True)
     dv = grouped_gemm(dyq, sdy, offsets, *experts.down_t, pow2=True)

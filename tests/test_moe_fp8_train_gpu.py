@@ -199,3 +199,53 @@ def test_step_in_a_graph():
     assert all(torch.equal(p, q) for p, q in zip(eager, kept))
     assert all(torch.equal(p, q) for p, q in zip(out, step(*held)))
     assert fp8bs.fp8bs_get_device_status() == 0
+
+
+def test_rows_behind_the_last_segment_do_not_matter():
+    """The products leave the rows behind the last expert's as they were: memory full of NaN there changes no bit."""
+    torch, fp8bs = require_gpu()
+    T, E, H, I, k = 90, 6, 256, 128, 2
+    x, res, wg, wd, z, gain, dout = _inputs(T, E, H, I, 8)
+    z[:, 3:] -= 100.0                      # few experts are chosen: most of the rows are behind the last segment
+    experts = moe.quantize_experts_fp8(to_dev_bf16(wg), to_dev_bf16(wd))
+    held = [to_dev_bf16(x), to_dev(gain), to_dev_bf16(res), to_dev(z), to_dev_bf16(dout)]
+
+    def step(fill):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        for n in (1 << 19, 1 << 20):       # what the allocator hands out again, small pieces and large
+            del_me = [torch.full((n,), fill, dtype=torch.uint8, device="cuda:0") for _ in range(64)]
+            del del_me
+        xd, gd, rd, zd, add = held
+        q, s, _, r, rstd = fp8bs.rmsnorm_quantize(xd, gd, rd, EPS, pow2=True)
+        out, saved = moe.moe_layer_fp8(q, s, zd, experts, k)
+        assert int(saved.layout[0][-1]) < len(saved.layout[1])
+        return (out, *moe.moe_layer_fp8_backward(add, saved, experts))
+
+    want = step(0)
+    got = step(0xFF)
+    assert fp8bs.fp8bs_get_device_status() == 0
+    assert all(torch.equal(p, q) for p, q in zip(got, want)) and all(bool(torch.isfinite(t.float()).all()) for t in got)
+
+
+def test_backward_refusals():
+    """Refused before anything is launched or added to."""
+    torch, fp8bs = require_gpu()
+    T, E, H, I, k = 20, 4, 256, 128, 2
+    x, res, wg, wd, z, gain, dout = _inputs(T, E, H, I, 9)
+    experts = moe.quantize_experts_fp8(to_dev_bf16(wg), to_dev_bf16(wd))
+    q, s, *_ = fp8bs.rmsnorm_quantize(to_dev_bf16(x), to_dev(gain), to_dev_bf16(res), EPS, pow2=True)
+    _, saved = moe.moe_layer_fp8(q, s, to_dev(z), experts, k)
+    down = torch.zeros((E, H, I), device="cuda:0")
+    up = torch.zeros((E, 2 * I, H), device="cuda:0")
+    for bad in (up.bfloat16(), up[:, :I], up.transpose(1, 2)):
+        with pytest.raises(ValueError, match="dw_gate_up"):
+            moe.moe_layer_fp8_backward(to_dev_bf16(dout), saved, experts, dw_gate_up=bad, dw_down=down)
+    with pytest.raises(ValueError, match="dw_down"):
+        moe.moe_layer_fp8_backward(to_dev_bf16(dout), saved, experts, dw_gate_up=up, dw_down=down[:2])
+    with pytest.raises(ValueError, match="dloss"):
+        moe.moe_layer_fp8_backward(to_dev_bf16(dout), saved, experts, torch.ones(1, device="cuda:0"))
+    with pytest.raises(ValueError, match="serving"):
+        moe.moe_layer_fp8_backward(to_dev_bf16(dout), saved, experts._replace(gate_up_t=None))
+    torch.cuda.synchronize()
+    assert not down.any() and not up.any()

@@ -127,6 +127,28 @@ def test_combine_gradient_of_no_tokens_bf16_alone_and_strides():
     assert np.array_equal(bits_of(dy), _expected_dy(bits_of(wide[:, :N].contiguous()), row_of, w, rows))
 
 
+@pytest.mark.parametrize("T", [9, 400])
+def test_weights_far_from_one(T):
+    """Weights and rows of any size whose product is a number: w / s alone may be none."""
+    torch, fp8bs = require_gpu()
+    E, k, N = 4, 3, 256
+    row_token, row_of, rows = _layout(T, E, k, 11, 0.0)
+    up = np.array([-125, -120, -60, 0, 60, 100])[np.arange(T) % 6]
+    x = f32(synth.normal_bf16((T, N), 1.0, 13, 4)).astype(np.float64)
+    dout = bf16_of((np.clip(x, -8, 8) * 2.0 ** up[:, None]).astype(np.float32))
+    w = np.stack([2.0 ** (-up - 3 + 20.0 * j) for j in (-1, 0, 1)], 1)
+    w = (np.clip(w, 2.0 ** -120, 2.0 ** 126) * 1.3).astype(np.float32)
+    want = _expected_dy(dout, row_of, w, rows)
+    assert np.isfinite(f32(want)).all() and (w[:, 0] > 2.0 ** 90).any()
+    y = synth.normal_bf16((rows, N), 2.0 ** -20, 14, 1)
+    for pow2 in (True, False):
+        q, s, dy, _ = fp8bs.moe_combine_backward(to_dev_bf16(dout), to_dev_bf16(y), to_dev(row_of), to_dev(row_token), to_dev(w),
+                                                 pow2, bf16=True)
+        assert np.array_equal(bits_of(dy), want)
+        check_codes(q, s, want, pow2, "dy")
+    assert fp8bs.fp8bs_get_device_status() == 0
+
+
 @pytest.mark.parametrize("T,E,k,N", [(1, 8, 2, 8), (3, 5, 1, 264), (37, 16, 4, 640), (300, 32, 8, 7168), (129, 64, 13, 128), (5, 64, 64, 1000)])
 @pytest.mark.parametrize("add", [False, True])
 def test_dispatch_gradient(T, E, k, N, add):

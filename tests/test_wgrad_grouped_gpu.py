@@ -53,7 +53,7 @@ def _run(offsets, N, K, R, out_dtype=None, accumulate=False, seed=0):
 
 SHAPES = [([0, 128], 128, 128, 128), ([0, 256, 256, 896], 256, 384, 896), ([128, 384, 384, 384, 1664], 384, 640, 2048),
           ([0, 0, 0, 128, 128], 128, 256, 256), ([0, 1152, 1280], 1152, 256, 1280), ([0, 128, 256, 384, 512, 640], 1024, 1408, 640),
-          ([0, 4096], 512, 256, 4096), ([256, 768, 1408], 2304, 2176, 1536)]
+          ([0, 4096], 512, 256, 4096), ([0, 384, 1024, 1024, 1920, 3200], 1152, 1408, 3200), ([256, 768, 1408], 2304, 2176, 1536)]
 
 
 @pytest.mark.parametrize("offsets,N,K,R", SHAPES)
