@@ -7,7 +7,9 @@
 // What is quantised is the BF16 value that the unfused operator would store,
 // so codes and scales are those of fp8bs_quantize_act_ex on it (one rounding
 // to BF16, then the quantiser's).  Statistics and sums are float32.  All are
-// memory-bound streams: every input is read once, into registers.
+// streams bound by memory, or next to it by instructions, that read each input
+// once from it: the norms' rows through a ring of bulk copies in shared memory,
+// the others straight into registers.
 #include <algorithm>
 #include <cstdint>
 
@@ -128,13 +130,6 @@ __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, 
     }
   }
   return quantise8<kPow2, true>(times8(a, w), a16, divisors, codes);
-}
-
-// |x| maximum (BF16 bits) over the 16 lanes of each half-warp; every lane of the warp takes part.
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
-#pragma unroll
-  for (int o = 1; o <= 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -291,13 +286,16 @@ struct NormParams {
 
 // A CTA's rows come by bulk copies into a ring of stages that the next rows fill
 // while one is worked on; the sum of x and the residual then stays in registers,
-// as the gain does over all rows.  Two stages, and the next copy issued after a
-// row's stores, keep the reads in flight few: [16384][7168] with a residual takes
-// 124 us (826 MB, 0.98 of the copy bandwidth), with three or four stages 145, with
-// two filled at the barrier 139.  Without a residual it is bound by instructions
-// (about 170 per eight values; 97 us for 355 MB).
-template <int kVecs, bool kGainF32, bool kPow2>
+// as the gain does over all rows, and is stored beside the codes.  Two stages, and
+// the next copy issued after a row's stores, keep the reads in flight few: with a
+// residual it is bound by memory, and [16384][7168] takes 124 us (826 MB, 0.98 of
+// the copy bandwidth), with three or four stages 145, with two filled at the
+// barrier 139, with the sum stored before the barrier or the maxima of two groups in one
+// word 127 to 131.  Without a residual it is bound by instructions, about 170 per
+// eight values at 0.7 of the issue slots: 89 us for 355 MB.
+template <int kVecs, bool kGainF32, bool kPow2, bool kRes>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams p) {
+  constexpr int kPair = kVecs == 4 || (kVecs == 2 && !kRes) ? 2 : 1;   // pieces whose maxima share the shuffles
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float s_part[2][kNormMaxThreads / 32];
   __shared__ uint64_t full[kRingMaxStages];
@@ -305,7 +303,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x / T, t = threadIdx.x - sub * T;
   const int nv = p.K / 8;
-  const int arrays = p.res != nullptr ? 2 : 1;
+  constexpr int arrays = kRes ? 2 : 1;
   const int rows = blockDim.x / T;
   RowRing rr(ring, full, p.K, rows, arrays, p.stages, p.M);
   const uint16_t* const src[3] = {p.x, p.res, nullptr};
@@ -342,13 +340,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
       v[i] = *reinterpret_cast<const uint4*>(stage + 16 * c);
       float2 a[4];
       widen8x2(v[i], a);
-      if (arrays == 2) {
+      if (kRes) {
         float2 b[4];
         widen8x2(*reinterpret_cast<const uint4*>(stage + rr.array_bytes + 16 * c), b);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = __fadd2_rn(a[e], b[e]);
         v[i] = round8x2(a);
-        *reinterpret_cast<uint4*>(p.r + at + 8 * i * T) = v[i];
         widen8x2(v[i], a);
       }
 #pragma unroll
@@ -369,21 +366,36 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
     const float2 rstd2 = make_float2(rstd, rstd);
     if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = i * T + t;
-      const bool here = live && c < nv;
-      float2 a[4], g[4];
-      widen8x2(v[i], a);
-      gain[i].get(g);
-      // r * gain is exact for a BF16 gain, so y is rounded once before BF16
+    for (int i0 = 0; i0 < kVecs; i0 += kPair) {
+      uint4 y[kPair];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], g[e]), rstd2);
-      const uint4 y = round8x2(a);
-      if (here && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + at + 8 * i * T) = y;
-      if (p.q != nullptr) {
-        uint2 codes;
-        const float s = quantise8<kPow2>(y, half_warp_max(umax_halves(absmax8_bits(y)) & 0xFFFFu), divisors, codes);
-        if (here) {
+      for (int i1 = 0; i1 < kPair; ++i1) {
+        const int i = i0 + i1;
+        float2 a[4], g[4];
+        widen8x2(v[i], a);
+        gain[i].get(g);
+        // r * gain is exact for a BF16 gain, so y is rounded once before BF16
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], g[e]), rstd2);
+        y[i1] = round8x2(a);
+        if (live && i * T + t < nv && p.y != nullptr) *reinterpret_cast<uint4*>(p.y + at + 8 * i * T) = y[i1];
+      }
+      uint32_t top = 0u;
+      if (p.q != nullptr) {   // the maxima of two groups in one word
+        top = umax_halves(absmax8_bits(y[0]));
+        if (kPair == 2) top = __byte_perm(top, umax_halves(absmax8_bits(y[kPair - 1])), 0x5410);
+#pragma unroll
+        for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+#pragma unroll
+      for (int i1 = 0; i1 < kPair; ++i1) {
+        const int i = i0 + i1;
+        uint2 codes = make_uint2(0u, 0u);
+        float s = 0.0f;
+        if (p.q != nullptr) s = quantise8<kPow2>(y[i1], i1 ? top >> 16 : top & 0xFFFFu, divisors, codes);
+        if (!(live && i * T + t < nv)) continue;
+        if (kRes) *reinterpret_cast<uint4*>(p.r + at + 8 * i * T) = v[i];
+        if (p.q != nullptr) {
           *reinterpret_cast<uint2*>(p.q + at + 8 * i * T) = codes;
           if ((lane & 15) == 0) ps[i * s_step] = s;
         }
@@ -879,7 +891,7 @@ cudaError_t resident_ctas(Kern kern, int threads, int sm_count, std::atomic<int>
 
 template <int kVecs, bool kGainF32, bool kPow2>
 cudaError_t run_norm(const NormParams& p, int grid, int threads, int smem, cudaStream_t stream) {
-  auto kern = norm_kernel<kVecs, kGainF32, kPow2>;
+  auto kern = p.res != nullptr ? norm_kernel<kVecs, kGainF32, kPow2, true> : norm_kernel<kVecs, kGainF32, kPow2, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
   if (e != cudaSuccess) return e;
   return launch_behind_smem(kern, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(threads), static_cast<size_t>(smem),
