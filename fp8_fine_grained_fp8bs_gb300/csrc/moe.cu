@@ -151,7 +151,8 @@ __device__ __forceinline__ void axpy8(float (&acc)[8], float w, const uint4& v) 
 // kWeighted: the combine.  Without weights it is the gradient of the dispatch
 // (the sum of a token's rows), which starts from `add` (or NULL; it may be
 // `out` itself).  `split` warps share a token's columns: with one each, a single
-// token of 7168 columns and 8 rows took 24 us.
+// token of 7168 columns and 8 rows took 24 us, now 2.6.  8192 such tokens take 174 us
+// (1.17 GB, 0.99 of the copy bandwidth).
 template <bool kWeighted>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const uint16_t* __restrict__ y, int64_t rows_y,
                                                                    int64_t N, const int32_t* __restrict__ idx,
