@@ -773,40 +773,44 @@ __device__ __forceinline__ void swiglu_grad2(uint32_t gw, uint32_t uw, uint32_t 
   duw = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The gradients of the gates below -64 among eight, where e^-g runs out of
-// float32's range in the end: sigma(g) = e^g to within 2^-92, applied as its root
-// twice, once to the larger factor, so that the product does not underflow on the
-// way.  Runs only for eights that hold such a gate; kept out of line.
+// The same for the gates below -64 of a pair, where e^-g runs out of float32's range
+// in the end: sigma(g) = e^g to within 2^-92, applied as its root twice, once to the
+// larger factor, so that the product does not underflow on the way.  Words in which
+// no gate is that low come back as they are.
 constexpr uint32_t kFarGate = 0xC280u;   // BF16 of -64; patterns above it are below -64
-__device__ __noinline__ void swiglu_grad8_far(const uint4 g, const uint4 u, const uint4 v, uint4* dg, uint4* du) {
-  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-  uint32_t* out[2] = {reinterpret_cast<uint32_t*>(dg), reinterpret_cast<uint32_t*>(du)};
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t sh = (i & 1) * 16;
-    const uint32_t gb = (gw[i >> 1] >> sh) & 0xFFFFu;
+__device__ __noinline__ uint2 swiglu_grad2_far(uint32_t gw, uint32_t uw, uint32_t vw, uint32_t dgw, uint32_t duw) {
+  uint2 out = make_uint2(dgw, duw);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t gb = k ? gw >> 16 : gw & 0xFFFFu;
     if (gb <= kFarGate) continue;
     const float gate = __uint_as_float(gb << 16);
-    const float up = __uint_as_float(((uw[i >> 1] >> sh) & 0xFFFFu) << 16);
-    const float dv = __uint_as_float(((vw[i >> 1] >> sh) & 0xFFFFu) << 16);
+    const float up = __uint_as_float(k ? uw & 0xFFFF0000u : uw << 16);
+    const float dv = __uint_as_float(k ? vw & 0xFFFF0000u : vw << 16);
     const float root = expf(0.5f * gate);
     const bool first = fabsf(dv) > fabsf(up);
-    const float r[2] = {(first ? dv : up) * root * (first ? up : dv) * root * (1.0f + gate), dv * root * (gate * root)};
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t rb = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(r[k])));
-      out[k][i >> 1] = (out[k][i >> 1] & ~(0xFFFFu << sh)) | (rb << sh);
-    }
+    const float dg = (first ? dv : up) * root * (first ? up : dv) * root * (1.0f + gate), du = dv * root * (gate * root);
+    const uint32_t a = __bfloat16_as_ushort(__float2bfloat16_rn(dg)), b = __bfloat16_as_ushort(__float2bfloat16_rn(du));
+    out.x = k ? (out.x & 0xFFFFu) | (a << 16) : (out.x & 0xFFFF0000u) | a;
+    out.y = k ? (out.y & 0xFFFFu) | (b << 16) : (out.y & 0xFFFF0000u) | b;
   }
+  return out;
+}
+__device__ __forceinline__ bool any_far_gate(const uint4& g) {
+  const uint32_t m = umax16x2(umax16x2(g.x, g.y), umax16x2(g.z, g.w));
+  return (m >> 16) > kFarGate || (m & 0xFFFFu) > kFarGate;
 }
 
 constexpr int kSbThreads = 256;   // or as many as a row has pieces, up to 512
 
 // Thread = eight columns of one half of h: the columns stay, the rows advance by
 // the grid, with the next row's loads in flight.  A group of 128 is a half-warp's
-// 16 threads; whole warps go through the loop together.  [67712][2048] takes 188 us
-// (1.12 GB, 0.87 of the copy bandwidth), bound by instructions (about 320 for eight
-// columns of both halves, 74% of the issue slots); by a ring of bulk copies 245,
-// unpacked with expf 325.  A minimum of CTAs an SM in the launch bounds costs 20%.
+// 16 threads; whole warps go through the loop together.  Rows with a gate below -64
+// among a warp's are left out and done in a second pass, which rarely has any: with
+// their call inside the loop the results went through local memory, and [67712][2048]
+// took 190 to 228 us as that memory fell; now 178 (1.12 GB, 0.92 of the copy
+// bandwidth).  Bound by instructions next (three quarters of the issue slots); by a
+// ring of bulk copies 245, unpacked with expf 325.
 template <bool kPow2>
 __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwardParams p) {
   __shared__ Divisors<kPow2> divisors;
@@ -844,47 +848,74 @@ __global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwa
       next[1] = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
       next[2] = __ldg(reinterpret_cast<const uint4*>(pv + ahead * p.lddv));
     };
-    load(row_live(0), 0);
-    bool live_after = row_live(rstep);            // a row ahead of the loads that wait for it
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.rows; first < p.M; first += rstep) {
-      const uint4 g = next[0], u = next[1], v = next[2];
-      load(live_after, rstep);
-      live_after = row_live(2 * rstep);
-      const bool here = inside && row < p.M;
-      uint4 d[2];
-      swiglu_grad2(g.x, u.x, v.x, d[0].x, d[1].x);
-      swiglu_grad2(g.y, u.y, v.y, d[0].y, d[1].y);
-      swiglu_grad2(g.z, u.z, v.z, d[0].z, d[1].z);
-      swiglu_grad2(g.w, u.w, v.w, d[0].w, d[1].w);
-      const uint32_t far = __vmaxu2(__vmaxu2(g.x, g.y), __vmaxu2(g.z, g.w));
-      if ((far >> 16) > kFarGate || (far & 0xFFFFu) > kFarGate) swiglu_grad8_far(g, u, v, &d[0], &d[1]);
+    // quantises and stores a row's piece; whole warps come here together
+    auto finish = [&](const uint4 (&d)[2], bool here) {
       if (here && p.dh != nullptr) {
         *reinterpret_cast<uint4*>(p.dh + out) = d[0];
         *reinterpret_cast<uint4*>(p.dh + out + p.I) = d[1];
       }
-      if (p.q != nullptr) {
-        // both halves' maxima in one word
-        uint32_t top = __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
+      if (p.q == nullptr) return;
+      // both halves' maxima in one word
+      uint32_t top = __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
 #pragma unroll
-        for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        uint2 cg, cu;
-        const float sg = quantise8<kPow2>(d[0], top & 0xFFFFu, divisors, cg);
-        const float su = quantise8<kPow2>(d[1], top >> 16, divisors, cu);
-        if (here) {
-          *reinterpret_cast<uint2*>(p.q + out) = cg;
-          *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
-          if ((c & 15) == 0) {
-            ps[0] = sg;
-            ps[half_s] = su;
-          }
-        }
+      for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      uint2 cg, cu;
+      const float sg = quantise8<kPow2>(d[0], top & 0xFFFFu, divisors, cg);
+      const float su = quantise8<kPow2>(d[1], top >> 16, divisors, cu);
+      if (!here) return;
+      *reinterpret_cast<uint2*>(p.q + out) = cg;
+      *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
+      if ((c & 15) == 0) {
+        ps[0] = sg;
+        ps[half_s] = su;
       }
-      row += rstep;
-      ph += rstep * p.ldh;
-      pv += rstep * p.lddv;
-      if (pl != nullptr) pl += rstep;
-      out += rstep * 2 * p.I;
-      ps += rstep;
+    };
+    auto gradients = [&](const uint4& g, const uint4& u, const uint4& v, uint4 (&d)[2]) {
+      swiglu_grad2(g.x, u.x, v.x, d[0].x, d[1].x);
+      swiglu_grad2(g.y, u.y, v.y, d[0].y, d[1].y);
+      swiglu_grad2(g.z, u.z, v.z, d[0].z, d[1].z);
+      swiglu_grad2(g.w, u.w, v.w, d[0].w, d[1].w);
+    };
+    auto move_on = [&](int64_t rows) {
+      row += rows;
+      ph += rows * p.ldh;
+      pv += rows * p.lddv;
+      if (pl != nullptr) pl += rows;
+      out += rows * 2 * p.I;
+      ps += rows;
+    };
+    const int64_t start = static_cast<int64_t>(blockIdx.x) * p.rows;
+    bool far = false;                             // a gate of a row that the warp left out
+    load(row_live(0), 0);
+    bool live_after = row_live(rstep);            // a row ahead of the loads that wait for it
+    for (int64_t first = start; first < p.M; first += rstep) {
+      const uint4 g = next[0], u = next[1], v = next[2];
+      load(live_after, rstep);
+      live_after = row_live(2 * rstep);
+      const bool left_out = __any_sync(0xffffffffu, any_far_gate(g));
+      far = far || left_out;
+      uint4 d[2];
+      gradients(g, u, v, d);
+      finish(d, inside && row < p.M && !left_out);
+      move_on(rstep);
+    }
+    if (!far) continue;
+    for (int64_t first = start; first < p.M; first += rstep) {   // the rows left out, one at a time
+      move_on(first == start ? start + sub - row : rstep);
+      load(row_live(0), 0);
+      if (!__any_sync(0xffffffffu, any_far_gate(next[0]))) continue;
+      const uint4 g = next[0], u = next[1], v = next[2];
+      uint4 d[2];
+      gradients(g, u, v, d);
+      uint2 w = swiglu_grad2_far(g.x, u.x, v.x, d[0].x, d[1].x);
+      d[0].x = w.x, d[1].x = w.y;
+      w = swiglu_grad2_far(g.y, u.y, v.y, d[0].y, d[1].y);
+      d[0].y = w.x, d[1].y = w.y;
+      w = swiglu_grad2_far(g.z, u.z, v.z, d[0].z, d[1].z);
+      d[0].z = w.x, d[1].z = w.y;
+      w = swiglu_grad2_far(g.w, u.w, v.w, d[0].w, d[1].w);
+      d[0].w = w.x, d[1].w = w.y;
+      finish(d, inside && row < p.M);
     }
   }
 }

@@ -106,3 +106,21 @@ def test_many_rows_sampled():
     ref, mag = train.swiglu_backward(to_host(h[rows]), to_host(dv[rows]), I)
     check_near(to_host(dh[rows]), ref, mag, 24, BF16_HALF, "dh")
     check_codes(q[rows], s[:, rows].contiguous(), bits_of(dh[rows]), True, "dh")
+
+
+@pytest.mark.parametrize("M,I,share", [(3000, 128, 1e-3), (2500, 1408, 1e-4), (1500, 4224, 1e-5), (700, 2048, 0.5), (1300, 384, 1e-3)])
+def test_gates_far_below_here_and_there(M, I, share):
+    """Gates below -64 in some rows, and in rows without a token, change no bit of the others."""
+    torch, fp8bs = require_gpu()
+    rng = np.random.default_rng(M)
+    h, dv = synth.normal_bf16((M, 2 * I), 2.0, 64, 5), synth.normal_bf16((M, I), 1.0, 65, 4)
+    live = np.where(rng.random(M) < 0.1, -1, 0).astype(np.int32)
+    far = np.zeros((M, 2 * I), bool)
+    far[:, :I] = rng.random((M, I)) < share
+    far[0, 0] = far[-1, I - 1] = True
+    wild = h.copy()
+    wild[far] = bf16_of(-np.exp(rng.uniform(np.log(64.5), np.log(150.0), int(far.sum()))).astype(np.float32))
+    with_far = _check(wild, dv, I, bool(M % 2), live)
+    _, _, without = fp8bs.swiglu_backward_quantize(to_dev_bf16(h), to_dev_bf16(dv), to_dev(live), True, bf16=True)
+    both = np.concatenate([far[:, :I], far[:, :I]], axis=1)
+    assert np.array_equal(bits_of(with_far)[~both], bits_of(without)[~both])
