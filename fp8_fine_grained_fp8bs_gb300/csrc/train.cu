@@ -12,6 +12,7 @@
 // the others straight into registers.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "group_quant.cuh"
@@ -73,16 +74,13 @@ struct Divisors<true> {
   __device__ __forceinline__ Divisor of(uint32_t a16) const { return pow2_divisor_bits(a16); }
 };
 
-// The general way out of line, for a kernel that quantises at many places.
-__device__ __noinline__ uint2 quant8m_call(const uint4 v, const Divisor d) { return quant8m(v, d); }
-
 // Eight BF16 values of a group with maximum a16 (BF16 bits) -> eight codes; the
 // scale.  A power of two: with e the biased exponent of the smallest power of two
 // times 1.75 that is at least the maximum (31 carries where the 7 bits of its
 // fraction exceed 96, those of 1.75), s = 2^(e - 135).  The quotient is then one
 // exact product, which keeps the sign of a zero.  Groups whose scale or its
 // reciprocal is not a normal number, zeros among them, take the general way.
-template <bool kPow2, bool kCall = false>
+template <bool kPow2>
 __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
@@ -99,7 +97,7 @@ __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const D
     }
   }
   const Divisor d = divisors.of(a16);
-  codes = kCall ? quant8m_call(v, d) : quant8m(v, d);
+  codes = quant8m(v, d);
   return d.s;
 }
 
@@ -129,7 +127,7 @@ __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, 
       return __uint_as_float((e - 8u) << 23);
     }
   }
-  return quantise8<kPow2, true>(times8(a, w), a16, divisors, codes);
+  return quantise8<kPow2>(times8(a, w), a16, divisors, codes);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -593,15 +591,18 @@ constexpr int kCbZeroRows = 8;    // rows that a warp looks over at a time for t
 // comes from L1 but once.  max |BF16(w x)| over a group is BF16(|w| max |x|), since
 // both roundings are monotonic, so the maximum is taken of dout, for two groups in
 // one word.  Behind the slots, warps zero the rows without a token.  8192 tokens of
-// 8 rows x 7168 take 281 us (1.54 GB, 0.81 of the copy bandwidth), half of the stalls
-// waits for loads, 64% of the issue slots; a CTA per token took 371, a ring filled by
-// a copying warp 352, prefetches into L2 288 to 344, 3 or 5 CTAs an SM 350.  509 tokens
-// 11.3 us; one token 5.2, its slots shared (13 with a warp each).
+// 8 rows x 7168 take 251 us (1.54 GB, 0.91 of the copy bandwidth), next bound by loads
+// waited for and instructions.  A CTA per token took 371, a ring filled by a copying
+// warp 352; with the warp's number not known to be uniform (pointers in vector
+// registers, spills) 281, with bounds checks on every piece 260; prefetches into L2
+// 272, five CTAs an SM 265 to 332.  509 tokens 10.3 us; one token 5.2, its slots
+// shared (13 with a warp each).
 template <bool kPow2, bool kShared>
 __global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(const CombineBackwardParams p) {
   __shared__ float s_dot[kCbWarps];
   __shared__ Divisors<kPow2> divisors;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // uniform, and known to be: rows and slots are a warp's
   const int nv = static_cast<int>(p.N / 8);
   constexpr int kApart = 32 * (kShared ? kCbWarps : 1);   // between a lane's pieces
   const int64_t slots = p.T * p.k;
@@ -639,21 +640,20 @@ __global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(cons
     if (dots || write) {
       const int v_first = (kShared ? 32 * warp : 0) + lane;
       const uint4* px = reinterpret_cast<const uint4*>(p.dout + t * p.ldo) + v_first;
-      const uint4* py = reinterpret_cast<const uint4*>(p.y + r * p.N) + v_first;
-      uint8_t* qo = p.q + r * p.N + 8 * v_first;
-      uint16_t* yo = p.dy + r * p.N + 8 * v_first;
+      int64_t at = r * p.N + 8 * v_first;      // in y, q and dy
       float* so = p.s + static_cast<int64_t>(v_first >> 4) * p.rows + r;
       const int64_t s_step = kApart / 16 * p.rows;
-      // whole warps go through the loop together (half-warp maxima)
-      for (int v0 = v_first - lane; v0 < nv; v0 += kCbUnroll * kApart) {
-        const int v = v0 + lane;
+      // kCbUnroll pieces a lane from piece v on, `all` where the row has them; whole
+      // warps come here together (half-warp maxima)
+      auto pieces = [&](auto all, int v) {
+        constexpr bool kAll = decltype(all)::value;
         uint4 x[kCbUnroll], y[kCbUnroll];
 #pragma unroll
         for (int i = 0; i < kCbUnroll; ++i) {
           x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (v + i * kApart >= nv) continue;
+          if (!kAll && v + i * kApart >= nv) continue;
           x[i] = __ldg(px + i * kApart);
-          if (dots) y[i] = __ldg(py + i * kApart);
+          if (dots) y[i] = __ldg(reinterpret_cast<const uint4*>(p.y + at) + i * kApart);
         }
         uint32_t top[kCbUnroll / 2];
         if (p.q != nullptr) {
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(cons
         }
 #pragma unroll
         for (int i = 0; i < kCbUnroll; ++i) {
-          if (v + i * kApart >= nv) continue;
+          if (!kAll && v + i * kApart >= nv) continue;
           float2 a[4];
           widen8x2(x[i], a);
           if (dots) {
@@ -676,22 +676,23 @@ __global__ void __launch_bounds__(32 * kCbWarps, 4) combine_backward_kernel(cons
             for (int e = 0; e < 4; ++e) dot[i] = __ffma2_rn(a[e], b[e], dot[i]);
           }
           if (!write) continue;
-          if (p.dy != nullptr) *reinterpret_cast<uint4*>(yo + 8 * i * kApart) = times8(a, w);
+          if (p.dy != nullptr) *reinterpret_cast<uint4*>(p.dy + at + 8 * i * kApart) = times8(a, w);
           if (p.q != nullptr) {
             const uint32_t top16 = i & 1 ? top[i / 2] & 0xFFFF0000u : top[i / 2] << 16;
             const uint32_t a16 = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(top16) * fabsf(w)));
             uint2 codes;
             const float s = quantise8_times<kPow2>(a, w, a16, divisors, codes);
-            *reinterpret_cast<uint2*>(qo + 8 * i * kApart) = codes;
+            *reinterpret_cast<uint2*>(p.q + at + 8 * i * kApart) = codes;
             if ((lane & 15) == 0) so[i * s_step] = s;
           }
         }
         px += kCbUnroll * kApart;
-        py += kCbUnroll * kApart;
-        qo += 8 * kCbUnroll * kApart;
-        yo += 8 * kCbUnroll * kApart;
+        at += 8 * kCbUnroll * kApart;
         so += kCbUnroll * s_step;
-      }
+      };
+      int v0 = v_first - lane;
+      for (; v0 + (kCbUnroll - 1) * kApart + 32 <= nv; v0 += kCbUnroll * kApart) pieces(std::true_type{}, v0 + lane);
+      for (; v0 < nv; v0 += kCbUnroll * kApart) pieces(std::false_type{}, v0 + lane);
     }
     if (p.dw == nullptr) continue;
     float sum = 0.0f;
