@@ -216,11 +216,11 @@ __device__ __forceinline__ uint32_t ue8m0_x4(const float (&s)[4], uint32_t& bad)
 // kSegK: the weight gradients of the experts.  A [M][K] and B [N][K] hold all
 // experts' rows along K (p.nkb blocks in all), group g those of its segment, and
 // D is [groups][M][N]; every role takes a tile's k-blocks from seg_tile.  A pair's
-// 256x256 tile takes 2.6 us per 1024 rows, the MMAs at their
-// full rate, plus 1.6 us in float32 and 0.7 in BF16, near the time in which the SM's
-// port to the crossbar takes the tile's stores (8 experts [4096][7168] of 2048 rows:
-// 341 and 297 us; of 1024: 215 and 171).  A second accumulator (256x192 tiles) does
-// not hide it: 364.
+// 256x256 tile takes 2.6 us per 1024 rows, the MMAs at their full rate, plus 1.6 us in
+// float32 and 0.7 in BF16 for its stores (8 experts [4096][7168] of 2048 rows: 342 and
+// 297 us; of 1024: 215 and 171).  A second accumulator (256x192 tiles, 364 us), a sixth
+// stage (339) or stores spread over the tile (343) do not hide them: the clock falls
+// with the power that both draw.
 template <int BN, bool kRowScale, bool kGrouped, bool kPair, bool kSegK = false>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
