@@ -306,6 +306,18 @@ class Fp8Saved(NamedTuple):
     y: object              # the experts' outputs
 
 
+def _check_weights(name, weights, shape):
+    """Codes [E, N, K] and scales [E, N/128, K/128] as the products read them, which see pointers only."""
+    import torch
+    from . import _checked, _on_one_device
+    E, N, K = shape
+    codes, scales = weights
+    if (tuple(_checked(codes, f"{name}: codes", (torch.uint8,), 3).shape) != shape
+            or tuple(_checked(scales, f"{name}: scales", (torch.float32,), 3).shape) != (E, N // 128, K // 128)):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)}, expected {shape} and one per 128 x 128")
+    _on_one_device(codes, scales)
+
+
 def moe_layer_fp8(xq, sx, logits, experts: Fp8Experts, k: int, score: int = 0, bias=None, valid=None, scale: float = 1.0,
                   seq=None, alpha: float | None = None):
     """One MoE layer with 8-bit experts on one rank: xq [T, H] E4M3 codes and sx [H/128, T] their
@@ -313,7 +325,8 @@ def moe_layer_fp8(xq, sx, logits, experts: Fp8Experts, k: int, score: int = 0, b
     the router's product), experts from quantize_experts_fp8.  Returns (out [T, H] bfloat16, saved): saved
     goes to moe_layer_fp8_backward; saved.route is moe_route's result, with ``alpha`` the balance loss in it.
     Every launch is on the current stream; nothing is read back."""
-    from . import grouped_gemm, moe_layout, moe_route, swiglu_quantize
+    import torch
+    from . import _checked, _on_one_device, grouped_gemm, moe_layout, moe_route, swiglu_quantize
     if xq.dim() != 2 or logits.dim() != 2 or xq.shape[0] != logits.shape[0]:
         raise ValueError(f"xq {tuple(xq.shape)} and logits {tuple(logits.shape)}: one row per token each")
     if tuple(sx.shape) != (xq.shape[1] // 128, xq.shape[0]):
@@ -322,6 +335,11 @@ def moe_layer_fp8(xq, sx, logits, experts: Fp8Experts, k: int, score: int = 0, b
     if logits.shape[1] != E or xq.shape[1] != H or tuple(experts.down[0].shape) != (E, H, two_i // 2):
         raise ValueError(f"xq {tuple(xq.shape)}, logits {tuple(logits.shape)} and experts "
                          f"{tuple(experts.gate_up[0].shape)}, {tuple(experts.down[0].shape)} do not fit")
+    _checked(xq, "xq", (torch.uint8,), 2)
+    _checked(sx, "sx", (torch.float32,), 2)
+    _on_one_device(xq, sx, logits)
+    _check_weights("experts.gate_up", experts.gate_up, (E, two_i, H))
+    _check_weights("experts.down", experts.down, (E, H, two_i // 2))
     routing = dict(score=score, valid=valid, seq=seq, scale=scale)
     route = moe_route(logits, k, bias=bias, alpha=alpha, **routing)
     layout = offsets, row_token, row_of = moe_layout(route[0], E)
@@ -341,8 +359,8 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     group that are not zeros but all below 448 * 2^-127 have no scale that the products take (the device status
     reports it): scale the loss."""
     import torch
-    from . import (grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward, moe_route_backward,
-                   requant_1x128_to_128x1, swiglu_backward_quantize)
+    from . import (grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward,
+                   moe_route_backward, requant_1x128_to_128x1, swiglu_backward_quantize)
     if experts.gate_up_t is None:
         raise ValueError("experts: quantised for serving only, without their transposed copies")
     idx, w, *stats = saved.route
@@ -352,8 +370,12 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     for name, out, shape in (("dw_gate_up", dw_gate_up, (E, two_i, H)), ("dw_down", dw_down, (E, H, two_i // 2))):
         if out is not None and (tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous()):
             raise ValueError(f"{name}: expected a contiguous float32 tensor {shape}")     # before either is added to
+    _check_weights("experts.gate_up_t", experts.gate_up_t, (E, H, two_i))
+    _check_weights("experts.down_t", experts.down_t, (E, two_i // 2, H))
     offsets, row_token, row_of = saved.layout
     dyq, sdy, _, dw = moe_combine_backward(dout, saved.y, row_of, row_token, w, pow2=True)
+    counts, tokens = stats[:2] if stats else (None, None)
+    dlogits = moe_route_backward(saved.logits, idx, dw, counts=counts, tokens=tokens, dloss=dloss, **saved.routing)
     dv = grouped_gemm(dyq, sdy, offsets, *experts.down_t, pow2=True)
     dhq, sdh, _ = swiglu_backward_quantize(saved.h, dv, row_token, pow2=True)
     drows = grouped_gemm(dhq, sdh, offsets, *experts.gate_up_t, pow2=True)
@@ -365,6 +387,4 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
 
     dw_down = weights((dyq, sdy), saved.v, dw_down)
     dw_gate_up = weights((dhq, sdh), saved.x, dw_gate_up)
-    counts, tokens = stats[:2] if stats else (None, None)
-    dlogits = moe_route_backward(saved.logits, idx, dw, counts=counts, tokens=tokens, dloss=dloss, **saved.routing)
     return dx, dlogits, dw_gate_up, dw_down

@@ -117,3 +117,26 @@ def test_layer_refusals(launched):  # noqa: F811
         with pytest.raises(ValueError):
             moe.quantize_experts_fp8(w, zeros((E, H, I), BF16))
     assert launched == []
+
+
+def test_layer_refuses_what_the_products_could_not_read(launched):  # noqa: F811
+    """Codes and scales of another type, layout or size, which the C entry points see as pointers."""
+    from fp8_fine_grained_fp8bs_gb300 import moe
+    T, E, H, I = 6, 4, 384, 128
+    one = lambda n, k: (zeros((E, n, k), U8), zeros((E, n // 128, k // 128), F32))  # noqa: E731
+    experts = moe.Fp8Experts(one(2 * I, H), one(H, I), one(H, 2 * I), one(I, H))
+    good = dict(xq=zeros((T, H), U8), sx=zeros((H // 128, T), F32), logits=zeros((T, E), F32), experts=experts, k=2)
+    up, down = experts.gate_up, experts.down
+    for bad in (dict(xq=zeros((T, H), torch.int8)), dict(xq=claim(torch.zeros((H, T), dtype=U8).t())),
+                dict(sx=zeros((H // 128, T), torch.float64)), dict(sx=claim(torch.zeros((T, H // 128)).t())), dict(xq=torch.zeros((T, H), dtype=U8)),
+                dict(experts=experts._replace(gate_up=(up[0], zeros((E, 3, 2), F32)))),
+                dict(experts=experts._replace(gate_up=(up[0], torch.zeros((E, 2, 3))))),
+                dict(experts=experts._replace(down=(down[0].to(torch.int32), down[1]))),
+                dict(experts=experts._replace(down=(down[0], zeros((E, 1, 3), F32))))):
+        with pytest.raises(ValueError):
+            moe.moe_layer_fp8(**{**good, **bad})
+    saved = moe.Fp8Saved(good["logits"], (zeros((T, 2), I32), zeros((T, 2), F32)), {}, None, None, None, None, None)
+    for bad in (dict(gate_up_t=one(2 * I, H)), dict(down_t=one(H, I)), dict(down_t=(experts.down_t[0], zeros((E, 1, 1), F32)))):
+        with pytest.raises(ValueError):
+            moe.moe_layer_fp8_backward(zeros((T, H), BF16), saved, experts._replace(**bad))
+    assert launched == []
