@@ -424,8 +424,8 @@ struct NormBackwardParams {
 // registers over the CTA's rows.  The rows (dy, r and dres) come by bulk copies
 // into a ring of stages that the next rows fill while one is worked on; both
 // passes over a row read it from there.  Bound by memory: [16384][7168] with dres
-// takes 140 us and the sums over CTAs 9 (940 MB, 0.93 of the copy bandwidth; with
-// loads straight into registers 260), [16384][1024] 28.6, [509][1984] 7.6, where the
+// takes 143 us and the gain's gradient 4 more (940 MB, 0.94 of the copy bandwidth; with
+// loads straight into registers 260), [16384][1024] 27.3, [509][1984] 5.9, where the
 // two launches' latency counts.
 template <int kVecs, bool kGainF32>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const NormBackwardParams p) {
@@ -541,27 +541,43 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
   }
 }
 
-// The gain's gradient: the CTAs' partial sums added up, 32 columns a CTA, each of its
-// warps every 32nd part, in a fixed order.  304 parts of 7168 columns take about 9 us.
-constexpr int kGainWarps = 32;
-__global__ void __launch_bounds__(32 * kGainWarps) norm_gain_kernel(const float* part, int parts, int K, float* dgain,
-                                                                    int accumulate) {
-  __shared__ float s_sum[kGainWarps][32];
+// The gain's gradient: the CTAs' partial sums added up, 32 columns a CTA, each group of
+// eight lanes every 32nd part, all of its loads in flight, in a fixed order.  Small CTAs
+// find room beside those of the gradient and wait there.  304 parts of 7168 columns take
+// about 4 us behind it, 255 of 1984 3.1 (in a loop without the loads in flight 5.6 and 4.9).
+constexpr int kMaxParts = 304;
+constexpr int kGainThreads = 256;
+__global__ void __launch_bounds__(kGainThreads) norm_gain_kernel(const float* part, int parts, int K, float* dgain,
+                                                                 int accumulate) {
+  constexpr int kGroups = kGainThreads / 8;   // of eight lanes, four columns each
+  __shared__ float4 s_sum[kGroups][8];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float sum = 0.0f;
-  if (c < K) {
-#pragma unroll 10
-    for (int i = warp; i < parts; i += kGainWarps) sum += part[static_cast<int64_t>(i) * K + c];
-  }
-  s_sum[warp][lane] = sum;
-  __syncthreads();
-  if (warp != 0 || c >= K) return;
+  const int group = threadIdx.x >> 3, at = threadIdx.x & 7;
+  const int c = blockIdx.x * 32 + 4 * at;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[(kMaxParts + kGroups - 1) / kGroups];
+  const float4* p = reinterpret_cast<const float4*>(part + c);
 #pragma unroll
-  for (int i = 1; i < kGainWarps; ++i) sum += s_sum[i][lane];
-  dgain[c] = accumulate ? dgain[c] + sum : sum;
+  for (int j = 0; j < (kMaxParts + kGroups - 1) / kGroups; ++j) {
+    const int i = group + j * kGroups;
+    v[j] = c < K && i < parts ? p[static_cast<int64_t>(i) * (K / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+#pragma unroll
+  for (int j = 0; j < (kMaxParts + kGroups - 1) / kGroups; ++j) {
+    sum.x += v[j].x;
+    sum.y += v[j].y;
+    sum.z += v[j].z;
+    sum.w += v[j].w;
+  }
+  s_sum[group][at] = sum;
+  __syncthreads();
+  const int mine = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || mine >= K) return;
+  const float* col = reinterpret_cast<const float*>(s_sum) + threadIdx.x;
+  float total = col[0];
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) total += col[32 * i];
+  dgain[mine] = accumulate ? dgain[mine] + total : total;
 }
 
 // ------------------------------------------------------ combine's gradient
@@ -962,7 +978,7 @@ NormBackwardPlan plan_norm_backward(int64_t M, int64_t K, bool dres) {
   n.stage_bytes = static_cast<int>((dres ? 3 : 2) * n.at.rows * K * 2);
   const bool two = 12 * n.at.rows * K <= kRingBytes;   // two stages of three arrays, with or without dres
   n.stages = std::min(kRingMaxStages, (two ? kRingBytes : kRingMaxBytes) / n.stage_bytes);
-  n.grid = static_cast<int>(std::min<int64_t>((M + n.at.rows - 1) / n.at.rows, two ? 304 : 152));
+  n.grid = static_cast<int>(std::min<int64_t>((M + n.at.rows - 1) / n.at.rows, two ? kMaxParts : kMaxParts / 2));
   return n;
 }
 
@@ -1012,7 +1028,7 @@ cudaError_t launch_rmsnorm_backward(const NormBackwardArgs& a, void* ws, cudaStr
                         : n.at.vecs == 2 ? (a.gain_f32 ? run_norm_backward<2, true>(p, n, stream) : run_norm_backward<2, false>(p, n, stream))
                                          : (a.gain_f32 ? run_norm_backward<1, true>(p, n, stream) : run_norm_backward<1, false>(p, n, stream));
   if (e != cudaSuccess || a.dgain == nullptr) return e;
-  return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), 32 * kGainWarps, stream,
+  return launch_behind(norm_gain_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), kGainThreads, stream,
                        static_cast<const float*>(p.part), n.grid, p.K, a.dgain, a.accumulate ? 1 : 0);
 }
 
