@@ -947,10 +947,24 @@ cudaError_t resident_ctas(Kern kern, int threads, int sm_count, std::atomic<int>
   return e;
 }
 
+// Lets `kern` take a ring's shared memory, once per device (the call costs 0.3 us).
+template <typename Kern>
+cudaError_t allow_ring(Kern kern, std::atomic<int> (&cache)[kMaxCachedDevices]) {
+  int done = 0;
+  return cached_per_device(
+      cache,
+      [&](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
+      },
+      &done);
+}
+
 template <int kVecs, bool kGainF32, bool kPow2>
 cudaError_t run_norm(const NormParams& p, int grid, int threads, int smem, cudaStream_t stream) {
   auto kern = p.res != nullptr ? norm_kernel<kVecs, kGainF32, kPow2, true> : norm_kernel<kVecs, kGainF32, kPow2, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
+  static std::atomic<int> cache[2][kMaxCachedDevices];
+  const cudaError_t e = allow_ring(kern, cache[p.res != nullptr ? 1 : 0]);
   if (e != cudaSuccess) return e;
   return launch_behind_smem(kern, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(threads), static_cast<size_t>(smem),
                             stream, p);
@@ -986,7 +1000,8 @@ template <int kVecs, bool kGainF32>
 cudaError_t run_norm_backward(const NormBackwardParams& p, const NormBackwardPlan& n, cudaStream_t stream) {
   auto kern = norm_backward_kernel<kVecs, kGainF32>;
   const int smem = n.stages * n.stage_bytes;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes);
+  static std::atomic<int> cache[kMaxCachedDevices];
+  const cudaError_t e = allow_ring(kern, cache);
   if (e != cudaSuccess) return e;
   return launch_behind_smem(kern, dim3(static_cast<unsigned>(n.grid)), static_cast<unsigned>(32 * n.at.warps * n.at.rows),
                             static_cast<size_t>(smem), stream, p);
