@@ -818,18 +818,18 @@ __device__ __forceinline__ bool any_far_gate(const uint4& g) {
   return (m >> 16) > kFarGate || (m & 0xFFFFu) > kFarGate;
 }
 
-constexpr int kSbThreads = 256;   // or as many as a row has pieces, up to 512
+constexpr int kSbThreads = 512;   // of a CTA, at most
 
 // Thread = eight columns of one half of h: the columns stay, the rows advance by
 // the grid, with the next row's loads in flight.  A group of 128 is a half-warp's
 // 16 threads; whole warps go through the loop together.  Rows with a gate below -64
 // among a warp's are left out and done in a second pass, which rarely has any: with
 // their call inside the loop the results went through local memory, and [67712][2048]
-// took 190 to 228 us as that memory fell; now 178 (1.12 GB, 0.92 of the copy
+// took 190 to 228 us as that memory fell; now 174 (1.12 GB, 0.94 of the copy
 // bandwidth).  Bound by instructions next (three quarters of the issue slots); by a
 // ring of bulk copies 245, unpacked with expf 325.
 template <bool kPow2>
-__global__ void __launch_bounds__(512) swiglu_backward_kernel(const SwigluBackwardParams p) {
+__global__ void __launch_bounds__(kSbThreads) swiglu_backward_kernel(const SwigluBackwardParams p) {
   __shared__ Divisors<kPow2> divisors;
   divisors.init();
   __syncthreads();
@@ -1072,9 +1072,14 @@ cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cu
   p.h = a.h; p.dv = a.dv; p.live = a.live; p.M = a.M; p.I = a.I; p.ldh = a.ldh; p.lddv = a.lddv;
   p.dh = a.dh; p.q = a.q; p.s = a.s;
   const int upr = static_cast<int>(a.I / 8);
-  // short rows share a CTA; longer ones take one of their own size, above 512 pieces 256 threads in steps
-  p.rows = std::max(1, kSbThreads / upr);
-  const int threads = upr > 512 ? kSbThreads : (p.rows * upr + 31) / 32 * 32;
+  // Rows share a CTA of 512 threads, or of 256 where there are few rows or short ones
+  // ([67712][2048] 174 us with 512, 178 with 256; [64][2048] 2.4 and 2.1, [312500][128] 57.0
+  // and 56.2).  Rows of more than 512 pieces take equal steps of at most as many ([9470][4224]
+  // 61 us, in steps of 256 with a short last one 74).
+  const int halves = upr >= 64 && a.M >= 2 * static_cast<int64_t>(sm_count) * std::max(1, kSbThreads / upr) ? 1 : 2;
+  p.rows = std::max(1, kSbThreads / halves / upr);
+  const int steps = (upr + kSbThreads - 1) / kSbThreads;
+  const int threads = ((steps > 1 ? (upr + steps - 1) / steps : p.rows * upr) + 31) / 32 * 32;
   auto kern = a.pow2 ? swiglu_backward_kernel<true> : swiglu_backward_kernel<false>;
   static std::atomic<int> cache[2][17][kMaxCachedDevices];
   int64_t slots = 0;
