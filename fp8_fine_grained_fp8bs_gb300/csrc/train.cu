@@ -203,7 +203,9 @@ struct Gain<true> {
 
 // The ring of a CTA: step i is the CTA's rows (i * CTAs + CTA) * rows and on, of up to
 // three matrices, copied row by row into stage i % stages, one lane of warp 0 per row
-// and matrix.  Steps are issued in order and taken in order.
+// and matrix (kMany: they may be more than 32).  Steps are issued in order and taken in
+// order.
+template <bool kMany>
 struct RowRing {
   uint8_t* base;
   uint64_t* full;
@@ -240,10 +242,11 @@ struct RowRing {
     const int lane = threadIdx.x;
     if (lane == 0) mbar_arrive_expect_tx(&full[in], arrays * n * row_bytes);
     __syncwarp();
-    if (lane < arrays * n) {
-      const int which = lane >= 2 * n ? 2 : lane >= n ? 1 : 0, i = lane - which * n;
+    for (int at = lane; at < arrays * n; at += 32) {
+      const int which = at >= 2 * n ? 2 : at >= n ? 1 : 0, i = at - which * n;
       const uint16_t* from = which == 0 ? src[0] + (in_row + i) * ld[0] : which == 1 ? src[1] + (in_row + i) * ld[1] : src[2] + (in_row + i) * ld[2];
       bulk_load(base + in * stage_bytes + which * array_bytes + i * row_bytes, from, row_bytes, &full[in]);
+      if (!kMany) break;
     }
     __syncwarp();
     ++issued;
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormParams 
   const int nv = p.K / 8;
   constexpr int arrays = kRes ? 2 : 1;
   const int rows = blockDim.x / T;
-  RowRing rr(ring, full, p.K, rows, arrays, p.stages, p.M);
+  RowRing<false> rr(ring, full, p.K, rows, arrays, p.stages, p.M);
   const uint16_t* const src[3] = {p.x, p.res, nullptr};
   const int64_t ld[3] = {p.ldx, p.ldr, 0};
   __shared__ Divisors<kPow2> divisors;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const No
   const int rows = blockDim.x / T;
   const int nv = p.K / 8;
   const int arrays = p.dres != nullptr ? 3 : 2;
-  RowRing rr(ring, full, p.K, rows, arrays, p.stages, p.M);
+  RowRing<kVecs == 1> rr(ring, full, p.K, rows, arrays, p.stages, p.M);
   const uint16_t* const src[3] = {p.dy, p.r, p.dres};
   const int64_t ld[3] = {p.lddy, p.ldr, p.lddres};
   rr.init();
@@ -989,6 +992,11 @@ struct NormBackwardPlan {
 NormBackwardPlan plan_norm_backward(int64_t M, int64_t K, bool dres) {
   NormBackwardPlan n;
   n.at = place_rows(static_cast<int>(K), 256);
+  // At least eight warps a CTA, sixteen for short rows, where four stages hold their rows:
+  // [65536][128] 39 us (51 with eight warps), [16384][512] 17.9 (24.6), [16384][1536] 37.3
+  // (43.6 with six).
+  const int target = K <= 512 ? 16 : 8, rows = (target + n.at.warps - 1) / n.at.warps;
+  if (kRingMaxStages * 6 * rows * K <= kRingBytes) n.at.rows = rows;
   n.stage_bytes = static_cast<int>((dres ? 3 : 2) * n.at.rows * K * 2);
   const bool two = 12 * n.at.rows * K <= kRingBytes;   // two stages of three arrays, with or without dres
   n.stages = std::min(kRingMaxStages, (two ? kRingBytes : kRingMaxBytes) / n.stage_bytes);
