@@ -992,11 +992,12 @@ struct NormBackwardPlan {
 NormBackwardPlan plan_norm_backward(int64_t M, int64_t K, bool dres) {
   NormBackwardPlan n;
   n.at = place_rows(static_cast<int>(K), 256);
-  // At least eight warps a CTA, sixteen for short rows, where four stages hold their rows:
+  // At least eight warps a CTA, sixteen for short rows, where four stages hold their rows
+  // and no CTA stays without any:
   // [65536][128] 39 us (51 with eight warps), [16384][512] 17.9 (24.6), [16384][1536] 37.3
   // (43.6 with six).
   const int target = K <= 512 ? 16 : 8, rows = (target + n.at.warps - 1) / n.at.warps;
-  if (kRingMaxStages * 6 * rows * K <= kRingBytes) n.at.rows = rows;
+  if (kRingMaxStages * 6 * rows * K <= kRingBytes && M >= int64_t{kMaxParts} * rows) n.at.rows = rows;
   n.stage_bytes = static_cast<int>((dres ? 3 : 2) * n.at.rows * K * 2);
   const bool two = 12 * n.at.rows * K <= kRingBytes;   // two stages of three arrays, with or without dres
   n.stages = std::min(kRingMaxStages, (two ? kRingBytes : kRingMaxBytes) / n.stage_bytes);
