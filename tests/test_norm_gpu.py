@@ -127,6 +127,13 @@ def test_gradient(M, K, kind, dres):
     assert same is held and torch.equal(held, dgain + 0.5)
 
 
+@pytest.mark.parametrize("M,K", [(4864, 8), (5003, 128), (9001, 264), (4871, 512), (4865, 504), (1000, 1536), (911, 1536), (912, 1160)])
+@pytest.mark.parametrize("kind,dres", [("bf16", True), ("f32", False)])
+def test_gradient_of_many_short_rows(M, K, kind, dres):
+    """More rows share a CTA there; up to 16 sums of a row's threads then stand in for as many of its rows."""
+    test_gradient(M, K, kind, dres)
+
+
 def test_gradient_in_place_strided_and_without_the_gain():
     torch, fp8bs = require_gpu()
     M, K, wide = 61, 512, 520
