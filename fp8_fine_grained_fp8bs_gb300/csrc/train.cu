@@ -79,12 +79,14 @@ struct Divisors<true> {
 // times 1.75 that is at least the maximum (31 carries where the 7 bits of its
 // fraction exceed 96, those of 1.75), s = 2^(e - 135).  The quotient is then one
 // exact product, which keeps the sign of a zero.  Groups whose scale or its
-// reciprocal is not a normal number, zeros among them, take the general way.
+// reciprocal is not a normal number, zeros among them, take the general way, and so
+// do maxima above 1.75 * 2^127: an infinity among the values has the code of no number
+// there, where a product with the conversion's saturation would make 448 of it.
 template <bool kPow2>
 __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
-    if (e >= 9u) {
+    if (e - 9u <= 254u - 9u) {
       const float y = __uint_as_float((262u - e) << 23);
       const float2 y2 = make_float2(y, y);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -113,14 +115,15 @@ __device__ __forceinline__ uint4 times8(const float2 (&a)[4], float w) {
 // quantise8 of the BF16 values of a * w.  Scaling by a power of two commutes with
 // rounding: the quotients are the BF16 values of a * (w / s), as long as those that
 // reach a code (|v / s| > 2^-10) are normal numbers, which s >= 2^-103 leaves them,
-// and w / s stays in range, which |w| < 2^24 does then.
+// w / s stays in range, which |w| < 2^24 does then, and no BF16 value of a * w is
+// infinite, since a * (w / s) would not be.
 constexpr float kPlainWeight = 16777216.0f;
 template <bool kPow2>
 __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, uint32_t a16, const Divisors<kPow2>& divisors,
                                                  uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
-    if (e >= 32u && fabsf(w) < kPlainWeight) {
+    if (e - 32u <= 254u - 32u && fabsf(w) < kPlainWeight) {
       float2 f[4];
       widen8x2(times8(a, w * __uint_as_float((262u - e) << 23)), f);
       codes = make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
