@@ -81,12 +81,13 @@ struct Divisors<true> {
 // exact product, which keeps the sign of a zero.  Groups whose scale or its
 // reciprocal is not a normal number, zeros among them, take the general way, and so
 // do maxima above 1.75 * 2^127: an infinity among the values has the code of no number
-// there, where a product with the conversion's saturation would make 448 of it.
-template <bool kPow2>
+// there, where a product with the conversion's saturation would make 448 of it
+// (kFinite: the caller knows of none).
+template <bool kPow2, bool kFinite = false>
 __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
   if (kPow2) {
     const uint32_t e = (a16 + 31u) >> 7;
-    if (e - 9u <= 254u - 9u) {
+    if (kFinite ? e >= 9u : e - 9u <= 254u - 9u) {
       const float y = __uint_as_float((262u - e) << 23);
       const float2 y2 = make_float2(y, y);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -755,6 +756,8 @@ struct SwigluBackwardParams {
   const int32_t* live;   // or NULL
   int64_t M, I, ldh, lddv;
   int rows;              // rows per CTA and step
+  uint32_t step;         // of the grid, in rows, and what that is in elements of h, dv and the outputs
+  int64_t step_h, step_v, step_out;
   uint16_t* dh;          // [M][2I] or NULL
   uint8_t* q;            // or NULL (with s)
   float* s;
@@ -796,46 +799,161 @@ __device__ __forceinline__ void swiglu_grad2(uint32_t gw, uint32_t uw, uint32_t 
   duw = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The same for the gates below -64 of a pair, where e^-g runs out of float32's range
-// in the end: sigma(g) = e^g to within 2^-92, applied as its root twice, once to the
-// larger factor, so that the product does not underflow on the way.  Words in which
-// no gate is that low come back as they are.
-constexpr uint32_t kFarGate = 0xC280u;   // BF16 of -64; patterns above it are below -64
-__device__ __noinline__ uint2 swiglu_grad2_far(uint32_t gw, uint32_t uw, uint32_t vw, uint32_t dgw, uint32_t duw) {
+// The same for what swiglu_grad2 cannot give of a pair: gates below -64, where e^-g
+// runs out of float32's range in the end (sigma(g) = e^g to within 2^-92), and
+// gradients that came out infinite, dv * up having left float32's range perhaps though
+// the gradient does not.  The exponents of dv, up and e^g = 2^n 2^f are kept apart until
+// the end, so that nothing overflows or vanishes on the way; below -512 e^g leaves nothing
+// of any dv and up.  The other values come back as they are.
+constexpr uint32_t kFarGate = 0xC280u;            // BF16 of -64; patterns above it are below -64
+constexpr float kLog2Hi = 1.44268798828125f;      // 23637 / 16384
+constexpr float kLog2Lo = 7.0526077e-06f;         // log2 e - kLog2Hi
+__device__ __noinline__ uint2 swiglu_grad2_wide(uint32_t gw, uint32_t uw, uint32_t vw, uint32_t dgw, uint32_t duw) {
   uint2 out = make_uint2(dgw, duw);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t gb = k ? gw >> 16 : gw & 0xFFFFu;
-    if (gb <= kFarGate) continue;
+    const bool far = gb > kFarGate;
+    const uint32_t high = k ? 0x7F800000u : 0x7F80u;   // the exponent's bits
+    if (!far && (dgw & high) != high && (duw & high) != high) continue;
     const float gate = __uint_as_float(gb << 16);
     const float up = __uint_as_float(k ? uw & 0xFFFF0000u : uw << 16);
     const float dv = __uint_as_float(k ? vw & 0xFFFF0000u : vw << 16);
-    const float root = expf(0.5f * gate);
-    const bool first = fabsf(dv) > fabsf(up);
-    const float dg = (first ? dv : up) * root * (first ? up : dv) * root * (1.0f + gate), du = dv * root * (gate * root);
-    const uint32_t a = __bfloat16_as_ushort(__float2bfloat16_rn(dg)), b = __bfloat16_as_ushort(__float2bfloat16_rn(du));
+    int ev, eu;
+    const float mv = frexpf(dv, &ev), mu = frexpf(up, &eu);
+    float dg, du;
+    if (far) {
+      const float t = fmaxf(gate, -512.0f) * kLog2Hi, n = rintf(t);    // both exact
+      const float s = exp2f(t - n + fmaxf(gate, -512.0f) * kLog2Lo);
+      const bool none = gate < -512.0f;
+      dg = ldexpf(mv * mu * (1.0f + gate) * (none ? 0.0f : s), ev + eu + static_cast<int>(n));
+      du = ldexpf(mv * gate * (none ? 0.0f : s), ev + static_cast<int>(n));
+    } else {
+      const float e = expf(-gate), s = 1.0f / (1.0f + e);
+      dg = ldexpf(mv * mu * (s * fmaf(gate, e * s, 1.0f)), ev + eu);
+      du = dv * (gate * s);
+    }
+    const uint32_t a = __bfloat16_as_ushort(__float2bfloat16_rn(dg));
+    const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(du));
     out.x = k ? (out.x & 0xFFFFu) | (a << 16) : (out.x & 0xFFFF0000u) | a;
     out.y = k ? (out.y & 0xFFFFu) | (b << 16) : (out.y & 0xFFFF0000u) | b;
   }
   return out;
 }
-__device__ __forceinline__ bool any_far_gate(const uint4& g) {
-  const uint32_t m = umax16x2(umax16x2(g.x, g.y), umax16x2(g.z, g.w));
-  return (m >> 16) > kFarGate || (m & 0xFFFFu) > kFarGate;
-}
 
 constexpr int kSbThreads = 512;   // of a CTA, at most
+
+__device__ __forceinline__ void swiglu_grad8(const uint4 (&in)[3], uint4 (&d)[2]) {
+  swiglu_grad2(in[0].x, in[1].x, in[2].x, d[0].x, d[1].x);
+  swiglu_grad2(in[0].y, in[1].y, in[2].y, d[0].y, d[1].y);
+  swiglu_grad2(in[0].z, in[1].z, in[2].z, d[0].z, d[1].z);
+  swiglu_grad2(in[0].w, in[1].w, in[2].w, d[0].w, d[1].w);
+}
+
+// What a thread writes, of row `row`, and reads, of the row to load next (at most 2^31 rows,
+// and a few of the grid's steps).
+struct SwigluPlace {
+  uint32_t row;
+  int64_t out;
+  float* ps;
+  const uint16_t* ph;
+  const uint16_t* pv;
+  __device__ __forceinline__ SwigluPlace(const SwigluBackwardParams& p, uint32_t row_, int c)
+      : row(row_), out(2 * p.I * row_ + 8 * c), ps(p.s == nullptr ? nullptr : p.s + static_cast<int64_t>(c >> 4) * p.M + row_),
+        ph(p.h + row_ * p.ldh + 8 * c), pv(p.dv + row_ * p.lddv + 8 * c) {}
+  __device__ __forceinline__ void move_on(const SwigluBackwardParams& p) {
+    row += p.step;
+    out += p.step_out;
+    ps += p.step;
+  }
+  __device__ __forceinline__ bool live(const SwigluBackwardParams& p, uint32_t ahead) const {
+    return row + ahead < p.M && (p.live == nullptr || __ldg(p.live + (row + ahead)) >= 0);
+  }
+  __device__ __forceinline__ void load(const SwigluBackwardParams& p, bool live, uint4 (&in)[3]) {
+    in[0] = in[1] = in[2] = make_uint4(0u, 0u, 0u, 0u);
+    if (live) {
+      in[0] = __ldg(reinterpret_cast<const uint4*>(ph));
+      in[1] = __ldg(reinterpret_cast<const uint4*>(ph + p.I));
+      in[2] = __ldg(reinterpret_cast<const uint4*>(pv));
+    }
+    ph += p.step_h;
+    pv += p.step_v;
+  }
+  // Quantises and stores the row's piece, `top` the halves' largest magnitudes in this
+  // thread; whole warps come here together.
+  template <bool kPow2, bool kFinite>
+  __device__ __forceinline__ void finish(const SwigluBackwardParams& p, const Divisors<kPow2>& divisors, const uint4 (&d)[2],
+                                         uint32_t top, bool first_of_group, bool here) const {
+    if (here && p.dh != nullptr) {
+      *reinterpret_cast<uint4*>(p.dh + out) = d[0];
+      *reinterpret_cast<uint4*>(p.dh + out + p.I) = d[1];
+    }
+    if (p.q == nullptr) return;
+#pragma unroll
+    for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint2 cg, cu;
+    const float sg = quantise8<kPow2, kFinite>(d[0], top & 0xFFFFu, divisors, cg);
+    const float su = quantise8<kPow2, kFinite>(d[1], top >> 16, divisors, cu);
+    if (!here) return;
+    *reinterpret_cast<uint2*>(p.q + out) = cg;
+    *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
+    if (first_of_group) {
+      ps[0] = sg;
+      ps[(p.I >> 7) * p.M] = su;
+    }
+  }
+};
+
+// Both halves' largest magnitudes of a thread in one word.
+__device__ __forceinline__ uint32_t swiglu_top(const uint4 (&d)[2]) {
+  return __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
+}
+// Whether pieces of rows need the second pass, by the largest of their gates' patterns and
+// of their gradients' magnitudes (in the halves of a word each): a gate below -64, or an
+// infinite gradient.
+__device__ __forceinline__ uint32_t top_gate(const uint4& g) { return umax16x2(umax16x2(g.x, g.y), umax16x2(g.z, g.w)); }
+__device__ __forceinline__ bool swiglu_again(uint32_t gate, uint32_t top) {
+  return (umax_halves(gate) & 0xFFFFu) > kFarGate || (umax_halves(top) & 0xFFFFu) >= 0x7F80u;
+}
+
+// The second pass over a warp's rows: those that need it, one at a time, written anew.
+template <bool kPow2>
+__device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, const Divisors<kPow2>& divisors, int sub, int c0,
+                                               int step_c) {
+  const int upr = static_cast<int>(p.I / 8);
+  for (int cc = 0; cc < upr; cc += step_c) {
+    const int c = c0 + cc;
+    const bool inside = sub < p.rows && c < upr;
+    SwigluPlace at(p, blockIdx.x * p.rows + sub, c);
+    for (; at.row - sub < p.M; at.move_on(p)) {
+      uint4 in[3], d[2];
+      at.load(p, inside && at.live(p, 0), in);
+      swiglu_grad8(in, d);
+      if (!__any_sync(0xffffffffu, swiglu_again(top_gate(in[0]), swiglu_top(d)))) continue;
+      uint2 w = swiglu_grad2_wide(in[0].x, in[1].x, in[2].x, d[0].x, d[1].x);
+      d[0].x = w.x, d[1].x = w.y;
+      w = swiglu_grad2_wide(in[0].y, in[1].y, in[2].y, d[0].y, d[1].y);
+      d[0].y = w.x, d[1].y = w.y;
+      w = swiglu_grad2_wide(in[0].z, in[1].z, in[2].z, d[0].z, d[1].z);
+      d[0].z = w.x, d[1].z = w.y;
+      w = swiglu_grad2_wide(in[0].w, in[1].w, in[2].w, d[0].w, d[1].w);
+      d[0].w = w.x, d[1].w = w.y;
+      at.finish<kPow2, false>(p, divisors, d, swiglu_top(d), (c & 15) == 0, inside && at.row < p.M);
+    }
+  }
+}
 
 // Thread = eight columns of one half of h: the columns stay, the rows advance by
 // the grid, with the next row's loads in flight.  A group of 128 is a half-warp's
 // 16 threads; whole warps go through the loop together.  Rows with a gate below -64
-// among a warp's are left out and done in a second pass, which rarely has any: with
-// their call inside the loop the results went through local memory, and [67712][2048]
-// took 190 to 228 us as that memory fell; now 174 (1.12 GB, 0.94 of the copy
-// bandwidth).  Bound by instructions next (three quarters of the issue slots); by a
-// ring of bulk copies 245, unpacked with expf 325.
+// or an infinite gradient are written anew in a second pass, which rarely has any: the
+// loop keeps the largest patterns of all rows, two instructions a row, and looks at
+// them once.  [67712][2048] takes 167 us (1.12 GB, the copy bandwidth); with a vote a
+// row, that kept such rows from being stored, 174 to 187, with a call inside the loop,
+// whose results went through local memory, 190 to 228.  With absmax scales 201, bound by
+// instructions; by a ring of bulk copies 245, unpacked with expf 325.
 template <bool kPow2>
-__global__ void __launch_bounds__(kSbThreads) swiglu_backward_kernel(const SwigluBackwardParams p) {
+__global__ void __launch_bounds__(kSbThreads, 2) swiglu_backward_kernel(const __grid_constant__ SwigluBackwardParams p) {
   __shared__ Divisors<kPow2> divisors;
   divisors.init();
   __syncthreads();
@@ -845,102 +963,30 @@ __global__ void __launch_bounds__(kSbThreads) swiglu_backward_kernel(const Swigl
   const int sub = whole ? threadIdx.x / upr : 0;
   const int step_c = whole ? upr : blockDim.x;        // rows longer than a CTA: in steps
   const int c0 = threadIdx.x - sub * upr;
-  const int64_t rstep = static_cast<int64_t>(gridDim.x) * p.rows;
   const bool mine = sub < p.rows;
+  uint32_t gates = 0u, tops = 0u;                     // the largest of all rows
   griddep_wait();
   for (int cc = 0; cc < upr; cc += step_c) {
     const int c = c0 + cc;
     const bool inside = mine && c < upr;
-    // what the thread reads and writes, moved on by the grid's rows
-    int64_t row = static_cast<int64_t>(blockIdx.x) * p.rows + sub;
-    const uint16_t* ph = p.h + row * p.ldh + 8 * c;
-    const uint16_t* pv = p.dv + row * p.lddv + 8 * c;
-    const int32_t* pl = p.live == nullptr ? nullptr : p.live + row;
-    int64_t out = row * 2 * p.I + 8 * c;
-    float* ps = p.s == nullptr ? nullptr : p.s + static_cast<int64_t>(c >> 4) * p.M + row;
-    const int64_t half_s = (p.I >> 7) * p.M;
-    auto row_live = [&](int64_t ahead) {
-      return inside && row + ahead < p.M && (pl == nullptr || __ldg(pl + ahead) >= 0);
-    };
+    SwigluPlace at(p, blockIdx.x * p.rows + sub, c);
     uint4 next[3];
-    auto load = [&](bool live, int64_t ahead) {
-      next[0] = next[1] = next[2] = make_uint4(0u, 0u, 0u, 0u);
-      if (!live) return;
-      const uint16_t* hr = ph + ahead * p.ldh;
-      next[0] = __ldg(reinterpret_cast<const uint4*>(hr));
-      next[1] = __ldg(reinterpret_cast<const uint4*>(hr + p.I));
-      next[2] = __ldg(reinterpret_cast<const uint4*>(pv + ahead * p.lddv));
-    };
-    // quantises and stores a row's piece; whole warps come here together
-    auto finish = [&](const uint4 (&d)[2], bool here) {
-      if (here && p.dh != nullptr) {
-        *reinterpret_cast<uint4*>(p.dh + out) = d[0];
-        *reinterpret_cast<uint4*>(p.dh + out + p.I) = d[1];
-      }
-      if (p.q == nullptr) return;
-      // both halves' maxima in one word
-      uint32_t top = __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
-#pragma unroll
-      for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
-      uint2 cg, cu;
-      const float sg = quantise8<kPow2>(d[0], top & 0xFFFFu, divisors, cg);
-      const float su = quantise8<kPow2>(d[1], top >> 16, divisors, cu);
-      if (!here) return;
-      *reinterpret_cast<uint2*>(p.q + out) = cg;
-      *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
-      if ((c & 15) == 0) {
-        ps[0] = sg;
-        ps[half_s] = su;
-      }
-    };
-    auto gradients = [&](const uint4& g, const uint4& u, const uint4& v, uint4 (&d)[2]) {
-      swiglu_grad2(g.x, u.x, v.x, d[0].x, d[1].x);
-      swiglu_grad2(g.y, u.y, v.y, d[0].y, d[1].y);
-      swiglu_grad2(g.z, u.z, v.z, d[0].z, d[1].z);
-      swiglu_grad2(g.w, u.w, v.w, d[0].w, d[1].w);
-    };
-    auto move_on = [&](int64_t rows) {
-      row += rows;
-      ph += rows * p.ldh;
-      pv += rows * p.lddv;
-      if (pl != nullptr) pl += rows;
-      out += rows * 2 * p.I;
-      ps += rows;
-    };
-    const int64_t start = static_cast<int64_t>(blockIdx.x) * p.rows;
-    bool far = false;                             // a gate of a row that the warp left out
-    load(row_live(0), 0);
-    bool live_after = row_live(rstep);            // a row ahead of the loads that wait for it
-    for (int64_t first = start; first < p.M; first += rstep) {
-      const uint4 g = next[0], u = next[1], v = next[2];
-      load(live_after, rstep);
-      live_after = row_live(2 * rstep);
-      const bool left_out = __any_sync(0xffffffffu, any_far_gate(g));
-      far = far || left_out;
+    at.load(p, inside && at.live(p, 0), next);
+    bool live_after = inside && at.live(p, p.step);   // a row ahead of the loads that wait for it
+    while (at.row - sub < p.M) {                  // as far as any of the CTA's rows goes
+      const uint4 in[3] = {next[0], next[1], next[2]};
+      at.load(p, live_after, next);
+      live_after = inside && at.live(p, 2 * p.step);
       uint4 d[2];
-      gradients(g, u, v, d);
-      finish(d, inside && row < p.M && !left_out);
-      move_on(rstep);
-    }
-    if (!far) continue;
-    for (int64_t first = start; first < p.M; first += rstep) {   // the rows left out, one at a time
-      move_on(first == start ? start + sub - row : rstep);
-      load(row_live(0), 0);
-      if (!__any_sync(0xffffffffu, any_far_gate(next[0]))) continue;
-      const uint4 g = next[0], u = next[1], v = next[2];
-      uint4 d[2];
-      gradients(g, u, v, d);
-      uint2 w = swiglu_grad2_far(g.x, u.x, v.x, d[0].x, d[1].x);
-      d[0].x = w.x, d[1].x = w.y;
-      w = swiglu_grad2_far(g.y, u.y, v.y, d[0].y, d[1].y);
-      d[0].y = w.x, d[1].y = w.y;
-      w = swiglu_grad2_far(g.z, u.z, v.z, d[0].z, d[1].z);
-      d[0].z = w.x, d[1].z = w.y;
-      w = swiglu_grad2_far(g.w, u.w, v.w, d[0].w, d[1].w);
-      d[0].w = w.x, d[1].w = w.y;
-      finish(d, inside && row < p.M);
+      swiglu_grad8(in, d);
+      const uint32_t top = swiglu_top(d);
+      gates = umax16x2(gates, top_gate(in[0]));
+      tops = umax16x2(tops, top);
+      at.finish<kPow2, true>(p, divisors, d, top, (c & 15) == 0, inside && at.row < p.M);
+      at.move_on(p);
     }
   }
+  if (__any_sync(0xffffffffu, swiglu_again(gates, tops))) swiglu_rows_again<kPow2>(p, divisors, sub, c0, step_c);
 }
 
 // CTAs of `kern` that fit on the device at once.
@@ -1097,8 +1143,12 @@ cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int sm_count, cu
   int64_t slots = 0;
   const cudaError_t e = resident_ctas(kern, threads, sm_count, cache[a.pow2 ? 1 : 0][threads / 32], &slots);
   if (e != cudaSuccess) return e;
-  const int64_t need = (p.M + p.rows - 1) / p.rows;
-  return launch_behind(kern, dim3(static_cast<unsigned>(std::min(need, slots))), threads, stream, p);
+  const int64_t grid = std::min((p.M + p.rows - 1) / p.rows, slots);
+  p.step = static_cast<uint32_t>(grid * p.rows);
+  p.step_h = p.step * p.ldh;
+  p.step_v = p.step * p.lddv;
+  p.step_out = 2 * p.I * p.step;
+  return launch_behind(kern, dim3(static_cast<unsigned>(grid)), threads, stream, p);
 }
 
 cudaError_t train_take_status(int* status) {
