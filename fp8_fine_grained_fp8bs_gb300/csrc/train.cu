@@ -801,8 +801,9 @@ __device__ __forceinline__ void swiglu_grad2(uint32_t gw, uint32_t uw, uint32_t 
 
 // The same for what swiglu_grad2 cannot give of a pair: gates below -64, where e^-g
 // runs out of float32's range in the end (sigma(g) = e^g to within 2^-92), and
-// gradients that came out infinite, dv * up having left float32's range perhaps though
-// the gradient does not.  The exponents of dv, up and e^g = 2^n 2^f are kept apart until
+// gradients that came out infinite or NaN, dv * up having left float32's range perhaps
+// though the gradient does not, or an infinite gate having made NaN of the exponential's
+// correction.  The exponents of dv, up and e^g = 2^n 2^f are kept apart until
 // the end, so that nothing overflows or vanishes on the way; below -512 e^g leaves nothing
 // of any dv and up.  The other values come back as they are.
 constexpr uint32_t kFarGate = 0xC280u;            // BF16 of -64; patterns above it are below -64
@@ -904,13 +905,25 @@ struct SwigluPlace {
   }
 };
 
-// Both halves' largest magnitudes of a thread in one word.
+// Both halves' largest magnitudes of a thread in one word; kNan: NaN where any value is.
+// Without it a number is larger than NaN, as in the quantisers.
+__device__ __forceinline__ uint32_t absmax_step_nan(uint32_t m, uint32_t w) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
+  return d;
+}
+template <bool kNan>
 __device__ __forceinline__ uint32_t swiglu_top(const uint4 (&d)[2]) {
-  return __byte_perm(umax_halves(absmax8_bits(d[0])), umax_halves(absmax8_bits(d[1])), 0x5410);
+  uint32_t m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    m[i] = kNan ? abs_bits(absmax_step_nan(absmax_step_nan(d[i].x, d[i].y), absmax_step_nan(d[i].z, d[i].w)))
+                : absmax8_bits(d[i]);
+  return __byte_perm(umax_halves(m[0]), umax_halves(m[1]), 0x5410);
 }
 // Whether pieces of rows need the second pass, by the largest of their gates' patterns and
-// of their gradients' magnitudes (in the halves of a word each): a gate below -64, or an
-// infinite gradient.
+// of their gradients' magnitudes (in the halves of a word each): a gate below -64, or a
+// gradient that is infinite or NaN.
 __device__ __forceinline__ uint32_t top_gate(const uint4& g) { return umax16x2(umax16x2(g.x, g.y), umax16x2(g.z, g.w)); }
 __device__ __forceinline__ bool swiglu_again(uint32_t gate, uint32_t top) {
   return (umax_halves(gate) & 0xFFFFu) > kFarGate || (umax_halves(top) & 0xFFFFu) >= 0x7F80u;
@@ -929,7 +942,7 @@ __device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, co
       uint4 in[3], d[2];
       at.load(p, inside && at.live(p, 0), in);
       swiglu_grad8(in, d);
-      if (!__any_sync(0xffffffffu, swiglu_again(top_gate(in[0]), swiglu_top(d)))) continue;
+      if (!__any_sync(0xffffffffu, swiglu_again(top_gate(in[0]), swiglu_top<true>(d)))) continue;
       uint2 w = swiglu_grad2_wide(in[0].x, in[1].x, in[2].x, d[0].x, d[1].x);
       d[0].x = w.x, d[1].x = w.y;
       w = swiglu_grad2_wide(in[0].y, in[1].y, in[2].y, d[0].y, d[1].y);
@@ -938,7 +951,7 @@ __device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, co
       d[0].z = w.x, d[1].z = w.y;
       w = swiglu_grad2_wide(in[0].w, in[1].w, in[2].w, d[0].w, d[1].w);
       d[0].w = w.x, d[1].w = w.y;
-      at.finish<kPow2, false>(p, divisors, d, swiglu_top(d), (c & 15) == 0, inside && at.row < p.M);
+      at.finish<kPow2, false>(p, divisors, d, swiglu_top<false>(d), (c & 15) == 0, inside && at.row < p.M);
     }
   }
 }
@@ -946,11 +959,11 @@ __device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, co
 // Thread = eight columns of one half of h: the columns stay, the rows advance by
 // the grid, with the next row's loads in flight.  A group of 128 is a half-warp's
 // 16 threads; whole warps go through the loop together.  Rows with a gate below -64
-// or an infinite gradient are written anew in a second pass, which rarely has any: the
+// or a gradient that is no finite number are written anew in a second pass, which rarely has any: the
 // loop keeps the largest patterns of all rows, two instructions a row, and looks at
 // them once.  [67712][2048] takes 167 us (1.12 GB, the copy bandwidth); with a vote a
 // row, that kept such rows from being stored, 174 to 187, with a call inside the loop,
-// whose results went through local memory, 190 to 228.  With absmax scales 201, bound by
+// whose results went through local memory, 190 to 228.  With absmax scales 205, bound by
 // instructions; by a ring of bulk copies 245, unpacked with expf 325.
 template <bool kPow2>
 __global__ void __launch_bounds__(kSbThreads, 2) swiglu_backward_kernel(const __grid_constant__ SwigluBackwardParams p) {
@@ -979,7 +992,7 @@ __global__ void __launch_bounds__(kSbThreads, 2) swiglu_backward_kernel(const __
       live_after = inside && at.live(p, 2 * p.step);
       uint4 d[2];
       swiglu_grad8(in, d);
-      const uint32_t top = swiglu_top(d);
+      const uint32_t top = swiglu_top<true>(d);
       gates = umax16x2(gates, top_gate(in[0]));
       tops = umax16x2(tops, top);
       at.finish<kPow2, true>(p, divisors, d, top, (c & 15) == 0, inside && at.row < p.M);
