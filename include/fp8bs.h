@@ -540,8 +540,16 @@ int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E);
 /* -------------------------------------------------------------- training
  * The operators of a training step around the 8-bit products.  Where one
  * quantises, it quantises the BF16 value that it would store: codes and scales
- * are bit for bit those of fp8bs_quantize_act_ex on that value.  Sums are taken
- * in float32 in a fixed order: the same inputs give the same bits.
+ * are bit for bit those of fp8bs_quantize_act_ex on that value, also where it is
+ * an infinity that finite inputs overflowed to: with power-of-two scales its code
+ * is E4M3's NaN, with absmax scales its whole group's.  Sums are taken in float32
+ * in a fixed order: the same inputs give the same bits.
+ *
+ * Infinities and NaN in the inputs are outside the contract here too: they leave
+ * the rest as it is and show in what they reach, but codes and scales may not be
+ * the quantiser's there.  A maximum passes over NaN, so that a NaN among zeros has
+ * code 0; an infinity of dout under a weight of zero, which is NaN, has NaN's code,
+ * where the quantiser has 0.
  */
 
 #define FP8BS_RMSNORM_MIN_EPS 7.8886090522101181e-31f /* 2^-100: squares that underflow do not count beside it */
