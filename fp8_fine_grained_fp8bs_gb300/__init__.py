@@ -929,7 +929,8 @@ def moe_combine_backward(dout, y, row_of, row_token, w, pow2: bool = False, bf16
     k = row_of.shape[1]
     dy = torch.empty((rows, N), dtype=torch.bfloat16, device=dout.device) if bf16 else None
     q, s = _codes(rows, N, dout.device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    # the library writes nothing where there are no columns: the sums over them are zeros
+    dw = (torch.empty if N else torch.zeros)((T, k), dtype=torch.float32, device=dout.device)
     fp8bs_moe_combine_backward(dout, T, N, _row_stride(dout), y, rows, row_of, row_token, w, k, dy, q, s, _scale_mode(pow2),
                                dw, stream)
     return q, s, dy, dw

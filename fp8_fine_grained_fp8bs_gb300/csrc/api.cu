@@ -640,7 +640,7 @@ int fp8bs_moe_combine_backward(const void* dout, int64_t T, int64_t N, int64_t l
                                const int32_t* row_of, const int32_t* row_token, const float* w, int k, void* dy,
                                uint8_t* q, float* s, int scale_mode, float* dw, void* stream) {
   if (T < 0 || N < 0 || ldo < N || rows < 0 || k < 1 || k > 64 || !scale_mode_ok(scale_mode)) return FP8BS_ERR_INVALID_ARG;
-  if ((q == nullptr) != (s == nullptr) || (dw != nullptr && rows > 0 && y == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if ((q == nullptr) != (s == nullptr) || (dw != nullptr && rows > 0 && N > 0 && y == nullptr)) return FP8BS_ERR_INVALID_ARG;
   if (N % 8 != 0 || (q != nullptr && N % 128 != 0)) return FP8BS_ERR_SHAPE;
   if (T > (int64_t(1) << 24) / k || rows > (int64_t(1) << 30) || N > (int64_t(1) << 24)) return FP8BS_ERR_SHAPE;
   if (N == 0 || (T == 0 && rows == 0)) return FP8BS_OK;

@@ -636,7 +636,8 @@ int fp8bs_swiglu_backward_quantize(const void* h, int64_t M, int64_t I, int64_t 
  * another records FP8BS_ERR_DEVICE_ARG and is passed over (dw 0).  Rows that
  * row_token gives to a token that does not name them are left as they are.
  * Rules: N % 8 == 0, with q N % 128 == 0; 1 <= k <= 64, T * k <= 2^24, rows <=
- * 2^30; dout, y, dy, q 16-byte aligned, ldo * 2 % 16 == 0, the others 4.
+ * 2^30; dout, y, dy, q 16-byte aligned, ldo * 2 % 16 == 0, the others 4.  N == 0
+ * writes nothing, dw neither.
  */
 int fp8bs_moe_combine_backward(const void* dout, int64_t T, int64_t N, int64_t ldo, const void* y, int64_t rows,
                                const int32_t* row_of, const int32_t* row_token, const float* w, int k, void* dy,

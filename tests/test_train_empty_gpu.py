@@ -1,0 +1,31 @@
+"""Matrices without columns: what the calls return is not memory that nothing wrote."""
+import pytest
+
+from _gpu import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def _dirty(torch, n):
+    """Memory full of ones' bits for the allocator to hand out again."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda:0") for _ in range(16)]
+    del held
+
+
+@pytest.mark.parametrize("slices", [False, True])
+def test_combine_gradient_without_columns(slices):
+    """The gate weights' gradient is a sum over no columns: zeros."""
+    torch, fp8bs = require_gpu()
+    T, k, rows = 37, 3, 128
+    row_of = torch.arange(T * k, dtype=torch.int32, device="cuda:0").view(T, k)
+    row_token = torch.full((rows,), -1, dtype=torch.int32, device="cuda:0")
+    row_token[:T * k] = torch.arange(T * k, device="cuda:0").div(k, rounding_mode="floor").int()
+    wide = 8 if slices else 0      # a slice of no columns has an address, an empty tensor has none
+    args = (torch.empty((T, wide), dtype=torch.bfloat16, device="cuda:0")[:, :0],
+            torch.empty((rows, wide), dtype=torch.bfloat16, device="cuda:0")[:, :0], row_of, row_token, torch.ones((T, k), device="cuda:0"))
+    _dirty(torch, 4 * T * k)
+    q, s, _, dw = fp8bs.moe_combine_backward(*args)
+    assert q.shape == (rows, 0) and s.shape == (0, rows) and dw.shape == (T, k) and not dw.any()
+    assert fp8bs.fp8bs_get_device_status() == 0
