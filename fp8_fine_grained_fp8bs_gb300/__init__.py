@@ -856,6 +856,8 @@ def rmsnorm_quantize(x, gain, residual=None, eps: float = 1e-6, pow2: bool = Fal
     rstd = torch.empty(M, dtype=torch.float32, device=x.device)
     fp8bs_rmsnorm_quantize(x, M, K, _row_stride(x), residual, K if residual is None else _row_stride(residual), gain, kind,
                            eps, r, y, q, s, _scale_mode(pow2), rstd, stream)
+    if K == 0:      # the library wrote nothing; the mean of no columns counts as zero
+        rstd.fill_(eps ** -0.5)
     return q, s, y, x if r is None else r, rstd
 
 

@@ -571,7 +571,8 @@ int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E);
  *   rstd     [M] float32 or NULL (the gradient reads it).              (out)
  * At least one of y and q.  Rules: K % 8 == 0, with q K % 128 == 0, K <= 16384;
  * 2^-100 <= eps <= 1e30; the sum of a row's squares has to stay in float32's
- * range.  x, residual, gain, r, y and q 16-byte aligned, s and rstd 4.
+ * range.  x, residual, gain, r, y and q 16-byte aligned, s and rstd 4.  K == 0 writes
+ * nothing, rstd neither.
  */
 int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
                            const void* gain, int gain_dtype, float eps, void* r, void* y, uint8_t* q, float* s,

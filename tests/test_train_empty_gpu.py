@@ -29,3 +29,15 @@ def test_combine_gradient_without_columns(slices):
     q, s, _, dw = fp8bs.moe_combine_backward(*args)
     assert q.shape == (rows, 0) and s.shape == (0, rows) and dw.shape == (T, k) and not dw.any()
     assert fp8bs.fp8bs_get_device_status() == 0
+
+
+def test_norm_without_columns():
+    """The rows' statistic is that of a mean of zero."""
+    torch, fp8bs = require_gpu()
+    M = 37
+    x, gain = torch.empty((M, 8), dtype=torch.bfloat16, device="cuda:0")[:, :0], torch.empty(0, device="cuda:0")
+    _dirty(torch, 4 * M)
+    q, s, y, r, rstd = fp8bs.rmsnorm_quantize(x, gain, eps=0.25, bf16=True)
+    assert q.shape == y.shape == r.shape == (M, 0) and s.shape == (0, M) and bool((rstd == 2.0).all())
+    dx, dgain = fp8bs.rmsnorm_backward(x, r, gain, rstd)
+    assert dx.shape == (M, 0) and dgain.shape == (0,)
