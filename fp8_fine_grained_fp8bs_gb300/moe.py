@@ -359,7 +359,7 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     group that are not zeros but all below 448 * 2^-127 have no scale that the products take (the device status
     reports it): scale the loss."""
     import torch
-    from . import (grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward,
+    from . import (_checked, _on_one_device, grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward,
                    moe_route_backward, requant_1x128_to_128x1, swiglu_backward_quantize)
     if experts.gate_up_t is None:
         raise ValueError("experts: quantised for serving only, without their transposed copies")
@@ -368,8 +368,10 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
         raise ValueError("dloss: the forward pass had no balance loss (alpha)")
     E, two_i, H = experts.gate_up[0].shape
     for name, out, shape in (("dw_gate_up", dw_gate_up, (E, two_i, H)), ("dw_down", dw_down, (E, H, two_i // 2))):
-        if out is not None and (tuple(out.shape) != shape or out.dtype != torch.float32 or not out.is_contiguous()):
-            raise ValueError(f"{name}: expected a contiguous float32 tensor {shape}")     # before either is added to
+        if out is not None:      # before either is added to
+            if tuple(_checked(out, name, (torch.float32,), 3).shape) != shape:
+                raise ValueError(f"{name}: shape {tuple(out.shape)}, expected {shape}")
+            _on_one_device(out)
     _check_weights("experts.gate_up_t", experts.gate_up_t, (E, H, two_i))
     _check_weights("experts.down_t", experts.down_t, (E, two_i // 2, H))
     offsets, row_token, row_of = saved.layout
