@@ -355,9 +355,10 @@ def moe_layer_fp8_backward(dout, saved: Fp8Saved, experts: Fp8Experts, dloss=Non
     """Gradients of moe_layer_fp8 from dout [T, H] bfloat16 (and dloss, one float32, of the balance loss):
     (dx [T, H] bfloat16, the gradient of the values that the layer's input codes stand for, ``dx_add`` added;
     dlogits; dw_gate_up [E, 2I, H] and dw_down [E, H, I] float32).  Weight gradients given are added to and
-    returned.  The experts are those of the forward pass, with their transposed copies.  Gradients of a 1x128
-    group that are not zeros but all below 448 * 2^-127 have no scale that the products take (the device status
-    reports it): scale the loss."""
+    returned.  The experts are those of the forward pass, with their transposed copies.  The products take
+    scales from 2^-127 up; the device status reports smaller ones.  Matrices whose 1x128 groups are zeros or reach
+    above 448 * 2^-111 have none, not in the weights' gradients either, whose 128x1 groups may hold a row's smallest
+    codes alone: scale the loss."""
     import torch
     from . import (_checked, _on_one_device, grouped_gemm, grouped_wgrad, moe_combine_backward, moe_dispatch_backward,
                    moe_route_backward, requant_1x128_to_128x1, swiglu_backward_quantize)
