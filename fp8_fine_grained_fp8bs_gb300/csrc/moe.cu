@@ -21,7 +21,8 @@
 //     idx[t][j] < 0 contributes nothing.
 //   * moe_dispatch_backward: out[t] = BF16(add[t] + sum_j d[idx[t][j]]), the
 //     gradient of the dispatch (each token's row copied to its k rows).
-// All are memory-bound copies: one warp per row, 16-byte accesses.
+// All are memory-bound copies with 16-byte accesses, a warp per row; few tokens of the
+// combine and of the dispatch's gradient are shared by several warps each.
 #include <cuda_bf16.h>
 
 #include <algorithm>
