@@ -81,9 +81,11 @@ constexpr int kSfRowsBytes = 512;
 // accumulators and the store); 4 x 32 x 72 + 8 x 32 x 216 or 4 x 32 x 88 +
 // 8 x 32 x 208 = 384 x 168, the CTA's allocation at launch.  The converter
 // of row-scaled B (eight B scales per lane and k-block) gets the larger
-// share: every spill is local-memory traffic through the same on-chip
-// memory that feeds the tensor core, and a late scale slot holds back the
-// operand loads.
+// share: a spill in its loop is local-memory traffic through the same
+// on-chip memory that feeds the tensor core, and a late scale slot holds back
+// the operand loads.  Some are left (bytes stored and reloaded, by ptxas, over all
+// roles): 16 and 136 dense with pairs, 8 and 48 in the paired weight gradients, none
+// in the grouped kernels.
 constexpr uint32_t kMxLaunchRegs = 168;
 // One staging box per epilogue warp: the accumulator is handed back before
 // the stores, so a store waiting for the previous box's copy delays no MMA;
@@ -723,10 +725,15 @@ cudaError_t launch_wgrad_pow2(const GemmArgs& a, int sm_count, cudaStream_t stre
   *tmap_failed = false;
   *reg_check_failed = false;
   // One CTA's 128x128 tiles, whose two accumulators hide the stores, where pairs would
-  // leave SMs idle and where few rows per expert leave the float32 stores to count (16
-  // experts [4096][7168] of 256 rows 298 us against 348 with pairs, of 1024 rows 575
-  // against 435).  The rows of a segment are known on the device only: K is their
-  // number with the padding.
+  // leave SMs idle and where few rows per expert leave the float32 stores to count: 16
+  // experts [4096][7168] of 256 rows 297 us against 349 with pairs, of 384 rows 340 against
+  // 355, of 512 rows 373 against 329; 12 experts [7168][2048] of 256 rows 124 against 133,
+  // of 384 rows 143 against 129 to 135.  In BF16 pairs win from 128 rows on (159 against
+  // 219).  Idle SMs: one expert [1024][2048] of 4096 rows 17 us against 21 with pairs,
+  // [2048][2048] of 512 rows 10.0 against 11.9 (of 4096 rows 26.6 against 21.9, which
+  // the rule gives away), [2560][2048], where it ends, of 4096 rows 35.9 against 31.7.
+  // The rows of a segment are known on the device only: K is their number with the
+  // padding.
   const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256) * a.num_groups;
   const bool few_rows = !a.out_bf16 && a.K <= int64_t{320} * a.num_groups;
   if (a.M <= 128 || a.N <= 128 || 2 * tiles < sm_count || few_rows)
