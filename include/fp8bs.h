@@ -612,8 +612,8 @@ int64_t fp8bs_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
  *         row of zeros, and h's and dv's row is not read.               (in)
  *   dh    [M][2I] BF16 or NULL: dgate, then dup.                       (out)
  *   q, s  [M][2I] E4M3 and [2I/128][M] float32, both or neither.       (out)
- * At least one of dh and q.  Rules: I % 128 == 0, ldh >= 2I, lddv >= I; 16-byte
- * rows and pointers (live and s: 4).
+ * At least one of dh and q; dh is not h or dv, which may be read again.  Rules:
+ * I % 128 == 0, ldh >= 2I, lddv >= I; 16-byte rows and pointers (live and s: 4).
  */
 int fp8bs_swiglu_backward_quantize(const void* h, int64_t M, int64_t I, int64_t ldh, const void* dv, int64_t lddv,
                                    const int32_t* live, void* dh, uint8_t* q, float* s, int scale_mode, void* stream);
