@@ -62,13 +62,14 @@ struct Divisors<true> {
 // exact product, which keeps the sign of a zero.  Groups whose scale or its
 // reciprocal is not a normal number, zeros among them, take the general way, and so
 // do maxima above 1.75 * 2^127: an infinity among the values has the code of no number
-// there, where a product with the conversion's saturation would make 448 of it
-// (kFinite: the caller knows of none).
-template <bool kPow2, bool kFinite = false>
+// there, where a product with the conversion's saturation would make 448 of it.  One
+// unsigned compare finds both ends.
+template <bool kPow2>
 __device__ __forceinline__ float quantise8(const uint4& v, uint32_t a16, const Divisors<kPow2>& divisors, uint2& codes) {
   if (kPow2) {
-    const uint32_t e = (a16 + 31u) >> 7;
-    if (kFinite ? e >= 9u : e - 9u <= 254u - 9u) {
+    const uint32_t a = a16 + 31u - (9u << 7);
+    if (a < (255u - 9u) << 7) {
+      const uint32_t e = (a >> 7) + 9u;
       const float y = __uint_as_float((262u - e) << 23);
       const float2 y2 = make_float2(y, y);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -104,8 +105,9 @@ template <bool kPow2>
 __device__ __forceinline__ float quantise8_times(const float2 (&a)[4], float w, uint32_t a16, const Divisors<kPow2>& divisors,
                                                  uint2& codes) {
   if (kPow2) {
-    const uint32_t e = (a16 + 31u) >> 7;
-    if (e - 32u <= 254u - 32u && fabsf(w) < kPlainWeight) {
+    const uint32_t b = a16 + 31u - (32u << 7);
+    if (b < (255u - 32u) << 7 && fabsf(w) < kPlainWeight) {
+      const uint32_t e = (b >> 7) + 32u;
       float2 f[4];
       widen8x2(times8(a, w * __uint_as_float((262u - e) << 23)), f);
       codes = make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y), e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
@@ -863,7 +865,7 @@ struct SwigluPlace {
   }
   // Quantises and stores the row's piece, `top` the halves' largest magnitudes in this
   // thread; whole warps come here together.
-  template <bool kPow2, bool kFinite>
+  template <bool kPow2>
   __device__ __forceinline__ void finish(const SwigluBackwardParams& p, const Divisors<kPow2>& divisors, const uint4 (&d)[2],
                                          uint32_t top, bool first_of_group, bool here) const {
     if (here && p.dh != nullptr) {
@@ -874,8 +876,8 @@ struct SwigluPlace {
 #pragma unroll
     for (int o = 1; o <= 8; o <<= 1) top = umax16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
     uint2 cg, cu;
-    const float sg = quantise8<kPow2, kFinite>(d[0], top & 0xFFFFu, divisors, cg);
-    const float su = quantise8<kPow2, kFinite>(d[1], top >> 16, divisors, cu);
+    const float sg = quantise8<kPow2>(d[0], top & 0xFFFFu, divisors, cg);
+    const float su = quantise8<kPow2>(d[1], top >> 16, divisors, cu);
     if (!here) return;
     *reinterpret_cast<uint2*>(p.q + out) = cg;
     *reinterpret_cast<uint2*>(p.q + out + p.I) = cu;
@@ -932,7 +934,7 @@ __device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, co
       d[0].z = w.x, d[1].z = w.y;
       w = swiglu_grad2_wide(in[0].w, in[1].w, in[2].w, d[0].w, d[1].w);
       d[0].w = w.x, d[1].w = w.y;
-      at.finish<kPow2, false>(p, divisors, d, swiglu_top<false>(d), (c & 15) == 0, inside && at.row < p.M);
+      at.finish<kPow2>(p, divisors, d, swiglu_top<false>(d), (c & 15) == 0, inside && at.row < p.M);
     }
   }
 }
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(kSbThreads, 2) swiglu_backward_kernel(const __
       const uint32_t top = swiglu_top<true>(d);
       gates = umax16x2(gates, top_gate(in[0]));
       tops = umax16x2(tops, top);
-      at.finish<kPow2, true>(p, divisors, d, top, (c & 15) == 0, inside && at.row < p.M);
+      at.finish<kPow2>(p, divisors, d, top, (c & 15) == 0, inside && at.row < p.M);
       at.move_on(p);
     }
   }
