@@ -944,7 +944,7 @@ __device__ __noinline__ void swiglu_rows_again(const SwigluBackwardParams& p, co
 // 16 threads; whole warps go through the loop together.  Rows with a gate below -64
 // or a gradient that is no finite number are written anew in a second pass, which rarely has any: the
 // loop keeps the largest patterns of all rows, two instructions a row, and looks at
-// them once.  [67712][2048] takes 167 us (1.12 GB, the copy bandwidth); with a vote a
+// them once.  [67712][2048] takes 167 us (1.12 GB, 0.99 of the copy bandwidth); with a vote a
 // row, that kept such rows from being stored, 174 to 187, with a call inside the loop,
 // whose results went through local memory, 190 to 228.  With absmax scales 205, bound by
 // instructions; by a ring of bulk copies 245, unpacked with expf 325.
