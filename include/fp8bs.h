@@ -570,8 +570,8 @@ int64_t fp8bs_moe_layout_workspace_bytes(int64_t T, int k, int E);
  *   q, s     [M][K] E4M3 and [K/128][M] float32, both or neither.      (out)
  *   rstd     [M] float32 or NULL (the gradient reads it).              (out)
  * At least one of y and q.  Rules: K % 8 == 0, with q K % 128 == 0, K <= 16384;
- * 2^-100 <= eps <= 1e30; the sum of a row's squares has to stay in float32's
- * range.  x, residual, gain, r, y and q 16-byte aligned, s and rstd 4.  K == 0 writes
+ * 2^-100 <= eps <= 1e30; the sum of a row's squares and each r * gain have to
+ * stay in float32's range.  x, residual, gain, r, y and q 16-byte aligned, s and rstd 4.  K == 0 writes
  * nothing, rstd neither.
  */
 int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
@@ -592,7 +592,8 @@ int fp8bs_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, con
  *         columns a row.  dgain [K] float32, or NULL.                  (out)
  *   ws    scratch of fp8bs_rmsnorm_backward_workspace_bytes(M, K) bytes, 16-byte
  *         aligned, with dgain; two calls at once need one each.
- * Rules as above, K % 8 == 0.  M == 0 gives a dgain of zeros.
+ * Rules as above, K % 8 == 0; dy * gain, dy * r and the sum of a row's t r have to
+ * stay in float32's range.  M == 0 gives a dgain of zeros.
  */
 int fp8bs_rmsnorm_backward(const void* dy, int64_t M, int64_t K, int64_t lddy, const void* r, int64_t ldr,
                            const void* gain, int gain_dtype, const float* rstd, const void* dres, int64_t lddres,
